@@ -73,7 +73,16 @@ typedef enum {
     CONV_ERR_STATIC_WORKSPACE_LIMIT = 17 /* call needs more scratch than CONV_STATIC_WORKSPACE_BYTES */
 } conv_status;
 
-typedef enum { CONV_INT8 = 1, CONV_INT32 = 2 } conv_dtype;
+/* The convolution entry points take CONV_INT8 and CONV_INT32; the float types
+ * belong to the channel operators (conv_linear, conv_layer_norm and their
+ * gradients). */
+typedef enum {
+    CONV_INT8 = 1,
+    CONV_INT32 = 2,
+    CONV_FLOAT32 = 3,
+    CONV_FLOAT16 = 4,
+    CONV_BFLOAT16 = 5
+} conv_dtype;
 
 typedef enum { CONV_CROSS_CORRELATION = 0, CONV_CONVOLUTION = 1 } conv_mode;
 
@@ -460,6 +469,170 @@ conv_status conv_measure_peak_rates(void *scratch, size_t scratch_bytes, conv_pe
 void conv_shutdown(void);
 conv_status conv_plan_cache_stats(uint64_t *plan_hits, uint64_t *plan_misses, uint64_t *launch_hits,
                                   uint64_t *launch_misses);
+
+/*
+ * Channel operators: what a network does between and after its convolutions
+ * on matrices whose rows are pixels or tokens and whose columns are channels
+ * (a channels-last image [N,H,W,C] is the matrix [N*H*W, C]).
+ *
+ * Matrix descriptor: rows x cols with one element stride each, like the
+ * tensor descriptors above.  Strides are positive and no two elements may
+ * share an address (a broadcast stride of 0 is refused); the stride of a dim
+ * of extent 1 is ignored.  Both orders and any padding are taken, rows or
+ * columns may be the contiguous dim.
+ */
+typedef struct {
+    int32_t dtype;     /* conv_dtype */
+    int32_t reserved;  /* must be 0 */
+    int64_t rows;
+    int64_t cols;
+    int64_t row_stride; /* elements from one row to the next */
+    int64_t col_stride; /* elements from one column to the next */
+    uint64_t capacity_bytes;
+} conv_matrix_desc;
+
+/* Activations of conv_linear:
+ *   CONV_ACT_RELU       max(0, z)
+ *   CONV_ACT_GELU       z * Phi(z), Phi the standard normal distribution
+ *   CONV_ACT_GELU_TANH  z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3)))
+ *   CONV_ACT_SILU       z / (1 + exp(-z)) */
+typedef enum {
+    CONV_ACT_NONE = 0,
+    CONV_ACT_RELU = 1,
+    CONV_ACT_GELU = 2,
+    CONV_ACT_GELU_TANH = 3,
+    CONV_ACT_SILU = 4
+} conv_activation;
+
+typedef struct {
+    int32_t activation;  /* conv_activation */
+    int32_t bias_dtype;  /* type of the bias (of its gradient, in conv_linear_grad): CONV_FLOAT32 or x's type;
+                            ignored without one */
+    int32_t reserved[2]; /* must be 0 */
+} conv_linear_params;
+
+/*
+ * Matrix product with bias, activation and residual:
+ *   z[m,n] = sum_k x[m,k] * w[n,k] + bias[n]
+ *   y[m,n] = act(z[m,n]) + residual[m,n],   preact[m,n] = z[m,n]
+ * x [M,K] and w [N,K] are both CONV_FLOAT16 or both CONV_BFLOAT16; y [M,N]
+ * is of x's type or CONV_FLOAT32, residual [M,N] of y's type, preact [M,N]
+ * of x's type.  Products are exact and summed in 32 bits; bias, activation
+ * and residual are applied to the 32-bit sum, and y and preact are each
+ * rounded once (to nearest even; f16 overflows to infinity).
+ * bias_dev, residual (with residual_dev) and preact (with preact_dev) may be
+ * NULL: none.  residual may be the same matrix as y (same address and
+ * strides, then y is updated in place); any other overlap of an output with
+ * an input, the other output or the workspace is refused.
+ * M = 0 or N = 0 does nothing; K = 0 gives act(bias) + residual.
+ *
+ * Workspace: conv_linear_workspace_size bytes, 256-byte aligned (may be NULL
+ * when that is 0).  It holds a packed copy of each of x and w that the
+ * tensor-memory accelerator cannot read in place: unless one of the
+ * strides is 1, the other one a multiple of 8 elements and the address
+ * 16-byte aligned.  x_dev and w_dev of the size query are the addresses the
+ * call will use (read only for their alignment; NULL counts as aligned).
+ * Asynchronous on `stream`; nothing is allocated and nothing synchronises.
+ * Results are the same from run to run: no sum's order depends on timing.
+ *
+ * Errors: CONV_ERR_NULL_PTR; CONV_ERR_DTYPE; CONV_ERR_BAD_PARAM (negative
+ * extent, unknown activation, reserved fields not 0); CONV_ERR_SHAPE_MISMATCH;
+ * CONV_ERR_BAD_STRIDES; CONV_ERR_BUFFER_TOO_SMALL; CONV_ERR_ALIGNMENT (an
+ * address that is not a multiple of its element's size); CONV_ERR_TOO_LARGE
+ * (an extent of 2^31 - 256 or more); CONV_ERR_OVERLAP; CONV_ERR_WORKSPACE;
+ * CONV_ERR_CUDA; CONV_ERR_UNSUPPORTED_DEVICE.  A refused call launches
+ * nothing.
+ */
+conv_status conv_linear_workspace_size(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w,
+                                       const void *w_dev, size_t *bytes);
+
+conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w, const void *w_dev,
+                        const void *bias_dev, const conv_matrix_desc *residual, const void *residual_dev,
+                        const conv_matrix_desc *preact, void *preact_dev, const conv_matrix_desc *y, void *y_dev,
+                        const conv_linear_params *p, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of conv_linear for the loss gradient dy [M,N] (of x's type):
+ *   dz = dy * act'(preact)     (dz = dy for CONV_ACT_NONE)
+ *   dx = dz w,  dw = dz^T x,  dbias = sum over the rows of dz
+ * preact [M,N] is the pre-activation conv_linear wrote; it is required with
+ * an activation and not read without one.  The residual's gradient is dy
+ * itself.  dx [M,K] and dw [N,K] are of x's type or CONV_FLOAT32, dbias [N]
+ * of p->bias_dtype.  Each of dx (with dx_dev), dw (with dw_dev) and
+ * dbias_dev may be NULL: not computed; at least one is wanted.  With an
+ * activation dz is rounded once to x's type before the products (as a
+ * stored gradient would be); dbias sums it unrounded, in 32 bits.
+ * ReLU's slope at 0 is 0.  M = 0 gives dw = 0 and dbias = 0; N = 0 gives
+ * dx = 0.
+ *
+ * The workspace (conv_linear_grad_workspace_size bytes, 256-byte aligned)
+ * holds dz where it is not dy itself, the partial sums of dbias and packed
+ * copies as for conv_linear; the size query takes the same descriptors and
+ * addresses as the call.  Errors, asynchrony and repeatability as for
+ * conv_linear.
+ */
+conv_status conv_linear_grad_workspace_size(const conv_matrix_desc *dy, const void *dy_dev,
+                                            const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w,
+                                            const void *w_dev, const conv_linear_params *p, size_t *bytes);
+
+conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_matrix_desc *x,
+                             const void *x_dev, const conv_matrix_desc *w, const void *w_dev,
+                             const conv_matrix_desc *preact, const void *preact_dev, const conv_matrix_desc *dx,
+                             void *dx_dev, const conv_matrix_desc *dw, void *dw_dev, void *dbias_dev,
+                             const conv_linear_params *p, void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    float eps;           /* > 0, finite: added to the variance */
+    float scale;         /* finite, not 0: x is taken as scale * x (1 for float inputs as they are) */
+    int32_t param_dtype; /* type of gain and shift (and of their gradients): CONV_FLOAT32, or y's type (dx's) */
+    int32_t reserved;    /* must be 0 */
+} conv_layer_norm_params;
+
+/*
+ * Layer norm of every row of x [M,C]: with v = scale * x,
+ *   mean = sum v / C,  var = sum (v - mean)^2 / C,  rstd = 1 / sqrt(var + eps)
+ *   y = (v - mean) * rstd * gain + shift
+ * x is CONV_FLOAT32, CONV_FLOAT16, CONV_BFLOAT16 or CONV_INT32: conv_fprop's
+ * channels-last accumulators are normalised as they are, `scale` being the
+ * step of the quantised product (integers above 2^24 are rounded to 32-bit
+ * floats).  y [M,C] is CONV_FLOAT32, CONV_FLOAT16 or CONV_BFLOAT16.
+ * gain_dev and shift_dev hold C values of param_dtype and may be NULL (1 and
+ * 0); mean_dev and rstd_dev receive M 32-bit floats and may be NULL.
+ * All arithmetic is in 32 bits, the variance from the differences to the
+ * mean; y is rounded once.  y may be the same matrix as x when the types
+ * have one size (same address and strides).  No workspace.  M = 0 does
+ * nothing; C must be at least 1.  A row with an infinity or a NaN gives NaN
+ * in that row alone.
+ * Errors as for conv_linear (CONV_ERR_BAD_PARAM also for eps and scale).
+ */
+conv_status conv_layer_norm(const conv_matrix_desc *x, const void *x_dev, const void *gain_dev,
+                            const void *shift_dev, const conv_matrix_desc *y, void *y_dev, float *mean_dev,
+                            float *rstd_dev, const conv_layer_norm_params *p, void *stream);
+
+/*
+ * Gradients of conv_layer_norm (float x, scale 1) for the loss gradient
+ * dy [M,C] (of x's type), with the mean and rstd that the forward call wrote:
+ *   n = (x - mean) * rstd,  t = dy * gain
+ *   dx = rstd * (t - sum t / C - n * sum (t n) / C) + residual_grad
+ *   dgain = sum over the rows of dy * n,  dshift = sum over the rows of dy
+ * residual_grad [M,C] (of x's type; NULL: none) is the gradient that reaches
+ * x past the norm, through a residual connection.  dx [M,C] is of x's type.
+ * dx (with dx_dev), dgain_dev and dshift_dev may each be NULL: not computed;
+ * at least one is wanted.  dx may be the same matrix as residual_grad.
+ * Sums run in 32 bits in an order that does not depend on timing.  M = 0
+ * gives dgain = dshift = 0.  The workspace
+ * (conv_layer_norm_grad_workspace_size bytes, 256-byte aligned) holds
+ * partial sums of dgain and dshift.  Errors as for conv_layer_norm;
+ * CONV_ERR_DTYPE for an integer x.
+ */
+conv_status conv_layer_norm_grad_workspace_size(const conv_matrix_desc *x, size_t *bytes);
+
+conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_matrix_desc *x,
+                                 const void *x_dev, const void *gain_dev, const float *mean_dev,
+                                 const float *rstd_dev, const conv_matrix_desc *residual_grad,
+                                 const void *residual_grad_dev, const conv_matrix_desc *dx, void *dx_dev,
+                                 void *dgain_dev, void *dshift_dev, const conv_layer_norm_params *p, void *workspace,
+                                 size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a status. */
 const char *conv_status_string(conv_status s);

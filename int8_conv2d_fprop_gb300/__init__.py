@@ -13,12 +13,22 @@ compute_data_type (INT32 only); ``padding`` is the symmetric overload.
 Tensors are described by logical dims [N,C,H,W] / [K,C,R,S] plus per-dim
 element strides, exactly what a torch tensor's ``size()``/``stride()`` give
 (a channels_last tensor is NHWC in memory).
+
+The channel operators that follow a convolution (matrix product with bias,
+activation and residual, layer norm, and their gradients) are in
+``channel.py`` and re-exported here.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
+
+from . import channel
+from .channel import (  # noqa: F401
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ACTIVATIONS, CONV_BFLOAT16, CONV_FLOAT16, CONV_FLOAT32,
+    LayerNormParams, LinearParams, MatrixDesc, conv_layer_norm, conv_layer_norm_grad, conv_linear, conv_linear_grad,
+)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libint8conv.so")
@@ -52,7 +62,7 @@ EXPORTED_SYMBOLS = (
     "conv_selftest_wait_timeout", "conv_status_string", "conv_library_version",
     "conv_dgrad_workspace_size", "conv_dgrad", "conv_wgrad_workspace_size", "conv_wgrad",
     "conv_measure_peak_rates", "conv_shutdown", "conv_plan_cache_stats",
-)
+) + channel.CHANNEL_SYMBOLS
 
 
 class PeakRates(ctypes.Structure):
@@ -196,6 +206,7 @@ def lib():
                      "conv_fprop_prepacked", "conv_fprop_static_workspace", "conv_device_status",
                      "conv_selftest_wait_timeout"):
             getattr(L, name).restype = ctypes.c_int
+        channel.declare(L)
         _lib = L
     return _lib
 

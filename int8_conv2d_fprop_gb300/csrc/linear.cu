@@ -1,0 +1,388 @@
+// linear.cu -- conv_linear and conv_linear_grad: argument checks, workspace
+// layout, the packed copies of operands the product cannot read in place,
+// and dz with the bias gradient.
+#include <cuda_runtime.h>
+
+#include "channel.h"
+#include "channel_math.cuh"
+
+namespace i8c {
+namespace {
+
+// ---------------------------------------------------------------- packing
+// Row-contiguous copy of a [rows, cols] matrix of 16-bit elements, rows
+// `ld` elements apart (a multiple of 8; the padding is never read).
+// 32 x 32 tiles through shared memory, so that both a row-contiguous and a
+// column-contiguous source are read in runs.
+__global__ void __launch_bounds__(256) pack_matrix_kernel(const uint16_t *src, int64_t rs, int64_t cs, int64_t rows,
+                                                          int64_t cols, uint16_t *dst, int64_t ld,
+                                                          int64_t col_tiles, bool by_rows) {
+    __shared__ uint16_t tile[32][33];
+    const int64_t r0 = (int64_t)blockIdx.x / col_tiles * 32, c0 = (int64_t)blockIdx.x % col_tiles * 32;
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        const int r = by_rows ? y + i : x, c = by_rows ? x : y + i;
+        if (r0 + r < rows && c0 + c < cols) tile[r][c] = src[(r0 + r) * rs + (c0 + c) * cs];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if (r0 + y + i < rows && c0 + x < cols) dst[(r0 + y + i) * ld + c0 + x] = tile[y + i][x];
+}
+
+conv_status pack_matrix(const MatRef &m, int64_t rows, int64_t cols, void *dst, int64_t ld, cudaStream_t s) {
+    const int64_t rt = (rows + 31) / 32, ct = (cols + 31) / 32;
+    if (rt * ct > INT32_MAX) return CONV_ERR_TOO_LARGE;
+    // lanes along the smaller stride (a dim of extent 1 has none)
+    const bool by_rows = rows == 1 || (cols > 1 && m.cs <= m.rs);
+    pack_matrix_kernel<<<(unsigned)(rt * ct), 256, 0, s>>>((const uint16_t *)m.p, m.rs, m.cs, rows, cols,
+                                                           (uint16_t *)dst, ld, ct, by_rows);
+    return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+}
+
+struct Packed {  // a packed copy in the workspace, or none
+    size_t off = 0, bytes = 0;
+    int64_t ld = 0;
+};
+
+void plan_pack(const conv_matrix_desc *d, const void *p, size_t *total, Packed *k) {
+    *k = Packed();
+    if (d->rows == 0 || d->cols == 0 || product_in_place(p, d->rows, d->row_stride, d->cols, d->col_stride)) return;
+    k->ld = round_up(d->cols, 8);
+    k->off = *total;
+    k->bytes = (size_t)round_up(d->rows * k->ld * 2, 256);
+    *total += k->bytes;
+}
+
+// Operand as the product reads it: in place, or its packed copy (made here).
+conv_status operand(const conv_matrix_desc *d, const void *p, const Packed &k, void *workspace, cudaStream_t s,
+                    MatRef *m) {
+    *m = mat_ref(d, p);
+    if (!k.bytes) return CONV_OK;
+    void *dst = (char *)workspace + k.off;
+    conv_status st = pack_matrix(*m, d->rows, d->cols, dst, k.ld, s);
+    m->p = dst;
+    m->rs = d->rows > 1 ? k.ld : 0;
+    m->cs = d->cols > 1 ? 1 : 0;
+    return st;
+}
+
+conv_status check_linear_params(const conv_linear_params *p, const conv_matrix_desc *x, bool has_bias) {
+    if (!p) return CONV_ERR_NULL_PTR;
+    if (p->activation < CONV_ACT_NONE || p->activation > CONV_ACT_SILU) return CONV_ERR_BAD_PARAM;
+    if (p->reserved[0] != 0 || p->reserved[1] != 0) return CONV_ERR_BAD_PARAM;
+    if (has_bias && p->bias_dtype != CONV_FLOAT32 && p->bias_dtype != x->dtype) return CONV_ERR_DTYPE;
+    return CONV_OK;
+}
+
+conv_status check_operands(const conv_matrix_desc *x, const conv_matrix_desc *w) {
+    conv_status st;
+    if ((st = check_matrix(x)) || (st = check_matrix(w))) return st;
+    if (!is_half_type(x->dtype) || w->dtype != x->dtype) return CONV_ERR_DTYPE;
+    if (x->cols != w->cols) return CONV_ERR_SHAPE_MISMATCH;
+    return CONV_OK;
+}
+
+conv_status check_like(const conv_matrix_desc *d, const void *p, int64_t rows, int64_t cols) {
+    conv_status st = check_matrix(d);
+    if (st) return st;
+    if (d->rows != rows || d->cols != cols) return CONV_ERR_SHAPE_MISMATCH;
+    return check_address(d, p);
+}
+
+conv_status check_vector(const void *p, int64_t n, int32_t dtype, const conv_matrix_desc *out, const void *out_dev) {
+    if (!p || n == 0) return CONV_OK;
+    if ((uintptr_t)p % (uintptr_t)channel_elem_size(dtype)) return CONV_ERR_ALIGNMENT;
+    if (out && overlaps(p, (uint64_t)(n * channel_elem_size(dtype)), out_dev, matrix_extent_bytes(out)))
+        return CONV_ERR_OVERLAP;
+    return CONV_OK;
+}
+
+conv_status check_workspace(const void *workspace, size_t have, size_t need) {
+    if (need == 0) return CONV_OK;
+    if (!workspace || have < need || (uintptr_t)workspace % 256) return CONV_ERR_WORKSPACE;
+    return CONV_OK;
+}
+
+struct LinearPlan {
+    Packed x, w;
+    size_t bytes = 0;
+};
+
+LinearPlan plan_linear(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w, const void *w_dev) {
+    LinearPlan pl;
+    plan_pack(x, x_dev, &pl.bytes, &pl.x);
+    plan_pack(w, w_dev, &pl.bytes, &pl.w);
+    return pl;
+}
+
+// ---------------------------------------------------------------- dz
+// dz = dy * act'(preact) in 16 bits, and the column sums of the unrounded dz
+// over this block's rows.  32 x 8 threads: 32 columns, 8 rows at a time.
+template <int kAct>
+__global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
+                                                        int64_t rows_per_block, void *dz, int64_t dz_ld,
+                                                        float *part) {
+    __shared__ float red[8][32];
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * 32 + x;
+    const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
+    const int64_t r1 = r0 + rows_per_block < rows ? r0 + rows_per_block : rows;
+    float sum = 0.0f;
+    if (c < cols)
+        for (int64_t r = r0 + y; r < r1; r += 8) {
+            float v = load_as_float(dy.p, r * dy.rs + c * dy.cs, dy.dtype);
+            if constexpr (kAct != CONV_ACT_NONE)
+                v *= activation_slope<kAct>(load_as_float(pre.p, r * pre.rs + c * pre.cs, pre.dtype));
+            if (dz) store_from_float(dz, r * dz_ld + c, dy.dtype, v);
+            sum += v;
+        }
+    if (!part) return;
+    red[y][x] = sum;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+        for (int i = 1; i < 8; ++i) sum += red[i][x];
+        part[(int64_t)blockIdx.y * cols + c] = sum;
+    }
+}
+
+__global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int64_t parts, int64_t cols, void *out,
+                                                         int32_t dtype) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    float sum = 0.0f;
+    for (int64_t i = 0; i < parts; ++i) sum += part[i * cols + c];
+    store_from_float(out, c, dtype, sum);
+}
+
+struct GradPlan {
+    bool dz = false;  // dz is made in the workspace
+    size_t dz_off = 0, part_off = 0;
+    int64_t dz_ld = 0, parts = 0, rows_per_part = 0;
+    Packed x, w;
+    size_t bytes = 0;
+};
+
+GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_matrix_desc *x, const void *x_dev,
+                   const conv_matrix_desc *w, const void *w_dev, const conv_linear_params *p) {
+    GradPlan pl;
+    const int64_t m = dy->rows, n = dy->cols;
+    if (m > 0 && n > 0) {
+        pl.dz = p->activation != CONV_ACT_NONE ||
+                !product_in_place(dy_dev, m, dy->row_stride, n, dy->col_stride);
+        if (pl.dz) {
+            pl.dz_ld = round_up(n, 8);
+            pl.dz_off = pl.bytes;
+            pl.bytes += (size_t)round_up(m * pl.dz_ld * 2, 256);
+        }
+        pl.rows_per_part = round_up((m + 255) / 256, 8);
+        pl.parts = (m + pl.rows_per_part - 1) / pl.rows_per_part;
+        pl.part_off = pl.bytes;
+        pl.bytes += (size_t)round_up(pl.parts * n * 4, 256);
+    }
+    plan_pack(x, x_dev, &pl.bytes, &pl.x);
+    plan_pack(w, w_dev, &pl.bytes, &pl.w);
+    return pl;
+}
+
+template <int kAct>
+void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, bool sums,
+               cudaStream_t s) {
+    const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pl.parts);
+    linear_dz_kernel<kAct><<<grid, 256, 0, s>>>(dy, pre, m, n, pl.rows_per_part,
+                                                pl.dz ? (char *)ws + pl.dz_off : nullptr, pl.dz_ld,
+                                                sums ? (float *)((char *)ws + pl.part_off) : nullptr);
+}
+
+conv_status make_dz(const GradPlan &pl, int32_t act, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n,
+                    void *ws, void *dbias, int32_t bias_dtype, cudaStream_t s) {
+    switch (act) {
+        case CONV_ACT_RELU: launch_dz<CONV_ACT_RELU>(pl, dy, pre, m, n, ws, dbias, s); break;
+        case CONV_ACT_GELU: launch_dz<CONV_ACT_GELU>(pl, dy, pre, m, n, ws, dbias, s); break;
+        case CONV_ACT_GELU_TANH: launch_dz<CONV_ACT_GELU_TANH>(pl, dy, pre, m, n, ws, dbias, s); break;
+        case CONV_ACT_SILU: launch_dz<CONV_ACT_SILU>(pl, dy, pre, m, n, ws, dbias, s); break;
+        default: launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, s); break;
+    }
+    if (dbias)
+        column_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>((const float *)((char *)ws + pl.part_off),
+                                                                      pl.parts, n, dbias, bias_dtype);
+    return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace i8c
+
+using namespace i8c;
+
+extern "C" {
+
+conv_status conv_linear_workspace_size(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w,
+                                       const void *w_dev, size_t *bytes) {
+    if (!x || !w || !bytes) return CONV_ERR_NULL_PTR;
+    conv_status st = check_operands(x, w);
+    if (st) return st;
+    *bytes = plan_linear(x, x_dev, w, w_dev).bytes;
+    return CONV_OK;
+}
+
+conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w, const void *w_dev,
+                        const void *bias_dev, const conv_matrix_desc *residual, const void *residual_dev,
+                        const conv_matrix_desc *preact, void *preact_dev, const conv_matrix_desc *y, void *y_dev,
+                        const conv_linear_params *p, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !w || !y || !p) return CONV_ERR_NULL_PTR;
+    conv_status st;
+    if ((st = check_operands(x, w)) || (st = check_linear_params(p, x, bias_dev != nullptr))) return st;
+    const int64_t m = x->rows, n = w->rows, k = x->cols;
+    if ((st = check_like(y, y_dev, m, n))) return st;
+    if (y->dtype != x->dtype && y->dtype != CONV_FLOAT32) return CONV_ERR_DTYPE;
+    if ((st = check_address(x, x_dev)) || (st = check_address(w, w_dev))) return st;
+    if (residual) {
+        if ((st = check_like(residual, residual_dev, m, n))) return st;
+        if (residual->dtype != y->dtype) return CONV_ERR_DTYPE;
+    }
+    if (preact) {
+        if ((st = check_like(preact, preact_dev, m, n))) return st;
+        if (preact->dtype != x->dtype) return CONV_ERR_DTYPE;
+    }
+    if ((st = check_vector(bias_dev, n, p->bias_dtype, y, y_dev))) return st;
+    if (preact && (st = check_vector(bias_dev, n, p->bias_dtype, preact, preact_dev))) return st;
+    if (m == 0 || n == 0) return CONV_OK;
+    if (matrices_overlap(y, y_dev, x, x_dev) || matrices_overlap(y, y_dev, w, w_dev) ||
+        (residual && !same_matrix(y, y_dev, residual, residual_dev) &&
+         matrices_overlap(y, y_dev, residual, residual_dev)) ||
+        (preact && (matrices_overlap(preact, preact_dev, x, x_dev) || matrices_overlap(preact, preact_dev, w, w_dev) ||
+                    matrices_overlap(preact, preact_dev, y, y_dev) ||
+                    (residual && matrices_overlap(preact, preact_dev, residual, residual_dev)))))
+        return CONV_ERR_OVERLAP;
+    const LinearPlan pl = plan_linear(x, x_dev, w, w_dev);
+    if ((st = check_workspace(workspace, workspace_bytes, pl.bytes))) return st;
+    if (pl.bytes) {
+        const conv_matrix_desc *d[] = {x, w, y, residual, preact};
+        const void *a[] = {x_dev, w_dev, y_dev, residual_dev, preact_dev};
+        for (int i = 0; i < 5; ++i)
+            if (d[i] && overlaps(workspace, pl.bytes, a[i], matrix_extent_bytes(d[i]))) return CONV_ERR_OVERLAP;
+        if (bias_dev && overlaps(workspace, pl.bytes, bias_dev, (uint64_t)(n * channel_elem_size(p->bias_dtype))))
+            return CONV_ERR_OVERLAP;
+    }
+    if ((st = check_device())) return st;
+    MatRef xr, wr;
+    if ((st = operand(x, x_dev, pl.x, workspace, (cudaStream_t)stream, &xr))) return st;
+    if ((st = operand(w, w_dev, pl.w, workspace, (cudaStream_t)stream, &wr))) return st;
+    Product pr;
+    pr.ma = m, pr.nb = n, pr.k = k;
+    pr.a = {xr.p, xr.rs, xr.cs};
+    pr.b = {wr.p, wr.rs, wr.cs};
+    pr.in_dtype = x->dtype;
+    const MatRef yr = mat_ref(y, y_dev), rr = mat_ref(residual, residual_dev), zr = mat_ref(preact, preact_dev);
+    pr.d = y_dev, pr.d_sa = yr.rs, pr.d_sb = yr.cs, pr.d_dtype = y->dtype;
+    pr.res = residual ? residual_dev : nullptr, pr.res_sa = rr.rs, pr.res_sb = rr.cs;
+    pr.pre = preact ? preact_dev : nullptr, pr.pre_sa = zr.rs, pr.pre_sb = zr.cs;
+    pr.bias = bias_dev, pr.bias_dtype = p->bias_dtype;
+    pr.act = p->activation;
+    return product_launch(pr, stream);
+}
+
+conv_status conv_linear_grad_workspace_size(const conv_matrix_desc *dy, const void *dy_dev,
+                                            const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w,
+                                            const void *w_dev, const conv_linear_params *p, size_t *bytes) {
+    if (!dy || !x || !w || !p || !bytes) return CONV_ERR_NULL_PTR;
+    conv_status st;
+    if ((st = check_operands(x, w)) || (st = check_linear_params(p, x, false)) || (st = check_matrix(dy))) return st;
+    if (dy->dtype != x->dtype) return CONV_ERR_DTYPE;
+    if (dy->rows != x->rows || dy->cols != w->rows) return CONV_ERR_SHAPE_MISMATCH;
+    *bytes = plan_grad(dy, dy_dev, x, x_dev, w, w_dev, p).bytes;
+    return CONV_OK;
+}
+
+conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_matrix_desc *x,
+                             const void *x_dev, const conv_matrix_desc *w, const void *w_dev,
+                             const conv_matrix_desc *preact, const void *preact_dev, const conv_matrix_desc *dx,
+                             void *dx_dev, const conv_matrix_desc *dw, void *dw_dev, void *dbias_dev,
+                             const conv_linear_params *p, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dy || !x || !w || !p || (!dx && !dw && !dbias_dev)) return CONV_ERR_NULL_PTR;
+    conv_status st;
+    if ((st = check_operands(x, w)) || (st = check_linear_params(p, x, dbias_dev != nullptr))) return st;
+    const int64_t m = x->rows, n = w->rows, k = x->cols;
+    if ((st = check_like(dy, dy_dev, m, n))) return st;
+    if (dy->dtype != x->dtype) return CONV_ERR_DTYPE;
+    if ((st = check_address(x, x_dev)) || (st = check_address(w, w_dev))) return st;
+    if (p->activation == CONV_ACT_NONE) preact = nullptr;
+    else if (!preact) return CONV_ERR_NULL_PTR;
+    if (preact) {
+        if ((st = check_like(preact, preact_dev, m, n))) return st;
+        if (preact->dtype != x->dtype) return CONV_ERR_DTYPE;
+    }
+    if (dx) {
+        if ((st = check_like(dx, dx_dev, m, k))) return st;
+        if (dx->dtype != x->dtype && dx->dtype != CONV_FLOAT32) return CONV_ERR_DTYPE;
+    }
+    if (dw) {
+        if ((st = check_like(dw, dw_dev, n, k))) return st;
+        if (dw->dtype != x->dtype && dw->dtype != CONV_FLOAT32) return CONV_ERR_DTYPE;
+    }
+    const conv_matrix_desc *in[] = {dy, x, w, preact};
+    const void *in_dev[] = {dy_dev, x_dev, w_dev, preact_dev};
+    for (int i = 0; i < 4; ++i) {
+        if (!in[i]) continue;
+        if (dx && matrices_overlap(dx, dx_dev, in[i], in_dev[i])) return CONV_ERR_OVERLAP;
+        if (dw && matrices_overlap(dw, dw_dev, in[i], in_dev[i])) return CONV_ERR_OVERLAP;
+        if ((st = check_vector(dbias_dev, n, p->bias_dtype, in[i], in_dev[i]))) return st;
+    }
+    if (dx && dw && matrices_overlap(dx, dx_dev, dw, dw_dev)) return CONV_ERR_OVERLAP;
+    if (dx && (st = check_vector(dbias_dev, n, p->bias_dtype, dx, dx_dev))) return st;
+    if (dw && (st = check_vector(dbias_dev, n, p->bias_dtype, dw, dw_dev))) return st;
+    const GradPlan pl = plan_grad(dy, dy_dev, x, x_dev, w, w_dev, p);
+    if ((st = check_workspace(workspace, workspace_bytes, pl.bytes))) return st;
+    if (pl.bytes) {
+        const conv_matrix_desc *d[] = {dy, x, w, preact, dx, dw};
+        const void *a[] = {dy_dev, x_dev, w_dev, preact_dev, dx_dev, dw_dev};
+        for (int i = 0; i < 6; ++i)
+            if (d[i] && overlaps(workspace, pl.bytes, a[i], matrix_extent_bytes(d[i]))) return CONV_ERR_OVERLAP;
+        if (dbias_dev && overlaps(workspace, pl.bytes, dbias_dev, (uint64_t)(n * channel_elem_size(p->bias_dtype))))
+            return CONV_ERR_OVERLAP;
+    }
+    if ((st = check_device())) return st;
+    const cudaStream_t s = (cudaStream_t)stream;
+    MatRef dz = mat_ref(dy, dy_dev);
+    if (m > 0 && n > 0 && (pl.dz || dbias_dev)) {
+        if ((st = make_dz(pl, p->activation, dz, mat_ref(preact, preact_dev), m, n, workspace, dbias_dev,
+                          p->bias_dtype, s)))
+            return st;
+        if (pl.dz) {
+            dz.p = (char *)workspace + pl.dz_off;
+            dz.rs = m > 1 ? pl.dz_ld : 0;
+            dz.cs = n > 1 ? 1 : 0;
+        }
+    } else if (m == 0 && n > 0 && dbias_dev) {
+        if (cudaMemsetAsync(dbias_dev, 0, (size_t)(n * channel_elem_size(p->bias_dtype)), s) != cudaSuccess)
+            return CONV_ERR_CUDA;
+    }
+    if (dx && m > 0 && k > 0) {
+        MatRef wr;
+        if ((st = operand(w, w_dev, pl.w, workspace, s, &wr))) return st;
+        Product pr;
+        pr.ma = m, pr.nb = k, pr.k = n;
+        pr.a = {dz.p, dz.rs, dz.cs};
+        pr.b = {wr.p, wr.cs, wr.rs};
+        pr.in_dtype = x->dtype;
+        const MatRef o = mat_ref(dx, dx_dev);
+        pr.d = dx_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dx->dtype;
+        if ((st = product_launch(pr, stream))) return st;
+    }
+    if (dw && n > 0 && k > 0) {
+        MatRef xr;
+        if ((st = operand(x, x_dev, pl.x, workspace, s, &xr))) return st;
+        Product pr;
+        pr.ma = n, pr.nb = k, pr.k = m;
+        pr.a = {dz.p, dz.cs, dz.rs};
+        pr.b = {xr.p, xr.cs, xr.rs};
+        pr.in_dtype = x->dtype;
+        const MatRef o = mat_ref(dw, dw_dev);
+        pr.d = dw_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dw->dtype;
+        if ((st = product_launch(pr, stream))) return st;
+    }
+    return CONV_OK;
+}
+
+}  // extern "C"
