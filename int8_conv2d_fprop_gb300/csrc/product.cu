@@ -1,9 +1,23 @@
 // product.cu -- D[a,b] = epilogue(sum_k A[a,k] * B[b,k]) for 16-bit float
-// operands with any strides.
+// operands, on the 5th-generation tensor cores.
+//
+// One warp loads 64-element k-steps of both operands with TMA (128-byte
+// swizzle) into a ring, one thread issues tcgen05.mma into one of two
+// accumulators in tensor memory, and eight warps take the other accumulator
+// through bias, pre-activation, activation and residual to the output.
+// Either operand may have k or its own dim contiguous: only the tensor map,
+// the descriptor strides and the instruction's transpose bits differ, so the
+// forward product and both gradients are one kernel.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "channel.h"
 #include "channel_math.cuh"
+#include "tc_ptx.cuh"
 
 namespace i8c {
 
@@ -16,64 +30,821 @@ bool product_in_place(const void *p, int64_t rows, int64_t rs, int64_t cols, int
 
 namespace {
 
-constexpr int T = 64, KT = 16;
+constexpr int kTileA = 128;        // accumulator lanes of one CTA
+constexpr int kStepK = 64;         // k elements per ring stage: one 128-byte row
+constexpr int kMaxTileB = 256;     // columns of one accumulator
+constexpr int kMaxStages = 12;
+constexpr int kThreads = 384;      // 4 control warps, 8 epilogue warps
+constexpr int kEpilogueWarps = 8;
+constexpr int kStagingBytes = kEpilogueWarps * 4096;
+constexpr int kBiasBytes = kEpilogueWarps * 128;
+constexpr int kMaxSplit = 8;       // portable cluster size
 
-// 64 x 64 outputs per block, 4 x 4 per thread, both operands staged as
-// floats in shared memory.
-template <int kAct>
-__global__ void __launch_bounds__(256) product_simple_kernel(Product pr) {
-    __shared__ float sa[KT][T + 1], sb[KT][T + 1];
-    const int64_t a0 = (int64_t)blockIdx.x * T, b0 = (int64_t)blockIdx.y * T;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < pr.k; k0 += KT) {
-        for (int i = threadIdx.x; i < T * KT; i += 256) {
-            const int kk = i % KT, r = i / KT;
-            const bool kin = k0 + kk < pr.k;
-            sa[kk][r] = (kin && a0 + r < pr.ma)
-                            ? load_as_float(pr.a.p, (a0 + r) * pr.a.s_mn + (k0 + kk) * pr.a.s_k, pr.in_dtype) : 0.0f;
-            sb[kk][r] = (kin && b0 + r < pr.nb)
-                            ? load_as_float(pr.b.p, (b0 + r) * pr.b.s_mn + (k0 + kk) * pr.b.s_k, pr.in_dtype) : 0.0f;
+// How an output, residual or pre-activation matrix is walked.
+enum Walk : int32_t {
+    kWalkNone = 0,
+    kWalkRows,    // b contiguous, 16-byte aligned rows: vectors, TMA stores
+    kWalkAlongB,  // lanes along b
+    kWalkAlongA,  // lanes along a
+};
+
+struct Side {
+    void *p;
+    int64_t sa, sb;
+    int32_t dtype;
+    int32_t walk;
+};
+
+struct ProductArgs {
+    CUtensorMap map_a, map_b, map_d, map_pre;
+    Side d, res, pre;
+    const void *bias;
+    int32_t bias_dtype, bias_along_a;
+    int32_t act;
+    int32_t ma, nb;
+    int32_t k_steps;
+    int32_t tile_b;              // NT, a multiple of 32
+    int32_t tiles_a, tiles_b;
+    int32_t a_mn, b_mn;          // operand's own dim (not k) contiguous
+    int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
+    int32_t stages, stage_bytes; // A is the first 16 KB of a stage
+    int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
+    uint32_t idesc;
+    uint64_t wait_limit_ns;
+    int *status;
+};
+
+struct SharedCtl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The address of this CTA's shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 2-D load whose completion is counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                    uint32_t accumulate) {
+    if constexpr (kPair) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        ptx::mma_f16_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
+    }
+}
+
+// Arrives on `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    if constexpr (kPair) {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                bar),
+            "h"((uint16_t)3)
+            : "memory");
+    } else {
+        ptx::mma_commit(bar);
+    }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+                     "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(dst), "r"(cols) : "memory");
+    } else {
+        ptx::tmem_alloc(dst, cols);
+        ptx::tmem_relinquish();
+    }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        ptx::tmem_dealloc(addr, cols);
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  k contiguous: rows of
+// 64 k elements, 8-row atoms 1024 bytes apart (the leading offset is unused).
+// Own dim contiguous: rows of 64 own elements, one per k; 8-k atoms 1024
+// bytes apart, the next 64 own elements one box (64 rows) further.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFF) >> 4);
+    d |= (uint64_t)(mn ? (kStepK * 128) >> 4 : 1) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Bounded wait; false when the CTA is giving up (the status word then holds
+// the timeout).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag, uint64_t limit_ns,
+                                       int *status) {
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::global_timer_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicExch(status, (int)CONV_ERR_DEVICE_TIMEOUT);
+            return false;
         }
-        __syncthreads();
-        for (int kk = 0; kk < KT; ++kk)
+    }
+}
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag,
+                                           uint64_t limit_ns, int *status) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, abort_flag, limit_ns, status);
+}
+
+struct Ring {
+    uint32_t idx = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t depth) {
+        if (++idx == depth) {
+            idx = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Tile t of the walk over the output: bands of 8 tiles along a, so that the
+// tiles in flight share operand rows in L2.
+__device__ __forceinline__ void tile_at(const ProductArgs &a, int t, int *ia, int *ib) {
+    constexpr int kBand = 8;
+    const int per_band = kBand * a.tiles_b;
+    const int band = t / per_band, in = t - band * per_band;
+    const int rows = min(kBand, a.tiles_a - band * kBand);
+    *ib = in / rows;
+    *ia = band * kBand + (in - *ib * rows);
+}
+
+// ---------------------------------------------------------------- epilogue
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int32_t dtype) {
+    if (dtype == CONV_FLOAT16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void unpack2(uint32_t w, int32_t dtype, float *lo, float *hi) {
+    if (dtype == CONV_FLOAT16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        *lo = f.x, *hi = f.y;
+    } else {
+        *lo = __uint_as_float(w << 16);
+        *hi = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+template <int kAct, int W>
+__device__ __forceinline__ void activate_all(float (&v)[W]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = activate<kAct>(v[j]);
+}
+
+template <int W>
+__device__ __forceinline__ void activate_runtime(float (&v)[W], int32_t act) {
+    switch (act) {
+        case CONV_ACT_RELU: activate_all<CONV_ACT_RELU>(v); break;
+        case CONV_ACT_GELU: activate_all<CONV_ACT_GELU>(v); break;
+        case CONV_ACT_GELU_TANH: activate_all<CONV_ACT_GELU_TANH>(v); break;
+        case CONV_ACT_SILU: activate_all<CONV_ACT_SILU>(v); break;
+        default: break;
+    }
+}
+
+// One warp's 32 rows x W columns at (row0, b0), lane = row, v = the row's
+// sums.  `stage` is the warp's 4 KB staging buffer, `half` the half of it
+// that the next 16-bit store uses.
+struct WarpTile {
+    int32_t row0, b0, rows, cols;  // rows, cols: how many are inside the matrix
+    uint32_t stage;
+    uint32_t half;
+    bool one_store;  // a 32-bit tile takes the whole buffer: one store in flight
+    int lane;
+};
+
+// Own row of a side matrix, W = 32: through the staging buffer when lanes
+// have to run along b.
+__device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, float (&r)[32]) {
+    const int64_t row = t.row0 + t.lane;
+    if (s.walk == kWalkAlongA) {
+        const bool in = t.lane < t.rows;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            r[j] = in && j < t.cols ? load_as_float(s.p, row * s.sa + (int64_t)(t.b0 + j) * s.sb, s.dtype) : 0.0f;
+        return;
+    }
+    // the buffer's earlier stores have to be read out first
+    if (t.lane == 0) ptx::bulk_wait_group_read<0>();
+    __syncwarp();
+    if (s.walk == kWalkRows && t.cols == 32) {
+        const bool wide = s.dtype == CONV_FLOAT32;
+        const int vecs = wide ? 8 : 4, per = wide ? 4 : 8;  // 16-byte vectors per row, elements per vector
+        const int c = t.lane & (vecs - 1);
+        uint4 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int rr = (t.lane + 32 * i) / vecs;
+            if (i < vecs && rr < t.rows)
+                q[i] = *reinterpret_cast<const uint4 *>((const char *)s.p + ((t.row0 + rr) * s.sa + t.b0 + c * per) *
+                                                                               (wide ? 4 : 2));
+            else
+                q[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int rr = (t.lane + 32 * i) / vecs;
+            if (i < vecs)
+                ptx::st_shared_v4(t.stage + (wide ? rr * 128 + ((c ^ (rr & 7)) << 4)
+                                                  : rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)), q[i]);
+        }
+        __syncwarp();
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 w = ptx::ld_shared_v4(t.stage + t.lane * 128 + ((i ^ (t.lane & 7)) << 4));
+                r[4 * i] = __uint_as_float(w.x), r[4 * i + 1] = __uint_as_float(w.y);
+                r[4 * i + 2] = __uint_as_float(w.z), r[4 * i + 3] = __uint_as_float(w.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = ptx::ld_shared_v4(t.stage + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4));
+                unpack2(w.x, s.dtype, &r[8 * i], &r[8 * i + 1]);
+                unpack2(w.y, s.dtype, &r[8 * i + 2], &r[8 * i + 3]);
+                unpack2(w.z, s.dtype, &r[8 * i + 4], &r[8 * i + 5]);
+                unpack2(w.w, s.dtype, &r[8 * i + 6], &r[8 * i + 7]);
+            }
+        }
+        __syncwarp();
+        return;
+    }
+    for (int rr = 0; rr < t.rows; ++rr)
+        if (t.lane < t.cols)
+            ptx::st_shared_b32(t.stage + (rr * 32 + (t.lane ^ rr)) * 4,
+                               __float_as_uint(load_as_float(s.p, (int64_t)(t.row0 + rr) * s.sa +
+                                                                      (int64_t)(t.b0 + t.lane) * s.sb, s.dtype)));
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        r[j] = t.lane < t.rows && j < t.cols
+                   ? __uint_as_float(ptx::ld_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4)) : 0.0f;
+    __syncwarp();
+}
+
+__device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *map, WarpTile &t, const float (&v)[32]) {
+    const int64_t row = t.row0 + t.lane;
+    if (s.walk == kWalkAlongA) {
+        if (t.lane < t.rows) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < t.cols) store_from_float(s.p, row * s.sa + (int64_t)(t.b0 + j) * s.sb, s.dtype, v[j]);
+        }
+        return;
+    }
+    if (s.walk == kWalkRows) {
+        // staged in the map's swizzle and stored by TMA, which clips to the
+        // matrix; 16-bit tiles alternate between the halves of the buffer
+        const bool wide = s.dtype == CONV_FLOAT32;
+        uint32_t buf = t.stage;
+        if (wide) {
+            if (t.lane == 0) ptx::bulk_wait_group_read<0>();
+        } else {
+            buf += t.half * 2048;
+            t.half ^= 1u;
+            if (t.lane == 0) {
+                if (t.one_store) ptx::bulk_wait_group_read<0>();
+                else ptx::bulk_wait_group_read<1>();
+            }
+        }
+        __syncwarp();
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                ptx::st_shared_v4(buf + t.lane * 128 + ((i ^ (t.lane & 7)) << 4),
+                                  make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+        } else {
+#pragma unroll
             for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[kk][ty + 16 * i] * sb[kk][tx + 16 * j];
+                ptx::st_shared_v4(buf + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4),
+                                  make_uint4(pack2(v[8 * i], v[8 * i + 1], s.dtype), pack2(v[8 * i + 2], v[8 * i + 3], s.dtype),
+                                             pack2(v[8 * i + 4], v[8 * i + 5], s.dtype), pack2(v[8 * i + 6], v[8 * i + 7], s.dtype)));
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (t.lane == 0) {
+            ptx::tma_store_2d(map, t.b0, t.row0, buf);
+            ptx::bulk_commit_group();
+        }
+        return;
+    }
+    if (t.lane == 0) ptx::bulk_wait_group_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) ptx::st_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4, __float_as_uint(v[j]));
+    __syncwarp();
+    if (t.lane < t.cols)
+        for (int rr = 0; rr < t.rows; ++rr)
+            store_from_float(s.p, (int64_t)(t.row0 + rr) * s.sa + (int64_t)(t.b0 + t.lane) * s.sb, s.dtype,
+                             __uint_as_float(ptx::ld_shared_b32(t.stage + (rr * 32 + (t.lane ^ rr)) * 4)));
+    __syncwarp();
+}
+
+// The same for 8 columns of a split tile: every lane on its own row.
+__device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, float (&r)[8]) {
+    const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)t.b0 * s.sb;
+    const bool in = t.lane < t.rows;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = in && j < t.cols ? load_as_float(s.p, at + j * s.sb, s.dtype) : 0.0f;
+}
+
+__device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *, WarpTile &t, const float (&v)[8]) {
+    if (t.lane >= t.rows) return;
+    const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)t.b0 * s.sb;
+    if (s.walk == kWalkRows && t.cols == 8) {
+        if (s.dtype == CONV_FLOAT32) {
+            float4 *p = reinterpret_cast<float4 *>((float *)s.p + at);
+            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+            p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>((uint16_t *)s.p + at) =
+                make_uint4(pack2(v[0], v[1], s.dtype), pack2(v[2], v[3], s.dtype), pack2(v[4], v[5], s.dtype),
+                           pack2(v[6], v[7], s.dtype));
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < t.cols) store_from_float(s.p, at + j * s.sb, s.dtype, v[j]);
+}
+
+template <int W>
+__device__ __forceinline__ void finish_tile(const ProductArgs &a, WarpTile &t, uint32_t bias_smem, float (&v)[W]) {
+    if (a.bias) {
+        if (a.bias_along_a) {
+            const float b = t.lane < t.rows ? load_as_float(a.bias, t.row0 + t.lane, a.bias_dtype) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[j] += b;
+        } else {
+            // lane j's bias to every row, through 128 bytes of shared memory
+            __syncwarp();
+            ptx::st_shared_b32(bias_smem + t.lane * 4,
+                               __float_as_uint(t.lane < t.cols ? load_as_float(a.bias, t.b0 + t.lane, a.bias_dtype) : 0.0f));
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < W; j += 4) {
+                const uint4 b = ptx::ld_shared_v4(bias_smem + j * 4);
+                v[j] += __uint_as_float(b.x), v[j + 1] += __uint_as_float(b.y);
+                v[j + 2] += __uint_as_float(b.z), v[j + 3] += __uint_as_float(b.w);
+            }
+        }
+    }
+    if (a.pre.walk) store_side(a.pre, &a.map_pre, t, v);
+    activate_runtime(v, a.act);
+    if (a.res.walk) {
+        float r[W];
+        load_side(a.res, t, r);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += r[j];
+    }
+    store_side(a.d, &a.map_d, t, v);
+}
+
+// ---------------------------------------------------------------- kernel
+// kPair: two CTAs of a cluster work on one tile of 256 x tile_b
+// (cta_group::2: each holds its 128 rows of A and half the rows of B, the
+// first one issues the MMAs for both).  Otherwise one CTA per tile of
+// 128 x tile_b, or `split` CTAs of a cluster that each sum part of k and
+// then add their partial tiles through distributed shared memory, in order
+// of rank.
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t ring = ptx::smem_addr(smem);
+    const uint32_t staging = ring + a.stages * a.stage_bytes;
+    const uint32_t bias_smem = staging + kStagingBytes;
+    SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + a.stages * a.stage_bytes + kStagingBytes + kBiasBytes);
+    volatile int32_t *abort_flag = &ctl->abort_flag;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = (kPair || a.split > 1) ? cluster_rank() : 0;
+    const int cluster_size = kPair ? 2 : a.split;
+    const int first = blockIdx.x / cluster_size, step = gridDim.x / cluster_size;
+    const int tiles = a.tiles_a * a.tiles_b;
+    constexpr int kRowsPerTile = kPair ? 2 * kTileA : kTileA;
+    int k_lo = 0, k_hi = a.k_steps;
+    if (!kPair && a.split > 1) {
+        k_lo = (int)((int64_t)a.k_steps * rank / a.split);
+        k_hi = (int)((int64_t)a.k_steps * (rank + 1) / a.split);
+    }
+
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&a.map_a);
+        ptx::prefetch_tensormap(&a.map_b);
+        for (int i = 0; i < a.stages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->acc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->acc_empty[i]), kPair ? 2 * kEpilogueWarps : kEpilogueWarps);
+        }
+        ctl->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 2) tmem_alloc<kPair>(ptx::smem_addr(&ctl->tmem_base), 512);
+    ptx::tc_fence_before();
+    if (kPair || a.split > 1) cluster_sync(); else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&ctl->tmem_base;
+    // nothing above reads or writes global memory
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ loads
+        Ring rg;
+        int64_t issued = 0;
+        bool ok = true;
+        const uint32_t bytes = (kPair ? 2u : 1u) * (16384u + (a.b_mn ? a.b_boxes * 8192u : a.b_rows * 128u));
+        for (int t = first; t < tiles && ok; t += step) {
+            int ia, ib;
+            tile_at(a, t, &ia, &ib);
+            const int a0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0);
+            const int b0 = ib * a.tile_b + (kPair ? rank * a.b_rows : 0);
+            for (int ks = k_lo; ks < k_hi; ++ks) {
+                if (!wait_phase(ptx::smem_addr(&ctl->empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]);
+                if (!kPair || rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                if (kPair) bar = map_to_rank(bar, 0);
+                const uint32_t sa = ring + rg.idx * a.stage_bytes, sb = sa + 16384;
+                const int k0 = ks * kStepK;
+                auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
+                    if constexpr (kPair) tma_load_2d_pair(dst, m, x, y, bar);
+                    else ptx::tma_load_2d(dst, m, x, y, bar);
+                };
+                if (a.a_mn) {
+                    load(sa, &a.map_a, a0, k0);
+                    load(sa + 8192, &a.map_a, a0 + 64, k0);
+                } else {
+                    load(sa, &a.map_a, k0, a0);
+                }
+                if (a.b_mn) {
+                    for (int i = 0; i < a.b_boxes; ++i) load(sb + i * 8192, &a.map_b, b0 + 64 * i, k0);
+                } else {
+                    load(sb, &a.map_b, k0, b0);
+                }
+                ++issued;
+                rg.next(a.stages);
+            }
+        }
+        // Every stage is released by the MMAs that read it; the releases
+        // reach both CTAs of a pair, so they have to be in before either
+        // leaves.  After a time-out the copies have to land first (in a pair
+        // on the leader's barriers; the cluster barrier below keeps both
+        // CTAs), and no release may come.
+        const bool drain_copies = *abort_flag && (!kPair || rank == 0);
+        for (int s = 0; s < a.stages; ++s) {
+            const int64_t n = issued / a.stages + (s < issued % a.stages ? 1 : 0);
+            if (n == 0) continue;
+            const uint32_t bar = ptx::smem_addr(drain_copies ? &ctl->full[s] : &ctl->empty[s]);
+            const uint64_t t0 = ptx::global_timer_ns();
+            while (!ptx::mbar_try_wait(bar, (uint32_t)((n - 1) & 1)))
+                if (ptx::global_timer_ns() - t0 > 10000000) break;
+        }
+    } else if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
+        // ------------------------------------------------ MMA
+        Ring rg;
+        int n = 0;
+        bool ok = true;
+        const uint32_t adv_a = a.a_mn ? 2048 >> 4 : 32 >> 4, adv_b = a.b_mn ? 2048 >> 4 : 32 >> 4;
+        for (int t = first; t < tiles && ok; t += step, ++n) {
+            const int slot = n & 1;
+            if (!wait_phase(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status)) break;
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + slot * kMaxTileB;
+            for (int ks = k_lo; ks < k_hi; ++ks) {
+                if (!wait_phase(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t sa = ring + rg.idx * a.stage_bytes;
+                const uint64_t da = operand_desc(sa, a.a_mn), db = operand_desc(sa + 16384, a.b_mn);
+#pragma unroll
+                for (int i = 0; i < kStepK / 16; ++i)
+                    mma<kPair>(d, da + i * adv_a, db + i * adv_b, a.idesc, (ks > k_lo || i > 0) ? 1u : 0u);
+                mma_commit<kPair>(ptx::smem_addr(&ctl->empty[rg.idx]));
+                rg.next(a.stages);
+            }
+            if (ok) mma_commit<kPair>(ptx::smem_addr(&ctl->acc_full[slot]));
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ epilogue
+        const int e = warp - 4, quad = warp & 3, part = e >> 2;
+        WarpTile wt;
+        wt.lane = lane;
+        wt.stage = staging + e * 4096;
+        wt.half = 0;
+        wt.one_store = a.d.dtype == CONV_FLOAT32;
+        const uint32_t my_bias = bias_smem + e * 128;
+        int n = 0;
+        for (int t = first; t < tiles; t += step, ++n) {
+            int ia, ib;
+            tile_at(a, t, &ia, &ib);
+            const int slot = n & 1;
+            if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) break;
+            ptx::tc_fence_after();
+            const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
+            const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
+            const bool none = k_lo == k_hi;  // no products: the accumulator was never written
+            wt.row0 = row0;
+            wt.rows = min(32, a.ma - row0);
+            if (!kPair && a.split > 1) {
+                // partial sums to shared memory [column][row], over the
+                // ring: its loads and MMAs are done
+                for (int c = part * 32; c < a.tile_b; c += 64) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(acc + c, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        ptx::st_shared_b32(ring + ((c + j) * kTileA + quad * 32 + lane) * 4, none ? 0u : v[j]);
+                }
+                break;  // one tile per cluster; the rest follows the cluster barrier
+            }
+            for (int c = part * 32; c < a.tile_b; c += 64) {
+                uint32_t u[32];
+                ptx::tmem_ld_32x32b_x32(acc + c, u);
+                ptx::tmem_ld_wait();
+                wt.b0 = ib * a.tile_b + c;
+                wt.cols = min(32, a.nb - wt.b0);
+                if (wt.rows <= 0 || wt.cols <= 0) continue;
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = none ? 0.0f : __uint_as_float(u[j]);
+                finish_tile<32>(a, wt, my_bias, v);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
+                if (kPair) mbar_arrive_cluster(map_to_rank(bar, 0));
+                else ptx::mbar_arrive(bar);
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+    }
+
+    __syncwarp();
+    if (!kPair && a.split > 1) {
+        cluster_sync();
+        if (warp >= 4 && !*abort_flag) {
+            // units of 32 rows x 8 columns, dealt to the cluster's warps
+            int ia, ib;
+            tile_at(a, first, &ia, &ib);
+            const int e = warp - 4;
+            WarpTile wt;
+            wt.lane = lane;
+            wt.stage = 0;
+            wt.half = 0;
+            wt.one_store = false;
+            const int units = a.tile_b / 8 * 4;
+            for (int u = e * a.split + (int)rank; u < units; u += kEpilogueWarps * a.split) {
+                const int quad = u & 3, c = (u >> 2) * 8;
+                wt.row0 = ia * kTileA + quad * 32;
+                wt.rows = min(32, a.ma - wt.row0);
+                wt.b0 = ib * a.tile_b + c;
+                wt.cols = min(8, a.nb - wt.b0);
+                if (wt.rows <= 0 || wt.cols <= 0) continue;
+                float v[8] = {};
+                for (int r = 0; r < a.split; ++r) {
+                    const uint32_t src = map_to_rank(ring + (c * kTileA + quad * 32 + lane) * 4, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += ld_cluster_f32(src + j * kTileA * 4);
+                }
+                finish_tile<8>(a, wt, bias_smem + e * 128, v);
+            }
+        }
+        cluster_sync();  // peers read this CTA's shared memory until here
+    } else if (kPair) {
+        cluster_sync();
+    } else {
         __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t a = a0 + ty + 16 * i, b = b0 + tx + 16 * j;
-            if (a >= pr.ma || b >= pr.nb) continue;
-            float z = acc[i][j];
-            if (pr.bias) z += load_as_float(pr.bias, pr.bias_along_a ? a : b, pr.bias_dtype);
-            if (pr.pre) store_from_float(pr.pre, a * pr.pre_sa + b * pr.pre_sb, pr.in_dtype, z);
-            float v = activate<kAct>(z);
-            if (pr.res) v += load_as_float(pr.res, a * pr.res_sa + b * pr.res_sb, pr.d_dtype);
-            store_from_float(pr.d, a * pr.d_sa + b * pr.d_sb, pr.d_dtype, v);
-        }
+    ptx::tc_fence_after();
+    if (warp == 2) tmem_dealloc<kPair>(tmem, 512);
 }
 
-template <int kAct>
-conv_status launch(const Product &pr, cudaStream_t s) {
-    const dim3 grid((unsigned)((pr.ma + T - 1) / T), (unsigned)((pr.nb + T - 1) / T));
-    if (grid.y > 65535) return CONV_ERR_TOO_LARGE;
-    product_simple_kernel<kAct><<<grid, 256, 0, s>>>(pr);
-    return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+// ---------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 tiled_encoder() {
+    static std::atomic<void *> fn{nullptr};
+    if (!fn.load()) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn.load());
 }
+
+// Map of a [outer, inner] matrix with `inner` contiguous.
+bool encode(CUtensorMap *m, int32_t dtype, const void *p, int64_t inner, int64_t outer, int64_t stride, int box_inner,
+            int box_outer, CUtensorMapSwizzle swizzle) {
+    auto enc = tiled_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType t = dtype == CONV_FLOAT32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : dtype == CONV_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int64_t size = channel_elem_size(dtype);
+    // (one row: any legal stride will do)
+    if (outer == 1) stride = round_up(inner * size, 16) / size;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)(stride * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer}, ones[2] = {1, 1};
+    return enc(m, t, 2, const_cast<void *>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// TMA strides are below 2^40 bytes.
+bool map_stride_ok(int64_t stride_elems, int64_t size) { return stride_elems * size < ((int64_t)1 << 40); }
+
+Side make_side(const void *p, int64_t sa, int64_t sb, int32_t dtype, int64_t ma, int64_t nb) {
+    Side s{const_cast<void *>(p), sa, sb, dtype, kWalkNone};
+    if (!p) return s;
+    const int64_t size = channel_elem_size(dtype);
+    // (TMA stores clip to the matrix in units of 16 bytes: rows of other
+    // lengths would be written past their end)
+    if ((sb == 1 || nb == 1) && (nb * size) % 16 == 0 && (sa * size) % 16 == 0 && (uintptr_t)p % 16 == 0 && map_stride_ok(sa, size))
+        s.walk = kWalkRows;
+    else if (nb > 1 && (ma == 1 || sb <= sa))
+        s.walk = kWalkAlongB;
+    else
+        s.walk = kWalkAlongA;
+    return s;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-conv_status product_launch(const Product &pr, void *stream) {
-    if (pr.ma == 0 || pr.nb == 0) return CONV_OK;
-    const cudaStream_t s = (cudaStream_t)stream;
-    switch (pr.act) {
-        case CONV_ACT_RELU: return launch<CONV_ACT_RELU>(pr, s);
-        case CONV_ACT_GELU: return launch<CONV_ACT_GELU>(pr, s);
-        case CONV_ACT_GELU_TANH: return launch<CONV_ACT_GELU_TANH>(pr, s);
-        case CONV_ACT_SILU: return launch<CONV_ACT_SILU>(pr, s);
-        default: return launch<CONV_ACT_NONE>(pr, s);
+conv_status product_launch(const Product &given, void *stream) {
+    if (given.ma == 0 || given.nb == 0) return CONV_OK;
+    Product pr = given;
+    const int sms = device_sm_count();
+    // Few rows: the long dim becomes the tile's 128 lanes and the few rows its
+    // columns, so that no lanes idle and every CTA streams its own weights.
+    if (pr.ma < pr.nb && pr.ma <= 128) {
+        std::swap(pr.ma, pr.nb);
+        std::swap(pr.a, pr.b);
+        std::swap(pr.d_sa, pr.d_sb);
+        std::swap(pr.res_sa, pr.res_sb);
+        std::swap(pr.pre_sa, pr.pre_sb);
+        pr.bias_along_a = !pr.bias_along_a;
     }
+    ProductArgs a;
+    a.ma = (int32_t)pr.ma, a.nb = (int32_t)pr.nb;
+    a.k_steps = (int32_t)cdiv(pr.k, kStepK);
+    a.d = make_side(pr.d, pr.d_sa, pr.d_sb, pr.d_dtype, pr.ma, pr.nb);
+    a.res = make_side(pr.res, pr.res_sa, pr.res_sb, pr.d_dtype, pr.ma, pr.nb);
+    a.pre = make_side(pr.pre, pr.pre_sa, pr.pre_sb, pr.in_dtype, pr.ma, pr.nb);
+    a.bias = pr.bias, a.bias_dtype = pr.bias_dtype, a.bias_along_a = pr.bias_along_a;
+    a.act = pr.act;
+    a.wait_limit_ns = wait_limit_ns();
+    a.status = device_status_word();
+    if (!a.status) return CONV_ERR_CUDA;
+
+    // k contiguous, or else the operand's own dim
+    a.a_mn = !(pr.a.s_k == 1 || pr.k <= 1) || (pr.a.s_mn == 1 && pr.k <= 1);
+    a.b_mn = !(pr.b.s_k == 1 || pr.k <= 1) || (pr.b.s_mn == 1 && pr.k <= 1);
+
+    // Tile shape: pairs of 256 x 256 where there are enough of them to fill
+    // the GPU, else single CTAs with narrower tiles, split along k while
+    // that brings more SMs in.
+    const int64_t pair_tiles = cdiv(pr.ma, 256) * cdiv(pr.nb, 256);
+    const bool pair = pair_tiles * 2 >= sms && pr.nb > 128;
+    int grid, cluster;
+    a.split = 1;
+    if (pair) {
+        a.tile_b = 256;
+        a.tiles_a = (int32_t)cdiv(pr.ma, 256);
+        a.tiles_b = (int32_t)cdiv(pr.nb, a.tile_b);
+        a.b_rows = a.tile_b / 2;
+        cluster = 2;
+        grid = 2 * (int)std::min<int64_t>((int64_t)a.tiles_a * a.tiles_b, sms / 2);
+    } else {
+        a.tile_b = (int32_t)std::min<int64_t>(round_up(pr.nb, 32), 256);
+        while (a.tile_b > 64 && cdiv(pr.ma, kTileA) * cdiv(pr.nb, a.tile_b) * 2 <= sms) a.tile_b = (int32_t)round_up(a.tile_b / 2, 32);
+        a.tiles_a = (int32_t)cdiv(pr.ma, kTileA);
+        a.tiles_b = (int32_t)cdiv(pr.nb, a.tile_b);
+        a.b_rows = a.tile_b;
+        const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b;
+        while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps >= a.split * 4) a.split *= 2;
+        cluster = a.split;
+        grid = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
+    }
+    a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
+    a.stage_bytes = 16384 + (int32_t)round_up(a.b_mn ? a.b_boxes * 8192 : a.b_rows * 128, 1024);
+    a.stages = std::min(kMaxStages, 196608 / a.stage_bytes);
+    const int tile_a = pair ? 256 : 128;
+    a.idesc = (1u << 4) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 7) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 10) |
+              ((a.a_mn ? 1u : 0u) << 15) | ((a.b_mn ? 1u : 0u) << 16) | ((uint32_t)(a.tile_b >> 3) << 17) |
+              ((uint32_t)(tile_a >> 4) << 24);
+
+    if (a.k_steps > 0) {
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        const bool ok_a = a.a_mn ? encode(&a.map_a, pr.in_dtype, pr.a.p, pr.ma, pr.k, pr.a.s_k, 64, kStepK, sw)
+                                 : encode(&a.map_a, pr.in_dtype, pr.a.p, pr.k, pr.ma, pr.a.s_mn, kStepK, kTileA, sw);
+        const bool ok_b = a.b_mn ? encode(&a.map_b, pr.in_dtype, pr.b.p, pr.nb, pr.k, pr.b.s_k, 64, kStepK, sw)
+                                 : encode(&a.map_b, pr.in_dtype, pr.b.p, pr.k, pr.nb, pr.b.s_mn, kStepK, a.b_rows, sw);
+        if (!ok_a || !ok_b) return CONV_ERR_CUDA;
+    }
+    for (auto [s, m] : {std::pair<Side *, CUtensorMap *>{&a.d, &a.map_d}, {&a.pre, &a.map_pre}})
+        if (s->walk == kWalkRows &&
+            !encode(m, s->dtype, s->p, pr.nb, pr.ma, s->sa, 32, 32,
+                    s->dtype == CONV_FLOAT32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return CONV_ERR_CUDA;
+
+    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kStagingBytes + kBiasBytes + sizeof(SharedCtl);
+    auto kernel = pair ? product_kernel<true> : product_kernel<false>;
+    static std::atomic<bool> ready[64][2];  // (check_device admits 64 devices)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CONV_ERR_CUDA;
+    if (!ready[dev][pair].load()) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess)
+            return CONV_ERR_CUDA;
+        ready[dev][pair].store(true);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return CONV_ERR_CUDA;
+    return CONV_OK;
 }
 
 }  // namespace i8c

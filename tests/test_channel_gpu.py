@@ -123,7 +123,7 @@ LAYOUTS = ("rows", "padded", "odd", "shifted", "cols", "cols_odd", "spread")
 
 @pytest.mark.parametrize("lx,lw", list(itertools.product(LAYOUTS, LAYOUTS)))
 def test_linear_operand_layouts(ic, lx, lw):
-    for m, k, n in ((5, 72, 136), (140, 136, 300)):
+    for m, k, n in ((5, 72, 136), (140, 136, 300), (9, 67, 45), (131, 70, 139), (260, 131, 261)):
         run_linear(ic, m, k, n, F16, "relu", lx=lx, lw=lw)
 
 
@@ -284,6 +284,7 @@ def test_linear_grad_layouts(ic, layout, which):
     layouts[which] = layout
     for act in ("none", "silu"):
         run_linear_grad(ic, 75, 72, 137, F16, act, layouts=layouts)
+        run_linear_grad(ic, 133, 139, 69, F16, act, layouts=layouts)
         run_linear_grad(ic, 264, 136, 144, BF16, act, layouts=layouts)
 
 
