@@ -27,10 +27,64 @@ __device__ __forceinline__ void store_from_float(void *p, int64_t i, int32_t dty
     }
 }
 
+// Two 16-bit values in a word, eight in a 16-byte vector.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int32_t dtype) {
+    if (dtype == CONV_FLOAT16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void unpack2(uint32_t w, int32_t dtype, float *lo, float *hi) {
+    if (dtype == CONV_FLOAT16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        *lo = f.x, *hi = f.y;
+    } else {
+        *lo = __uint_as_float(w << 16);
+        *hi = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *v, int32_t dtype) {
+    return make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype),
+                      pack2(v[6], v[7], dtype));
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &w, int32_t dtype, float *v) {
+    unpack2(w.x, dtype, v, v + 1);
+    unpack2(w.y, dtype, v + 2, v + 3);
+    unpack2(w.z, dtype, v + 4, v + 5);
+    unpack2(w.w, dtype, v + 6, v + 7);
+}
+
 // Logistic function and Phi, the standard normal distribution.
+__device__ __forceinline__ float exp2f_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678f * z); }
+// Phi(z) by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x),
+// off by at most 1.5e-7 for x >= 0; here x = |z| / sqrt(2) and the halved
+// coefficients give Phi(-|z|), off by 7.5e-8.  One exponential and one
+// reciprocal per value (erfcf takes about twice the instructions); *density
+// is exp(-z^2 / 2), which the slope needs too.
+__device__ __forceinline__ float normal_cdf(float z, float *density) {
+    const float e = exp2f_fast(-0.72134752f * z * z);
+    const float t = __fdividef(1.0f, fmaf(0.23164189f, fabsf(z), 1.0f));
+    float h = fmaf(t, 0.5307027145f, -0.7265760135f);
+    h = fmaf(t, h, 0.7107068705f);
+    h = fmaf(t, h, -0.142248368f);
+    h = fmaf(t, h, 0.127414796f);
+    h = h * t * e;
+    *density = e;
+    return z < 0.0f ? h : 1.0f - h;
+}
 
 // z/2 (1 + tanh u) = z * logistic(2u): no cancellation where tanh u is near -1.
 __device__ __forceinline__ float gelu_tanh_arg2(float z) {
@@ -40,7 +94,10 @@ __device__ __forceinline__ float gelu_tanh_arg2(float z) {
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (kAct == CONV_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if constexpr (kAct == CONV_ACT_GELU) return z * normal_cdf(z);
+    if constexpr (kAct == CONV_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, &e);
+    }
     if constexpr (kAct == CONV_ACT_GELU_TANH) return z * logistic(gelu_tanh_arg2(z));
     if constexpr (kAct == CONV_ACT_SILU) return z * logistic(z);
     return z;
@@ -50,7 +107,11 @@ __device__ __forceinline__ float activate(float z) {
 template <int kAct>
 __device__ __forceinline__ float activation_slope(float z) {
     if constexpr (kAct == CONV_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (kAct == CONV_ACT_GELU) return normal_cdf(z) + z * 0.39894228f * __expf(-0.5f * z * z);
+    if constexpr (kAct == CONV_ACT_GELU) {
+        float e;
+        const float c = normal_cdf(z, &e);
+        return fmaf(0.39894228f * z, e, c);
+    }
     if constexpr (kAct == CONV_ACT_GELU_TANH) {
         // (z held to +-64 in the second term, which has long vanished there,
         // so that no infinity meets its zero)

@@ -3,8 +3,12 @@
 // and dz with the bias gradient.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "channel.h"
+#include "channel_launch.cuh"
 #include "channel_math.cuh"
+#include "tc_ptx.cuh"
 
 namespace i8c {
 namespace {
@@ -20,6 +24,8 @@ __global__ void __launch_bounds__(256) pack_matrix_kernel(const uint16_t *src, i
     __shared__ uint16_t tile[32][33];
     const int64_t r0 = (int64_t)blockIdx.x / col_tiles * 32, c0 = (int64_t)blockIdx.x % col_tiles * 32;
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
         const int r = by_rows ? y + i : x, c = by_rows ? x : y + i;
@@ -36,9 +42,9 @@ conv_status pack_matrix(const MatRef &m, int64_t rows, int64_t cols, void *dst, 
     if (rt * ct > INT32_MAX) return CONV_ERR_TOO_LARGE;
     // lanes along the smaller stride (a dim of extent 1 has none)
     const bool by_rows = rows == 1 || (cols > 1 && m.cs <= m.rs);
-    pack_matrix_kernel<<<(unsigned)(rt * ct), 256, 0, s>>>((const uint16_t *)m.p, m.rs, m.cs, rows, cols,
-                                                           (uint16_t *)dst, ld, ct, by_rows);
-    return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    return launch_behind(pack_matrix_kernel, dim3((unsigned)(rt * ct)), 256, 0, s, (const uint16_t *)m.p, m.rs, m.cs, rows,
+                         cols, (uint16_t *)dst, ld, ct, by_rows)
+               ? CONV_OK : CONV_ERR_CUDA;
 }
 
 struct Packed {  // a packed copy in the workspace, or none
@@ -129,6 +135,8 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, i
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
     const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
     const int64_t r1 = r0 + rows_per_block < rows ? r0 + rows_per_block : rows;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
     float sum = 0.0f;
     if (c < cols)
         for (int64_t r = r0 + y; r < r1; r += 8) {
@@ -147,13 +155,80 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, i
     }
 }
 
-__global__ void __launch_bounds__(256) column_sum_kernel(const float *part, int64_t parts, int64_t cols, void *out,
-                                                         int32_t dtype) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
-    float sum = 0.0f;
-    for (int64_t i = 0; i < parts; ++i) sum += part[i * cols + c];
-    store_from_float(out, c, dtype, sum);
+// The same for rows of 16-byte vectors (columns contiguous and a multiple of
+// 8, aligned rows): 32 x 8 threads of 8 columns each, four rows in flight per
+// thread.
+template <int kAct>
+__global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
+                                                             int64_t rows_per_block, void *dz, int64_t dz_ld,
+                                                             float *part) {
+    __shared__ float red[8][256];
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * 256 + x * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
+    const int64_t r1 = r0 + rows_per_block < rows ? r0 + rows_per_block : rows;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    float sum[8] = {};
+    if (c < cols) {
+        constexpr int kRows = 4;
+        for (int64_t r = r0 + y; r < r1; r += 8 * kRows) {
+            uint4 g[kRows], z[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (r + 8 * i >= r1) break;
+                g[i] = *reinterpret_cast<const uint4 *>((const uint16_t *)dy.p + (r + 8 * i) * dy.rs + c);
+                if constexpr (kAct != CONV_ACT_NONE)
+                    z[i] = *reinterpret_cast<const uint4 *>((const uint16_t *)pre.p + (r + 8 * i) * pre.rs + c);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (r + 8 * i >= r1) break;
+                float v[8];
+                unpack8(g[i], dy.dtype, v);
+                if constexpr (kAct != CONV_ACT_NONE) {
+                    float p[8];
+                    unpack8(z[i], dy.dtype, p);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] *= activation_slope<kAct>(p[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += v[j];
+                if (dz)
+                    *reinterpret_cast<uint4 *>((uint16_t *)dz + (r + 8 * i) * dz_ld + c) = pack8(v, dy.dtype);
+            }
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[y][x * 8 + j] = sum[j];
+    __syncthreads();
+    const int64_t mine = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (mine < cols) {
+        float s = red[0][threadIdx.x];
+        for (int i = 1; i < 8; ++i) s += red[i][threadIdx.x];
+        part[(int64_t)blockIdx.y * cols + mine] = s;
+    }
+}
+
+// Adds the blocks' partial sums: 32 columns per block, 32 threads per column.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int64_t parts, int64_t cols, void *out,
+                                                          int32_t dtype) {
+    __shared__ float red[32][33];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+    const int64_t c = (int64_t)blockIdx.x * 32 + tx;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    float s = 0.0f;
+    if (c < cols)
+        for (int64_t i = ty; i < parts; i += 32) s += part[i * cols + c];
+    red[ty][tx] = s;
+    __syncthreads();
+    const int64_t mine = (int64_t)blockIdx.x * 32 + ty;
+    s = red[tx][ty];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (tx == 0 && mine < cols) store_from_float(out, mine, dtype, s);
 }
 
 struct GradPlan {
@@ -176,7 +251,9 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
             pl.dz_off = pl.bytes;
             pl.bytes += (size_t)round_up(m * pl.dz_ld * 2, 256);
         }
-        pl.rows_per_part = round_up((m + 255) / 256, 8);
+        // enough blocks for every SM to hold several, whichever kernel runs
+        const int64_t wanted = std::min<int64_t>(512, std::max<int64_t>(1, 2432 / ((n + 255) / 256)));
+        pl.rows_per_part = round_up((m + wanted - 1) / wanted, 8);
         pl.parts = (m + pl.rows_per_part - 1) / pl.rows_per_part;
         pl.part_off = pl.bytes;
         pl.bytes += (size_t)round_up(pl.parts * n * 4, 256);
@@ -189,10 +266,14 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
 template <int kAct>
 void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, bool sums,
                cudaStream_t s) {
-    const dim3 grid((unsigned)((n + 31) / 32), (unsigned)pl.parts);
-    linear_dz_kernel<kAct><<<grid, 256, 0, s>>>(dy, pre, m, n, pl.rows_per_part,
-                                                pl.dz ? (char *)ws + pl.dz_off : nullptr, pl.dz_ld,
-                                                sums ? (float *)((char *)ws + pl.part_off) : nullptr);
+    void *dz = pl.dz ? (char *)ws + pl.dz_off : nullptr;
+    float *part = sums ? (float *)((char *)ws + pl.part_off) : nullptr;
+    if (n % 8 == 0 && vector_rows(dy) && vector_rows(pre))
+        launch_behind(linear_dz_rows_kernel<kAct>, dim3((unsigned)((n + 255) / 256), (unsigned)pl.parts), 256, 0, s, dy,
+                      pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part);
+    else
+        launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts), 256, 0, s, dy, pre,
+                      m, n, pl.rows_per_part, dz, pl.dz_ld, part);
 }
 
 conv_status make_dz(const GradPlan &pl, int32_t act, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n,
@@ -205,8 +286,8 @@ conv_status make_dz(const GradPlan &pl, int32_t act, const MatRef &dy, const Mat
         default: launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, s); break;
     }
     if (dbias)
-        column_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>((const float *)((char *)ws + pl.part_off),
-                                                                      pl.parts, n, dbias, bias_dtype);
+        launch_behind(column_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, 0, s,
+                      (const float *)((char *)ws + pl.part_off), pl.parts, n, dbias, bias_dtype);
     return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 

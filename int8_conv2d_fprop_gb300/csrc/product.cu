@@ -225,25 +225,6 @@ __device__ __forceinline__ void tile_at(const ProductArgs &a, int t, int *ia, in
 }
 
 // ---------------------------------------------------------------- epilogue
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, int32_t dtype) {
-    if (dtype == CONV_FLOAT16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ void unpack2(uint32_t w, int32_t dtype, float *lo, float *hi) {
-    if (dtype == CONV_FLOAT16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-        *lo = f.x, *hi = f.y;
-    } else {
-        *lo = __uint_as_float(w << 16);
-        *hi = __uint_as_float(w & 0xffff0000u);
-    }
-}
-
 template <int kAct, int W>
 __device__ __forceinline__ void activate_all(float (&v)[W]) {
 #pragma unroll
@@ -319,10 +300,7 @@ __device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, floa
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 w = ptx::ld_shared_v4(t.stage + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4));
-                unpack2(w.x, s.dtype, &r[8 * i], &r[8 * i + 1]);
-                unpack2(w.y, s.dtype, &r[8 * i + 2], &r[8 * i + 3]);
-                unpack2(w.z, s.dtype, &r[8 * i + 4], &r[8 * i + 5]);
-                unpack2(w.w, s.dtype, &r[8 * i + 6], &r[8 * i + 7]);
+                unpack8(w, s.dtype, r + 8 * i);
             }
         }
         __syncwarp();
@@ -377,8 +355,7 @@ __device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *map
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 ptx::st_shared_v4(buf + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4),
-                                  make_uint4(pack2(v[8 * i], v[8 * i + 1], s.dtype), pack2(v[8 * i + 2], v[8 * i + 3], s.dtype),
-                                             pack2(v[8 * i + 4], v[8 * i + 5], s.dtype), pack2(v[8 * i + 6], v[8 * i + 7], s.dtype)));
+                                  pack8(v + 8 * i, s.dtype));
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -417,9 +394,7 @@ __device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *, W
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-            *reinterpret_cast<uint4 *>((uint16_t *)s.p + at) =
-                make_uint4(pack2(v[0], v[1], s.dtype), pack2(v[2], v[3], s.dtype), pack2(v[4], v[5], s.dtype),
-                           pack2(v[6], v[7], s.dtype));
+            *reinterpret_cast<uint4 *>((uint16_t *)s.p + at) = pack8(v, s.dtype);
         }
         return;
     }
@@ -782,7 +757,16 @@ conv_status product_launch(const Product &given, void *stream) {
     int grid, cluster;
     a.split = 1;
     if (pair) {
-        a.tile_b = 256;
+        // The width that wastes least in the last round of tiles; 32 columns
+        // stand for a tile's share of operand A's loads.
+        int64_t best = INT64_MAX;
+        for (int nt = 256; nt >= 128; nt -= 32) {
+            const int64_t rounds = cdiv(cdiv(pr.ma, 256) * cdiv(pr.nb, nt), sms / 2);
+            if (rounds * (nt + 32) < best) {
+                best = rounds * (nt + 32);
+                a.tile_b = nt;
+            }
+        }
         a.tiles_a = (int32_t)cdiv(pr.ma, 256);
         a.tiles_b = (int32_t)cdiv(pr.nb, a.tile_b);
         a.b_rows = a.tile_b / 2;
