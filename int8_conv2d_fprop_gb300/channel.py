@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from ctypes import byref as _byref
 
 CONV_FLOAT32, CONV_FLOAT16, CONV_BFLOAT16 = 3, 4, 5
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
@@ -55,16 +56,31 @@ def declare(L) -> None:
         f.restype = ctypes.c_int
 
 
-_SIZES = None
+_lib = None        # the loaded library, its types declared
+_torch = None
+_types = {}        # torch dtype -> (code, element size)
+_raw_stream = None  # device index -> address of its current stream
+_WORKSPACE = 13    # CONV_ERR_WORKSPACE
 
 
-def _types():
-    global _SIZES
-    if _SIZES is None:
-        import torch
-        _SIZES = {torch.int8: (1, 1), torch.int32: (2, 4), torch.float32: (CONV_FLOAT32, 4),
-                  torch.float16: (CONV_FLOAT16, 2), torch.bfloat16: (CONV_BFLOAT16, 2)}
-    return _SIZES
+def _load():
+    global _lib, _torch, _raw_stream
+    import torch
+
+    from . import lib
+    _torch = torch
+    _types.update({torch.int8: (1, 1), torch.int32: (2, 4), torch.float32: (CONV_FLOAT32, 4),
+                   torch.float16: (CONV_FLOAT16, 2), torch.bfloat16: (CONV_BFLOAT16, 2)})
+    # the address alone costs a small part of a torch.cuda.Stream object
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _lib = lib()
+    return _lib
+
+
+def _failed(status: int, what: str):
+    from . import ConvError
+    raise ConvError(status, what)
 
 
 def _matrix(t, what: str):
@@ -73,34 +89,37 @@ def _matrix(t, what: str):
     taken, nothing is copied)."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    code, size = _types().get(t.dtype, (0, 1))
     shape = t.shape
-    if len(shape) != 2:
+    if len(shape) == 2:
+        rows, cols = shape
+        rs, cs = t.stride()
+    else:
         if len(shape) == 0:
             raise ValueError(f"{what} must have at least one dimension")
         try:
-            t = t.view(math.prod(shape[:-1]), shape[-1])
+            v = t.view(math.prod(shape[:-1]), shape[-1])
         except RuntimeError as e:
             raise ValueError(f"{what}: leading dimensions without a common stride; make it contiguous") from e
-        shape = t.shape
-    rows, cols = shape
-    rs, cs = t.stride()
+        rows, cols = v.shape
+        rs, cs = v.stride()
+    code, size = _types.get(t.dtype, (0, 1))
     # (a torch tensor always lies inside its storage: the capacity is its own extent)
-    last = (rows - 1) * rs + (cols - 1) * cs + 1 if rows and cols else 0
-    return MatrixDesc(code, 0, rows, cols, rs, cs, last * size)
+    return MatrixDesc(code, 0, rows, cols, rs, cs, ((rows - 1) * rs + (cols - 1) * cs + 1) * size if rows and cols else 0)
 
 
 def _vector(t, n: int, what: str):
     if t is None:
         return None
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or not (t.is_contiguous() or n <= 1):
+    shape = t.shape
+    if not t.is_cuda or len(shape) != 1 or shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous CUDA vector of {n} elements")
     return t.data_ptr()
 
 
 def _stats(t, n: int, what: str):
-    import torch
-    if t is not None and t.dtype != torch.float32:
+    if t is None:
+        return None
+    if t.dtype != _torch.float32:
         raise ValueError(f"{what} must be float32")
     return _vector(t, n, what)
 
@@ -113,38 +132,27 @@ def _activation(a) -> int:
     return int(a)
 
 
-class _Call:
-    """Where a call's memory comes from: the stream it runs on."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.torch, self.device, self.given = torch, device, stream is not None
-        self.stream = stream if self.given else torch.cuda.current_stream(device)
-
-    def empty(self, shape, dtype):
-        # memory that is first used on the call's stream belongs to it, so
-        # that the allocator hands it out again only behind the call
-        if self.given:
-            with self.torch.cuda.stream(self.stream):
-                return self.torch.empty(shape, dtype=dtype, device=self.device)
-        return self.torch.empty(shape, dtype=dtype, device=self.device)
-
-    def workspace(self, need: int, given):
-        if need == 0:
-            return None, 0
-        if given is None or given.numel() * given.element_size() < need:
-            given = self.empty((need,), self.torch.uint8)
-        return given, given.numel() * given.element_size()
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream` (None: the current one).  Memory that is
+    first used on the call's stream belongs to it, so that the allocator
+    hands it out again only behind the call."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _workspace(need: int, given, device, stream):
+    """(tensor to keep until the call is queued, address, bytes)"""
+    if need == 0:
+        return None, None, 0
+    if given is None or given.numel() * given.element_size() < need:
+        given = _empty((need,), _torch.uint8, device, stream)
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
 
-def _need(status: int, size, what: str) -> int:
-    from . import _check
-    _check(status, what)
-    return int(size.value)
+def _stream(stream, device) -> int:
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def conv_linear(x, w, bias=None, *, activation=ACT_NONE, residual=None, preact=None, out=None, workspace=None,
@@ -160,25 +168,36 @@ def conv_linear(x, w, bias=None, *, activation=ACT_NONE, residual=None, preact=N
     ``residual`` itself may be given).  Sums are in 32 bits.  Runs on
     ``stream`` (default: the current one).  Returns ``out``.
     """
-    from . import _check, lib
-    L = lib()
-    c = _Call(x.device, stream)
+    L = _lib or _load()
     xd, wd = _matrix(x, "x"), _matrix(w, "w")
+    device = x.device
     if out is None:
-        out = c.empty((*x.shape[:-1], wd.rows), x.dtype)
+        shape = x.shape
+        out = _empty((shape[0], wd.rows) if len(shape) == 2 else (*shape[:-1], wd.rows), x.dtype, device, stream)
     yd = _matrix(out, "out")
-    rd = None if residual is None else _matrix(residual, "residual")
-    zd = None if preact is None else _matrix(preact, "preact")
-    code = 0 if bias is None else _types().get(bias.dtype, (0, 1))[0]
-    p = LinearParams(_activation(activation), code)
-    ref = ctypes.byref
-    xp, wp = x.data_ptr(), w.data_ptr()
-    size = ctypes.c_size_t()
-    need = _need(L.conv_linear_workspace_size(ref(xd), xp, ref(wd), wp, ref(size)), size, "linear workspace size")
-    ws, have = c.workspace(need, workspace)
-    _check(L.conv_linear(ref(xd), xp, ref(wd), wp, _vector(bias, wd.rows, "bias"), rd and ref(rd), _ptr(residual),
-                         zd and ref(zd), _ptr(preact), ref(yd), out.data_ptr(), ref(p), _ptr(ws), have,
-                         c.stream.cuda_stream), "conv_linear")
+    rd = zd = rp = zp = bp = None
+    code = 0
+    if residual is not None:
+        rd, rp = _byref(_matrix(residual, "residual")), residual.data_ptr()
+    if preact is not None:
+        zd, zp = _byref(_matrix(preact, "preact")), preact.data_ptr()
+    if bias is not None:
+        bp, code = _vector(bias, wd.rows, "bias"), _types.get(bias.dtype, (0, 1))[0]
+    p = _byref(LinearParams(_activation(activation), code))
+    xp, wp, yp, s = x.data_ptr(), w.data_ptr(), out.data_ptr(), _stream(stream, device)
+    xd, wd, yd = _byref(xd), _byref(wd), _byref(yd)
+    status = _WORKSPACE
+    if workspace is None:
+        # most calls need none; one that does is refused before anything runs
+        status = L.conv_linear(xd, xp, wd, wp, bp, rd, rp, zd, zp, yd, yp, p, None, 0, s)
+    if status == _WORKSPACE:
+        size = ctypes.c_size_t()
+        status = L.conv_linear_workspace_size(xd, xp, wd, wp, _byref(size))
+        if status == 0:
+            keep, ws, have = _workspace(size.value, workspace, device, stream)
+            status = L.conv_linear(xd, xp, wd, wp, bp, rd, rp, zd, zp, yd, yp, p, ws, have, s)
+    if status:
+        _failed(status, "conv_linear")
     return out
 
 
@@ -189,24 +208,29 @@ def conv_linear_grad(dy, x, w, *, preact=None, activation=ACT_NONE, dx=None, dw=
     given.  dy [..., N] is the loss gradient, preact the pre-activation of
     the forward call (needed with an activation); the residual's gradient is
     dy itself.  Returns (dx, dw, dbias)."""
-    from . import _check, lib
-    L = lib()
-    c = _Call(x.device, stream)
+    L = _lib or _load()
     gd, xd, wd = _matrix(dy, "dy"), _matrix(x, "x"), _matrix(w, "w")
-    zd = None if preact is None else _matrix(preact, "preact")
-    dxd = None if dx is None else _matrix(dx, "dx")
-    dwd = None if dw is None else _matrix(dw, "dw")
-    code = 0 if dbias is None else _types().get(dbias.dtype, (0, 1))[0]
-    p = LinearParams(_activation(activation), code)
-    ref = ctypes.byref
-    gp, xp, wp = dy.data_ptr(), x.data_ptr(), w.data_ptr()
+    device = x.device
+    zd = dxd = dwd = zp = dxp = dwp = dbp = None
+    code = 0
+    if preact is not None:
+        zd, zp = _byref(_matrix(preact, "preact")), preact.data_ptr()
+    if dx is not None:
+        dxd, dxp = _byref(_matrix(dx, "dx")), dx.data_ptr()
+    if dw is not None:
+        dwd, dwp = _byref(_matrix(dw, "dw")), dw.data_ptr()
+    if dbias is not None:
+        dbp, code = _vector(dbias, wd.rows, "dbias"), _types.get(dbias.dtype, (0, 1))[0]
+    p = _byref(LinearParams(_activation(activation), code))
+    gp, xp, wp, s = dy.data_ptr(), x.data_ptr(), w.data_ptr(), _stream(stream, device)
+    gd, xd, wd = _byref(gd), _byref(xd), _byref(wd)
     size = ctypes.c_size_t()
-    need = _need(L.conv_linear_grad_workspace_size(ref(gd), gp, ref(xd), xp, ref(wd), wp, ref(p), ref(size)), size,
-                 "linear gradient workspace size")
-    ws, have = c.workspace(need, workspace)
-    _check(L.conv_linear_grad(ref(gd), gp, ref(xd), xp, ref(wd), wp, zd and ref(zd), _ptr(preact), dxd and ref(dxd),
-                              _ptr(dx), dwd and ref(dwd), _ptr(dw), _vector(dbias, wd.rows, "dbias"), ref(p),
-                              _ptr(ws), have, c.stream.cuda_stream), "conv_linear_grad")
+    status = L.conv_linear_grad_workspace_size(gd, gp, xd, xp, wd, wp, p, _byref(size))
+    if status == 0:
+        keep, ws, have = _workspace(size.value, workspace, device, stream)
+        status = L.conv_linear_grad(gd, gp, xd, xp, wd, wp, zd, zp, dxd, dxp, dwd, dwp, dbp, p, ws, have, s)
+    if status:
+        _failed(status, "conv_linear_grad")
     return dx, dw, dbias
 
 
@@ -220,18 +244,17 @@ def conv_layer_norm(x, gain=None, shift=None, *, eps: float = 1e-5, scale: float
     float32 for int32); mean, rstd: optional float32 vectors with one element
     per row that receive the statistics (what conv_layer_norm_grad wants).
     Returns ``out``."""
-    from . import _check, lib
-    L = lib()
-    c = _Call(x.device, stream)
+    L = _lib or _load()
     xd = _matrix(x, "x")
+    device, c, m = x.device, xd.cols, xd.rows
     if out is None:
-        out = c.empty(x.shape, x.dtype if x.dtype.is_floating_point else c.torch.float32)
-    yd = _matrix(out, "out")
+        out = _empty(x.shape, x.dtype if x.dtype.is_floating_point else _torch.float32, device, stream)
     p = LayerNormParams(eps, scale, _param_dtype(gain, shift), 0)
-    ref = ctypes.byref
-    _check(L.conv_layer_norm(ref(xd), x.data_ptr(), _vector(gain, xd.cols, "gain"), _vector(shift, xd.cols, "shift"),
-                             ref(yd), out.data_ptr(), _stats(mean, xd.rows, "mean"), _stats(rstd, xd.rows, "rstd"),
-                             ref(p), c.stream.cuda_stream), "conv_layer_norm")
+    status = L.conv_layer_norm(_byref(xd), x.data_ptr(), _vector(gain, c, "gain"), _vector(shift, c, "shift"),
+                               _byref(_matrix(out, "out")), out.data_ptr(), _stats(mean, m, "mean"),
+                               _stats(rstd, m, "rstd"), _byref(p), _stream(stream, device))
+    if status:
+        _failed(status, "conv_layer_norm")
     return out
 
 
@@ -242,27 +265,35 @@ def conv_layer_norm_grad(dy, x, gain, mean, rstd, *, residual_grad=None, dx=None
     dx [..., C] (x's type; residual_grad is added to it), dgain and dshift
     [C] (float32 or x's type, gain's type when gain is given) that are
     given.  Returns (dx, dgain, dshift)."""
-    from . import _check, lib
-    L = lib()
-    c = _Call(x.device, stream)
+    L = _lib or _load()
     gd, xd = _matrix(dy, "dy"), _matrix(x, "x")
-    rd = None if residual_grad is None else _matrix(residual_grad, "residual_grad")
-    dxd = None if dx is None else _matrix(dx, "dx")
+    device, c, m = x.device, xd.cols, xd.rows
+    rd = dxd = rp = dxp = None
+    if residual_grad is not None:
+        rd, rp = _byref(_matrix(residual_grad, "residual_grad")), residual_grad.data_ptr()
+    if dx is not None:
+        dxd, dxp = _byref(_matrix(dx, "dx")), dx.data_ptr()
     p = LayerNormParams(1e-5, 1.0, _param_dtype(gain, dgain, dshift), 0)
-    ref = ctypes.byref
+    xd = _byref(xd)
     size = ctypes.c_size_t()
-    need = _need(L.conv_layer_norm_grad_workspace_size(ref(xd), ref(size)), size, "layer norm gradient workspace size")
-    ws, have = c.workspace(need, workspace)
-    _check(L.conv_layer_norm_grad(ref(gd), dy.data_ptr(), ref(xd), x.data_ptr(), _vector(gain, xd.cols, "gain"),
-                                  _stats(mean, xd.rows, "mean"), _stats(rstd, xd.rows, "rstd"), rd and ref(rd),
-                                  _ptr(residual_grad), dxd and ref(dxd), _ptr(dx), _vector(dgain, xd.cols, "dgain"),
-                                  _vector(dshift, xd.cols, "dshift"), ref(p), _ptr(ws), have, c.stream.cuda_stream),
-           "conv_layer_norm_grad")
+    status = L.conv_layer_norm_grad_workspace_size(xd, _byref(size))
+    if status == 0:
+        keep, ws, have = _workspace(size.value, workspace, device, stream)
+        status = L.conv_layer_norm_grad(_byref(gd), dy.data_ptr(), xd, x.data_ptr(), _vector(gain, c, "gain"),
+                                        _stats(mean, m, "mean"), _stats(rstd, m, "rstd"), rd, rp, dxd, dxp,
+                                        _vector(dgain, c, "dgain"), _vector(dshift, c, "dshift"), _byref(p), ws, have,
+                                        _stream(stream, device))
+    if status:
+        _failed(status, "conv_layer_norm_grad")
     return dx, dgain, dshift
 
 
 def _param_dtype(*tensors) -> int:
-    codes = {_types().get(t.dtype, (0, 1))[0] for t in tensors if t is not None}
-    if len(codes) > 1:
-        raise ValueError("gain, shift and their gradients must have one type")
-    return codes.pop() if codes else CONV_FLOAT32
+    code = 0
+    for t in tensors:
+        if t is not None:
+            c = _types.get(t.dtype, (0, 1))[0]
+            if code and c != code:
+                raise ValueError("gain, shift and their gradients must have one type")
+            code = c
+    return code or CONV_FLOAT32

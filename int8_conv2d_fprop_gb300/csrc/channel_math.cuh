@@ -59,71 +59,151 @@ __device__ __forceinline__ void unpack8(const uint4 &w, int32_t dtype, float *v)
     unpack2(w.w, dtype, v + 6, v + 7);
 }
 
-// Logistic function and Phi, the standard normal distribution.
-__device__ __forceinline__ float exp2f_fast(float v) {
+// ---------------------------------------------------------------- pairs
+// The activations work on two values at a time with the packed 32-bit
+// instructions, which take half the issue slots of the plain ones.
+struct Pair {
+    uint64_t v;
+};
+
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(Pair p, float *a, float *b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(p.v)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_approx(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// |v| held to `to`, max(v, 0): both keep a NaN.
+__device__ __forceinline__ float abs_min(float v, float to) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(v)), "f"(to));
+    return r;
+}
+__device__ __forceinline__ float max0(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ Pair exp2_2(Pair p) {
+    float a, b;
+    split(p, &a, &b);
+    return pair(exp2_approx(a), exp2_approx(b));
+}
 
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// Logistic function of u from -u * log2(e): 1 / (1 + 2^arg).
+__device__ __forceinline__ Pair logistic_of(Pair arg) {
+    const Pair d = add2(exp2_2(arg), pair(1.0f));
+    float a, b;
+    split(d, &a, &b);
+    return pair(rcp_approx(a), rcp_approx(b));
+}
 
-// Phi(z) by formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
-// Functions: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2), t = 1 / (1 + p x),
-// off by at most 1.5e-7 for x >= 0; here x = |z| / sqrt(2) and the halved
-// coefficients give Phi(-|z|), off by 7.5e-8.  One exponential and one
-// reciprocal per value (erfcf takes about twice the instructions); *density
-// is exp(-z^2 / 2), which the slope needs too.
-__device__ __forceinline__ float normal_cdf(float z, float *density) {
-    const float e = exp2f_fast(-0.72134752f * z * z);
-    const float t = __fdividef(1.0f, fmaf(0.23164189f, fabsf(z), 1.0f));
-    float h = fmaf(t, 0.5307027145f, -0.7265760135f);
-    h = fmaf(t, h, 0.7107068705f);
-    h = fmaf(t, h, -0.142248368f);
-    h = fmaf(t, h, 0.127414796f);
-    h = h * t * e;
+// z/2 (1 + tanh u) = z * logistic(2u), without cancellation where tanh u is
+// near -1; the logistic's argument is 2u = 2 sqrt(2/pi) (z + 0.044715 z^3).
+__device__ __forceinline__ Pair gelu_tanh_arg(Pair z) {
+    const Pair z2 = mul2(z, z);
+    return mul2(z, fma2(z2, pair(-0.102943245f), pair(-2.302208198f)));  // times -log2(e)
+}
+
+// Phi(-x) for x = min(|z|, 16), negated: exp(-x^2/2) times a polynomial of
+// degree 10 fitted to minimise the largest error of the product over
+// [0, 6.5] (weighted least squares on Chebyshev nodes, reweighted towards
+// the maximum): off by 1.2e-7 at most in 32-bit arithmetic, beyond the
+// interval by less still, since the exponential vanishes faster than the
+// polynomial grows.  One exponential and no reciprocal per value.
+__device__ __forceinline__ Pair minus_normal_tail(Pair x, Pair *density) {
+    const Pair e = exp2_2(mul2(mul2(x, x), pair(-0.72134752f)));
+    Pair r = fma2(x, pair(-1.631688633e-06f), pair(3.520776227e-05f));
+    r = fma2(x, r, pair(-3.397382679e-04f));
+    r = fma2(x, r, pair(1.974626677e-03f));
+    r = fma2(x, r, pair(-7.939388976e-03f));
+    r = fma2(x, r, pair(2.431392670e-02f));
+    r = fma2(x, r, pair(-6.115488335e-02f));
+    r = fma2(x, r, pair(1.325137913e-01f));
+    r = fma2(x, r, pair(-2.499167919e-01f));
+    r = fma2(x, r, pair(3.989365101e-01f));
+    r = fma2(x, r, pair(-4.999999404e-01f));
     *density = e;
-    return z < 0.0f ? h : 1.0f - h;
+    return mul2(r, e);
 }
 
-// z/2 (1 + tanh u) = z * logistic(2u): no cancellation where tanh u is near -1.
-__device__ __forceinline__ float gelu_tanh_arg2(float z) {
-    return 1.5957691216f * (z + 0.044715f * z * z * z);
-}
-
+// Activation of two values, in place.
 template <int kAct>
-__device__ __forceinline__ float activate(float z) {
-    if constexpr (kAct == CONV_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if constexpr (kAct == CONV_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, &e);
+__device__ __forceinline__ void activate(float &a, float &b) {
+    if constexpr (kAct == CONV_ACT_RELU) {
+        a = max0(a), b = max0(b);
+    } else if constexpr (kAct == CONV_ACT_GELU) {
+        // z Phi(z) = max(z, 0) - x Phi(-x), x = |z| (0 for z = -inf, its limit)
+        Pair e;
+        const Pair x = pair(abs_min(a, 16.0f), abs_min(b, 16.0f));
+        split(fma2(x, minus_normal_tail(x, &e), pair(max0(a), max0(b))), &a, &b);
+    } else if constexpr (kAct == CONV_ACT_GELU_TANH) {
+        const Pair z = pair(a, b);
+        split(mul2(z, logistic_of(gelu_tanh_arg(z))), &a, &b);
+    } else if constexpr (kAct == CONV_ACT_SILU) {
+        const Pair z = pair(a, b);
+        split(mul2(z, logistic_of(mul2(z, pair(-1.442695041f)))), &a, &b);
     }
-    if constexpr (kAct == CONV_ACT_GELU_TANH) return z * logistic(gelu_tanh_arg2(z));
-    if constexpr (kAct == CONV_ACT_SILU) return z * logistic(z);
-    return z;
 }
 
-// Derivative of the activation at z.
+// Derivative of the activation at two values, in place.
 template <int kAct>
-__device__ __forceinline__ float activation_slope(float z) {
-    if constexpr (kAct == CONV_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if constexpr (kAct == CONV_ACT_GELU) {
-        float e;
-        const float c = normal_cdf(z, &e);
-        return fmaf(0.39894228f * z, e, c);
+__device__ __forceinline__ void activation_slope(float &a, float &b) {
+    if constexpr (kAct == CONV_ACT_RELU) {
+        a = a > 0.0f ? 1.0f : 0.0f, b = b > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (kAct == CONV_ACT_GELU) {
+        // Phi(z) + z phi(z), Phi(z) = 1/2 + sign(z) (1/2 - Phi(-x))
+        Pair e;
+        const Pair x = pair(abs_min(a, 16.0f), abs_min(b, 16.0f));
+        float u, v;
+        split(add2(minus_normal_tail(x, &e), pair(0.5f)), &u, &v);
+        const Pair z = pair(copysignf(u, a), copysignf(v, b));
+        split(x, &u, &v);  // (z phi(z) with z held to +-16 as well: phi is 0 there)
+        const Pair zc = pair(copysignf(u, a), copysignf(v, b));
+        split(fma2(mul2(zc, pair(0.39894228f)), e, add2(z, pair(0.5f))), &a, &b);
+    } else if constexpr (kAct == CONV_ACT_GELU_TANH) {
+        // s + z s (1 - s) (2u)', s = logistic(2u); z held to +-64 in the
+        // second term, which has long vanished there, so that no infinity
+        // meets its zero
+        const Pair s = logistic_of(gelu_tanh_arg(pair(a, b)));
+        const Pair z = pair(copysignf(abs_min(a, 64.0f), a), copysignf(abs_min(b, 64.0f), b));
+        const Pair d = mul2(z, fma2(mul2(z, z), pair(0.2140644488f), pair(1.5957691216f)));
+        const Pair q = fma2(mul2(s, pair(-1.0f)), s, s);
+        split(fma2(d, q, s), &a, &b);
+    } else if constexpr (kAct == CONV_ACT_SILU) {
+        const Pair z = pair(a, b);
+        const Pair s = logistic_of(mul2(z, pair(-1.442695041f)));
+        const Pair q = fma2(mul2(s, pair(-1.0f)), s, s);
+        split(fma2(z, q, s), &a, &b);
+    } else {
+        a = 1.0f, b = 1.0f;
     }
-    if constexpr (kAct == CONV_ACT_GELU_TANH) {
-        // (z held to +-64 in the second term, which has long vanished there,
-        // so that no infinity meets its zero)
-        const float s = logistic(gelu_tanh_arg2(z));
-        const float zc = fminf(fmaxf(z, -64.0f), 64.0f);
-        return s + zc * s * (1.0f - s) * 1.5957691216f * (1.0f + 0.134145f * zc * zc);
-    }
-    if constexpr (kAct == CONV_ACT_SILU) {
-        const float s = logistic(z);
-        return s + z * s * (1.0f - s);
-    }
-    return 1.0f;
 }
 
 }  // namespace i8c

@@ -141,8 +141,11 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, i
     if (c < cols)
         for (int64_t r = r0 + y; r < r1; r += 8) {
             float v = load_as_float(dy.p, r * dy.rs + c * dy.cs, dy.dtype);
-            if constexpr (kAct != CONV_ACT_NONE)
-                v *= activation_slope<kAct>(load_as_float(pre.p, r * pre.rs + c * pre.cs, pre.dtype));
+            if constexpr (kAct != CONV_ACT_NONE) {
+                float slope = load_as_float(pre.p, r * pre.rs + c * pre.cs, pre.dtype), unused = 0.0f;
+                activation_slope<kAct>(slope, unused);
+                v *= slope;
+            }
             if (dz) store_from_float(dz, r * dz_ld + c, dy.dtype, v);
             sum += v;
         }
@@ -190,7 +193,11 @@ __global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef p
                     float p[8];
                     unpack8(z[i], dy.dtype, p);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= activation_slope<kAct>(p[j]);
+                    for (int j = 0; j < 8; j += 2) {
+                        activation_slope<kAct>(p[j], p[j + 1]);
+                        v[j] *= p[j];
+                        v[j + 1] *= p[j + 1];
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += v[j];

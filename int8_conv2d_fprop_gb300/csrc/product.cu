@@ -228,7 +228,7 @@ __device__ __forceinline__ void tile_at(const ProductArgs &a, int t, int *ia, in
 template <int kAct, int W>
 __device__ __forceinline__ void activate_all(float (&v)[W]) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = activate<kAct>(v[j]);
+    for (int j = 0; j < W; j += 2) activate<kAct>(v[j], v[j + 1]);
 }
 
 template <int W>
@@ -306,16 +306,22 @@ __device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, floa
         __syncwarp();
         return;
     }
-    for (int rr = 0; rr < t.rows; ++rr)
-        if (t.lane < t.cols)
-            ptx::st_shared_b32(t.stage + (rr * 32 + (t.lane ^ rr)) * 4,
-                               __float_as_uint(load_as_float(s.p, (int64_t)(t.row0 + rr) * s.sa +
-                                                                      (int64_t)(t.b0 + t.lane) * s.sb, s.dtype)));
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+        float q[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            q[i] = r0 + i < t.rows && t.lane < t.cols
+                       ? load_as_float(s.p, (int64_t)(t.row0 + r0 + i) * s.sa + (int64_t)(t.b0 + t.lane) * s.sb, s.dtype)
+                       : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            ptx::st_shared_b32(t.stage + ((r0 + i) * 32 + (t.lane ^ (r0 + i))) * 4, __float_as_uint(q[i]));
+    }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        r[j] = t.lane < t.rows && j < t.cols
-                   ? __uint_as_float(ptx::ld_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4)) : 0.0f;
+        r[j] = __uint_as_float(ptx::ld_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4));
     __syncwarp();
 }
 
@@ -371,6 +377,7 @@ __device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *map
     for (int j = 0; j < 32; ++j) ptx::st_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4, __float_as_uint(v[j]));
     __syncwarp();
     if (t.lane < t.cols)
+#pragma unroll 8
         for (int rr = 0; rr < t.rows; ++rr)
             store_from_float(s.p, (int64_t)(t.row0 + rr) * s.sa + (int64_t)(t.b0 + t.lane) * s.sb, s.dtype,
                              __uint_as_float(ptx::ld_shared_b32(t.stage + (rr * 32 + (t.lane ^ rr)) * 4)));
@@ -403,18 +410,23 @@ __device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *, W
         if (j < t.cols) store_from_float(s.p, at + j * s.sb, s.dtype, v[j]);
 }
 
+// The lane's bias: of its row, or of column b0 + lane for the others to share.
+__device__ __forceinline__ float lane_bias(const ProductArgs &a, int row0, int b0, int lane) {
+    if (!a.bias) return 0.0f;
+    const int at = (a.bias_along_a ? row0 : b0) + lane;
+    return at < (a.bias_along_a ? a.ma : a.nb) ? load_as_float(a.bias, at, a.bias_dtype) : 0.0f;
+}
+
 template <int W>
-__device__ __forceinline__ void finish_tile(const ProductArgs &a, WarpTile &t, uint32_t bias_smem, float (&v)[W]) {
+__device__ __forceinline__ void finish_tile(const ProductArgs &a, WarpTile &t, uint32_t bias_smem, float b, float (&v)[W]) {
     if (a.bias) {
         if (a.bias_along_a) {
-            const float b = t.lane < t.rows ? load_as_float(a.bias, t.row0 + t.lane, a.bias_dtype) : 0.0f;
 #pragma unroll
             for (int j = 0; j < W; ++j) v[j] += b;
         } else {
             // lane j's bias to every row, through 128 bytes of shared memory
             __syncwarp();
-            ptx::st_shared_b32(bias_smem + t.lane * 4,
-                               __float_as_uint(t.lane < t.cols ? load_as_float(a.bias, t.b0 + t.lane, a.bias_dtype) : 0.0f));
+            ptx::st_shared_b32(bias_smem + t.lane * 4, __float_as_uint(b));
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < W; j += 4) {
@@ -582,11 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int ia, ib;
             tile_at(a, t, &ia, &ib);
             const int slot = n & 1;
+            const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
+            // this warp's biases, loaded while the tile is being summed
+            float bias[kMaxTileB / 64];
+#pragma unroll
+            for (int i = 0; i < kMaxTileB / 64; ++i)
+                bias[i] = part * 32 + i * 64 < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + part * 32 + i * 64, lane) : 0.0f;
             if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) break;
             ptx::tc_fence_after();
-            const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
-            const bool none = k_lo == k_hi;  // no products: the accumulator was never written
+            if (k_lo == k_hi) {  // no products: the accumulator was never written
+                const uint32_t zero[32] = {};
+                for (int c = part * 32; c < a.tile_b; c += 64) ptx::tmem_st_32x32b_x32(acc + c, zero);
+                ptx::tmem_st_wait();
+            }
             wt.row0 = row0;
             wt.rows = min(32, a.ma - row0);
             if (!kPair && a.split > 1) {
@@ -598,11 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        ptx::st_shared_b32(ring + ((c + j) * kTileA + quad * 32 + lane) * 4, none ? 0u : v[j]);
+                        ptx::st_shared_b32(ring + ((c + j) * kTileA + quad * 32 + lane) * 4, v[j]);
                 }
                 break;  // one tile per cluster; the rest follows the cluster barrier
             }
-            for (int c = part * 32; c < a.tile_b; c += 64) {
+#pragma unroll
+            for (int i = 0; i < kMaxTileB / 64; ++i) {
+                const int c = part * 32 + i * 64;
+                if (c >= a.tile_b) break;
                 uint32_t u[32];
                 ptx::tmem_ld_32x32b_x32(acc + c, u);
                 ptx::tmem_ld_wait();
@@ -611,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = none ? 0.0f : __uint_as_float(u[j]);
-                finish_tile<32>(a, wt, my_bias, v);
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+                finish_tile<32>(a, wt, my_bias, bias[i], v);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] += ld_cluster_f32(src + j * kTileA * 4);
                 }
-                finish_tile<8>(a, wt, bias_smem + e * 128, v);
+                finish_tile<8>(a, wt, bias_smem + e * 128, lane_bias(a, wt.row0, wt.b0, lane), v);
             }
         }
         cluster_sync();  // peers read this CTA's shared memory until here
