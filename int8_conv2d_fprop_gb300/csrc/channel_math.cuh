@@ -99,10 +99,10 @@ __device__ __forceinline__ float rcp_approx(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// |v| held to `to`, max(v, 0): both keep a NaN.
-__device__ __forceinline__ float abs_min(float v, float to) {
+// -|v| held to -16, max(v, 0): both keep a NaN.
+__device__ __forceinline__ float minus_abs16(float v) {
     float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(v)), "f"(to));
+    asm("max.NaN.f32 %0, %1, 0fC1800000;" : "=f"(r) : "f"(-fabsf(v)));
     return r;
 }
 __device__ __forceinline__ float max0(float v) {
@@ -131,26 +131,21 @@ __device__ __forceinline__ Pair gelu_tanh_arg(Pair z) {
     return mul2(z, fma2(z2, pair(-0.102943245f), pair(-2.302208198f)));  // times -log2(e)
 }
 
-// Phi(-x) for x = min(|z|, 16), negated: exp(-x^2/2) times a polynomial of
-// degree 10 fitted to minimise the largest error of the product over
-// [0, 6.5] (weighted least squares on Chebyshev nodes, reweighted towards
-// the maximum): off by 1.2e-7 at most in 32-bit arithmetic, beyond the
-// interval by less still, since the exponential vanishes faster than the
-// polynomial grows.  One exponential and no reciprocal per value.
-__device__ __forceinline__ Pair minus_normal_tail(Pair x, Pair *density) {
-    const Pair e = exp2_2(mul2(mul2(x, x), pair(-0.72134752f)));
-    Pair r = fma2(x, pair(-1.631688633e-06f), pair(3.520776227e-05f));
-    r = fma2(x, r, pair(-3.397382679e-04f));
-    r = fma2(x, r, pair(1.974626677e-03f));
-    r = fma2(x, r, pair(-7.939388976e-03f));
-    r = fma2(x, r, pair(2.431392670e-02f));
-    r = fma2(x, r, pair(-6.115488335e-02f));
-    r = fma2(x, r, pair(1.325137913e-01f));
-    r = fma2(x, r, pair(-2.499167919e-01f));
-    r = fma2(x, r, pair(3.989365101e-01f));
-    r = fma2(x, r, pair(-4.999999404e-01f));
-    *density = e;
-    return mul2(r, e);
+// Phi(x) for x = -min(|z|, 16), as 2^p(x): the logarithm of the normal tail
+// is nearly a parabola, so that a polynomial of degree 6 does (fitted to
+// minimise the largest error of Phi over [-9, 0], by least squares on
+// Chebyshev nodes reweighted towards the maximum): off by 1.4e-7 at most in
+// 32-bit arithmetic, and falling below 2^-126 before x = -16.  One
+// exponential per value and half the instructions of a polynomial times
+// exp(-x^2/2).
+__device__ __forceinline__ Pair normal_tail(Pair x) {
+    Pair p = fma2(x, pair(1.917647205e-05f), pair(6.586165400e-04f));
+    p = fma2(x, p, pair(7.754437625e-03f));
+    p = fma2(x, p, pair(5.296542495e-02f));
+    p = fma2(x, p, pair(-4.590602517e-01f));
+    p = fma2(x, p, pair(1.151122093e+00f));
+    p = fma2(x, p, pair(-9.999997020e-01f));
+    return exp2_2(p);
 }
 
 // Activation of two values, in place.
@@ -159,10 +154,9 @@ __device__ __forceinline__ void activate(float &a, float &b) {
     if constexpr (kAct == CONV_ACT_RELU) {
         a = max0(a), b = max0(b);
     } else if constexpr (kAct == CONV_ACT_GELU) {
-        // z Phi(z) = max(z, 0) - x Phi(-x), x = |z| (0 for z = -inf, its limit)
-        Pair e;
-        const Pair x = pair(abs_min(a, 16.0f), abs_min(b, 16.0f));
-        split(fma2(x, minus_normal_tail(x, &e), pair(max0(a), max0(b))), &a, &b);
+        // z Phi(z) = max(z, 0) + x Phi(x), x = -|z| (0 for z = -inf, its limit)
+        const Pair x = pair(minus_abs16(a), minus_abs16(b));
+        split(fma2(x, normal_tail(x), pair(max0(a), max0(b))), &a, &b);
     } else if constexpr (kAct == CONV_ACT_GELU_TANH) {
         const Pair z = pair(a, b);
         split(mul2(z, logistic_of(gelu_tanh_arg(z))), &a, &b);
@@ -178,21 +172,21 @@ __device__ __forceinline__ void activation_slope(float &a, float &b) {
     if constexpr (kAct == CONV_ACT_RELU) {
         a = a > 0.0f ? 1.0f : 0.0f, b = b > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (kAct == CONV_ACT_GELU) {
-        // Phi(z) + z phi(z), Phi(z) = 1/2 + sign(z) (1/2 - Phi(-x))
-        Pair e;
-        const Pair x = pair(abs_min(a, 16.0f), abs_min(b, 16.0f));
-        float u, v;
-        split(add2(minus_normal_tail(x, &e), pair(0.5f)), &u, &v);
-        const Pair z = pair(copysignf(u, a), copysignf(v, b));
-        split(x, &u, &v);  // (z phi(z) with z held to +-16 as well: phi is 0 there)
-        const Pair zc = pair(copysignf(u, a), copysignf(v, b));
-        split(fma2(mul2(zc, pair(0.39894228f)), e, add2(z, pair(0.5f))), &a, &b);
+        // Phi(z) + z phi(z), Phi(z) = 1/2 + sign(z) (1/2 - Phi(x)), z held
+        // to +-16 in the second term, where phi has vanished
+        const Pair x = pair(minus_abs16(a), minus_abs16(b));
+        const Pair e = exp2_2(mul2(mul2(x, x), pair(-0.72134752f)));
+        float u, v, xa, xb;
+        split(fma2(normal_tail(x), pair(-1.0f), pair(0.5f)), &u, &v);
+        split(x, &xa, &xb);
+        const Pair zc = pair(copysignf(xa, a), copysignf(xb, b));
+        split(fma2(mul2(zc, pair(0.39894228f)), e, add2(pair(copysignf(u, a), copysignf(v, b)), pair(0.5f))), &a, &b);
     } else if constexpr (kAct == CONV_ACT_GELU_TANH) {
         // s + z s (1 - s) (2u)', s = logistic(2u); z held to +-64 in the
         // second term, which has long vanished there, so that no infinity
         // meets its zero
         const Pair s = logistic_of(gelu_tanh_arg(pair(a, b)));
-        const Pair z = pair(copysignf(abs_min(a, 64.0f), a), copysignf(abs_min(b, 64.0f), b));
+        const Pair z = pair(fminf(fmaxf(a, -64.0f), 64.0f), fminf(fmaxf(b, -64.0f), 64.0f));
         const Pair d = mul2(z, fma2(mul2(z, z), pair(0.2140644488f), pair(1.5957691216f)));
         const Pair q = fma2(mul2(s, pair(-1.0f)), s, s);
         split(fma2(d, q, s), &a, &b);

@@ -3,7 +3,7 @@
 //
 // One warp loads 64-element k-steps of both operands with TMA (128-byte
 // swizzle) into a ring, one thread issues tcgen05.mma into one of two
-// accumulators in tensor memory, and eight warps take the other accumulator
+// accumulators in tensor memory, and sixteen warps take the other accumulator
 // through bias, pre-activation, activation and residual to the output.
 // Either operand may have k or its own dim contiguous: only the tensor map,
 // the descriptor strides and the instruction's transpose bits differ, so the
@@ -34,16 +34,17 @@ constexpr int kTileA = 128;        // accumulator lanes of one CTA
 constexpr int kStepK = 64;         // k elements per ring stage: one 128-byte row
 constexpr int kMaxTileB = 256;     // columns of one accumulator
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 384;      // 4 control warps, 8 epilogue warps
-constexpr int kEpilogueWarps = 8;
-constexpr int kStagingBytes = kEpilogueWarps * 4096;
+constexpr int kThreads = 640;      // 4 control warps, 16 epilogue warps
+constexpr int kEpilogueWarps = 16;
+constexpr int kSlotBytes = 2048;   // staging of one epilogue warp
 constexpr int kBiasBytes = kEpilogueWarps * 128;
+constexpr int kRingBytes = 196608;
 constexpr int kMaxSplit = 8;       // portable cluster size
 
 // How an output, residual or pre-activation matrix is walked.
 enum Walk : int32_t {
     kWalkNone = 0,
-    kWalkRows,    // b contiguous, 16-byte aligned rows: vectors, TMA stores
+    kWalkRows,    // b contiguous, 16-byte aligned rows: vectors
     kWalkAlongB,  // lanes along b
     kWalkAlongA,  // lanes along a
 };
@@ -60,10 +61,9 @@ struct ProductArgs {
     Side d, res, pre;
     const void *bias;
     int32_t bias_dtype, bias_along_a;
-    int32_t act;
     int32_t ma, nb;
     int32_t k_steps;
-    int32_t tile_b;              // NT, a multiple of 32
+    int32_t tile_b;              // a multiple of 32
     int32_t tiles_a, tiles_b;
     int32_t a_mn, b_mn;          // operand's own dim (not k) contiguous
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
@@ -105,8 +105,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrival that orders nothing but itself (and, behind tcgen05.fence, the
+// tensor-memory reads): a releasing one would first wait for every global
+// store of the epilogue to be acknowledged.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 2-D load whose completion is counted on a barrier of either CTA of the pair.
@@ -231,168 +234,234 @@ __device__ __forceinline__ void activate_all(float (&v)[W]) {
     for (int j = 0; j < W; j += 2) activate<kAct>(v[j], v[j + 1]);
 }
 
-template <int W>
-__device__ __forceinline__ void activate_runtime(float (&v)[W], int32_t act) {
-    switch (act) {
-        case CONV_ACT_RELU: activate_all<CONV_ACT_RELU>(v); break;
-        case CONV_ACT_GELU: activate_all<CONV_ACT_GELU>(v); break;
-        case CONV_ACT_GELU_TANH: activate_all<CONV_ACT_GELU_TANH>(v); break;
-        case CONV_ACT_SILU: activate_all<CONV_ACT_SILU>(v); break;
-        default: break;
-    }
-}
-
-// One warp's 32 rows x W columns at (row0, b0), lane = row, v = the row's
-// sums.  `stage` is the warp's 4 KB staging buffer, `half` the half of it
-// that the next 16-bit store uses.
+// One warp's 32 rows x up to 32 columns at (row0, b0), lane = row.  The warp
+// owns 2 KB of shared memory, the slot, through which every output, residual
+// and pre-activation is turned: rows of 64 bytes (32 columns of a 16-bit
+// matrix, 16 of a 32-bit one), each lane writing or reading its own row, and
+// runs of a row going to or from global memory.
 struct WarpTile {
-    int32_t row0, b0, rows, cols;  // rows, cols: how many are inside the matrix
-    uint32_t stage;
-    uint32_t half;
-    bool one_store;  // a 32-bit tile takes the whole buffer: one store in flight
+    int32_t row0, b0, rows, cols;  // rows, cols: how many are inside the matrix and the tile
+    uint32_t slot, bias;           // bias: 128 bytes of shared memory
     int lane;
 };
 
-// Own row of a side matrix, W = 32: through the staging buffer when lanes
-// have to run along b.
-__device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, float (&r)[32]) {
-    const int64_t row = t.row0 + t.lane;
-    if (s.walk == kWalkAlongA) {
-        const bool in = t.lane < t.rows;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            r[j] = in && j < t.cols ? load_as_float(s.p, row * s.sa + (int64_t)(t.b0 + j) * s.sb, s.dtype) : 0.0f;
-        return;
-    }
-    // the buffer's earlier stores have to be read out first
-    if (t.lane == 0) ptx::bulk_wait_group_read<0>();
-    __syncwarp();
-    if (s.walk == kWalkRows && t.cols == 32) {
-        const bool wide = s.dtype == CONV_FLOAT32;
-        const int vecs = wide ? 8 : 4, per = wide ? 4 : 8;  // 16-byte vectors per row, elements per vector
-        const int c = t.lane & (vecs - 1);
-        uint4 q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int rr = (t.lane + 32 * i) / vecs;
-            if (i < vecs && rr < t.rows)
-                q[i] = *reinterpret_cast<const uint4 *>((const char *)s.p + ((t.row0 + rr) * s.sa + t.b0 + c * per) *
-                                                                               (wide ? 4 : 2));
-            else
-                q[i] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int rr = (t.lane + 32 * i) / vecs;
-            if (i < vecs)
-                ptx::st_shared_v4(t.stage + (wide ? rr * 128 + ((c ^ (rr & 7)) << 4)
-                                                  : rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4)), q[i]);
-        }
-        __syncwarp();
-        if (wide) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 w = ptx::ld_shared_v4(t.stage + t.lane * 128 + ((i ^ (t.lane & 7)) << 4));
-                r[4 * i] = __uint_as_float(w.x), r[4 * i + 1] = __uint_as_float(w.y);
-                r[4 * i + 2] = __uint_as_float(w.z), r[4 * i + 3] = __uint_as_float(w.w);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 w = ptx::ld_shared_v4(t.stage + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4));
-                unpack8(w, s.dtype, r + 8 * i);
-            }
-        }
-        __syncwarp();
-        return;
-    }
-#pragma unroll 1
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-        float q[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            q[i] = r0 + i < t.rows && t.lane < t.cols
-                       ? load_as_float(s.p, (int64_t)(t.row0 + r0 + i) * s.sa + (int64_t)(t.b0 + t.lane) * s.sb, s.dtype)
-                       : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            ptx::st_shared_b32(t.stage + ((r0 + i) * 32 + (t.lane ^ (r0 + i))) * 4, __float_as_uint(q[i]));
-    }
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        r[j] = __uint_as_float(ptx::ld_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4));
-    __syncwarp();
+// 16-byte piece i of a slot row, the pieces exchanged so that neither walk
+// meets a bank twice; element c of a slot row.
+__device__ __forceinline__ uint32_t piece(uint32_t slot, uint32_t row, uint32_t i) {
+    return slot + row * 64 + ((i ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t at16(uint32_t slot, uint32_t row, uint32_t c) { return piece(slot, row, c >> 3) + (c & 7) * 2; }
+__device__ __forceinline__ uint32_t at32(uint32_t slot, uint32_t row, uint32_t c) { return piece(slot, row, c >> 2) + (c & 3) * 4; }
+
+__device__ __forceinline__ uint16_t ld_shared_b16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_shared_b16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-__device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *map, WarpTile &t, const float (&v)[32]) {
-    const int64_t row = t.row0 + t.lane;
-    if (s.walk == kWalkAlongA) {
-        if (t.lane < t.rows) {
+// Rows of a side matrix with aligned rows to the slot: 64-byte runs, eight
+// rows per access.  p: the first row's 64 bytes.
+__device__ __forceinline__ void rows_to_slot(const WarpTile &t, const char *p, int64_t row_bytes) {
+    p += (int64_t)(t.lane / 4) * row_bytes + (t.lane & 3) * 16;
+    uint4 q[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < t.cols) store_from_float(s.p, row * s.sa + (int64_t)(t.b0 + j) * s.sb, s.dtype, v[j]);
+    for (int i = 0; i < 4; ++i) {
+        q[i] = t.lane / 4 + 8 * i < t.rows ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        p += 8 * row_bytes;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane / 4 + 8 * i, t.lane & 3), q[i]);
+}
+
+// The same for any strides, an element at a time, `cols` columns from column
+// b0 + c on: lanes along the rows, or along the columns (32 of 16 bits, or 16
+// of 32 bits and two rows).
+__device__ __noinline__ void slot_to_any(Side s, WarpTile t, int c, int cols) {
+    const bool wide = s.dtype == CONV_FLOAT32;
+    if (s.walk == kWalkAlongA) {
+        const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)(t.b0 + c) * s.sb;
+        if (t.lane < t.rows)
+            for (int j = 0; j < cols; ++j) {
+                if (wide) ((uint32_t *)s.p)[at + j * s.sb] = ptx::ld_shared_b32(at32(t.slot, t.lane, j));
+                else ((uint16_t *)s.p)[at + j * s.sb] = ld_shared_b16(at16(t.slot, t.lane, j));
+            }
+        return;
+    }
+    const int col = wide ? t.lane & 15 : t.lane, first = wide ? t.lane >> 4 : 0, step = wide ? 2 : 1;
+    const int64_t at = (int64_t)t.row0 * s.sa + (int64_t)(t.b0 + c + col) * s.sb;
+    if (col < cols) {
+#pragma unroll 4
+        for (int r = first; r < t.rows; r += step) {
+            if (wide) ((uint32_t *)s.p)[at + r * s.sa] = ptx::ld_shared_b32(at32(t.slot, r, col));
+            else ((uint16_t *)s.p)[at + r * s.sa] = ld_shared_b16(at16(t.slot, r, col));
+        }
+    }
+}
+__device__ __noinline__ void any_to_slot(Side s, WarpTile t, int c, int cols) {
+    const bool wide = s.dtype == CONV_FLOAT32;
+    if (s.walk == kWalkAlongA) {
+        const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)(t.b0 + c) * s.sb;
+        if (t.lane < t.rows) {
+#pragma unroll 8
+            for (int j = 0; j < cols; ++j) {
+                if (wide) ptx::st_shared_b32(at32(t.slot, t.lane, j), ((const uint32_t *)s.p)[at + j * s.sb]);
+                else st_shared_b16(at16(t.slot, t.lane, j), ((const uint16_t *)s.p)[at + j * s.sb]);
+            }
         }
         return;
     }
-    if (s.walk == kWalkRows) {
-        // staged in the map's swizzle and stored by TMA, which clips to the
-        // matrix; 16-bit tiles alternate between the halves of the buffer
-        const bool wide = s.dtype == CONV_FLOAT32;
-        uint32_t buf = t.stage;
-        if (wide) {
-            if (t.lane == 0) ptx::bulk_wait_group_read<0>();
-        } else {
-            buf += t.half * 2048;
-            t.half ^= 1u;
-            if (t.lane == 0) {
-                if (t.one_store) ptx::bulk_wait_group_read<0>();
-                else ptx::bulk_wait_group_read<1>();
-            }
-        }
-        __syncwarp();
-        if (wide) {
+    const int col = wide ? t.lane & 15 : t.lane, first = wide ? t.lane >> 4 : 0, step = wide ? 2 : 1;
+    const int64_t at = (int64_t)t.row0 * s.sa + (int64_t)(t.b0 + c + col) * s.sb;
+    if (col < cols) {
+#pragma unroll 1
+        for (int r = first; r < t.rows; r += 8 * step) {
+            // (eight loads in flight)
+            uint32_t q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                ptx::st_shared_v4(buf + t.lane * 128 + ((i ^ (t.lane & 7)) << 4),
-                                  make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
-        } else {
+                if (r + i * step < t.rows)
+                    q[i] = wide ? ((const uint32_t *)s.p)[at + (r + i * step) * s.sa]
+                                : ((const uint16_t *)s.p)[at + (r + i * step) * s.sa];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                ptx::st_shared_v4(buf + t.lane * 64 + ((i ^ ((t.lane >> 1) & 3)) << 4),
-                                  pack8(v + 8 * i, s.dtype));
+            for (int i = 0; i < 8; ++i)
+                if (r + i * step < t.rows) {
+                    if (wide) ptx::st_shared_b32(at32(t.slot, r + i * step, col), q[i]);
+                    else st_shared_b16(at16(t.slot, r + i * step, col), (uint16_t)q[i]);
+                }
         }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (t.lane == 0) {
-            ptx::tma_store_2d(map, t.b0, t.row0, buf);
-            ptx::bulk_commit_group();
+    }
+}
+
+// The slot to `map`'s matrix by TMA, and the wait before the slot is used again.
+__device__ __forceinline__ void send_slot(const CUtensorMap *map, const WarpTile &t, int c) {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (t.lane == 0) {
+        ptx::tma_store_2d(map, t.b0 + c, t.row0, t.slot);
+        ptx::bulk_commit_group();
+    }
+}
+__device__ __forceinline__ void free_slot(const WarpTile &t) {
+    if (t.lane == 0) ptx::bulk_wait_group_read<0>();
+    __syncwarp();
+}
+
+__device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *map, const WarpTile &t, const float (&v)[32]) {
+    const bool rows = s.walk == kWalkRows && t.cols == 32;
+    if (s.dtype != CONV_FLOAT32) {
+        free_slot(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane, i), pack8(v + 8 * i, s.dtype));
+        if (rows) {
+            send_slot(map, t, 0);
+        } else {
+            __syncwarp();
+            slot_to_any(s, t, 0, t.cols);
         }
         return;
     }
-    if (t.lane == 0) ptx::bulk_wait_group_read<0>();
-    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) ptx::st_shared_b32(t.stage + (t.lane * 32 + (j ^ t.lane)) * 4, __float_as_uint(v[j]));
-    __syncwarp();
-    if (t.lane < t.cols)
-#pragma unroll 8
-        for (int rr = 0; rr < t.rows; ++rr)
-            store_from_float(s.p, (int64_t)(t.row0 + rr) * s.sa + (int64_t)(t.b0 + t.lane) * s.sb, s.dtype,
-                             __uint_as_float(ptx::ld_shared_b32(t.stage + (rr * 32 + (t.lane ^ rr)) * 4)));
-    __syncwarp();
+    for (int c = 0; c < 32; c += 16) {
+        free_slot(t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            ptx::st_shared_v4(piece(t.slot, t.lane, i),
+                              make_uint4(__float_as_uint(v[c + 4 * i]), __float_as_uint(v[c + 4 * i + 1]),
+                                         __float_as_uint(v[c + 4 * i + 2]), __float_as_uint(v[c + 4 * i + 3])));
+        if (rows) {
+            send_slot(map, t, c);
+            continue;
+        }
+        __syncwarp();
+        if (c < t.cols) slot_to_any(s, t, c, min(16, t.cols - c));
+    }
 }
 
-// The same for 8 columns of a split tile: every lane on its own row.
-__device__ __forceinline__ void load_side(const Side &s, const WarpTile &t, float (&r)[8]) {
-    const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)t.b0 * s.sb;
-    const bool in = t.lane < t.rows;
+// (Slot elements outside the matrix are whatever they were: they are added
+// to sums that are not stored.)
+__device__ __forceinline__ void add_chunk(const Side &s, const WarpTile &t, float (&v)[32]) {
+    const bool rows = s.walk == kWalkRows && t.cols == 32;
+    if (s.dtype != CONV_FLOAT32) {
+        free_slot(t);
+        if (rows) rows_to_slot(t, (const char *)s.p + ((int64_t)t.row0 * s.sa + t.b0) * 2, s.sa * 2);
+        else any_to_slot(s, t, 0, t.cols);
+        __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = in && j < t.cols ? load_as_float(s.p, at + j * s.sb, s.dtype) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            float r[8];
+            unpack8(ptx::ld_shared_v4(piece(t.slot, t.lane, i)), s.dtype, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+        free_slot(t);
+        if (rows) rows_to_slot(t, (const char *)s.p + ((int64_t)t.row0 * s.sa + t.b0 + c) * 4, s.sa * 4);
+        else if (c < t.cols) any_to_slot(s, t, c, min(16, t.cols - c));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 q = ptx::ld_shared_v4(piece(t.slot, t.lane, i));
+            v[c + 4 * i] += __uint_as_float(q.x), v[c + 4 * i + 1] += __uint_as_float(q.y);
+            v[c + 4 * i + 2] += __uint_as_float(q.z), v[c + 4 * i + 3] += __uint_as_float(q.w);
+        }
+    }
 }
 
-__device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *, WarpTile &t, const float (&v)[8]) {
+// The lane's bias: of its row, or of column b0 + lane for the others to share.
+__device__ __forceinline__ float lane_bias(const ProductArgs &a, int row0, int b0, int lane) {
+    if (!a.bias) return 0.0f;
+    const int at = (a.bias_along_a ? row0 : b0) + lane;
+    return at < (a.bias_along_a ? a.ma : a.nb) ? load_as_float(a.bias, at, a.bias_dtype) : 0.0f;
+}
+
+template <int W>
+__device__ __forceinline__ void add_bias(const ProductArgs &a, const WarpTile &t, float bias, float (&v)[W]) {
+    if (!a.bias) return;
+    if (a.bias_along_a) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += bias;
+        return;
+    }
+    // lane j's bias to every row, through 128 bytes of shared memory
+    __syncwarp();
+    ptx::st_shared_b32(t.bias + t.lane * 4, __float_as_uint(bias));
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < W; j += 4) {
+        const uint4 b = ptx::ld_shared_v4(t.bias + j * 4);
+        split(add2(pair(v[j], v[j + 1]), pair(__uint_as_float(b.x), __uint_as_float(b.y))), &v[j], &v[j + 1]);
+        split(add2(pair(v[j + 2], v[j + 3]), pair(__uint_as_float(b.z), __uint_as_float(b.w))), &v[j + 2], &v[j + 3]);
+    }
+}
+
+__device__ __forceinline__ void load_sums(uint32_t acc, float (&v)[32]) {
+    uint32_t u[32];
+    ptx::tmem_ld_32x32b_x32(acc, u);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+}
+
+// 32 rows x 32 columns of sums at `acc` in tensor memory.
+template <int kAct>
+__device__ __forceinline__ void finish_chunk(const ProductArgs &a, const WarpTile &t, uint32_t acc, float bias) {
+    float v[32];
+    load_sums(acc, v);
+    add_bias(a, t, bias, v);
+    if (a.pre.walk) store_chunk(a.pre, &a.map_pre, t, v);
+    activate_all<kAct>(v);
+    if (a.res.walk) add_chunk(a.res, t, v);
+    store_chunk(a.d, &a.map_d, t, v);
+}
+
+// 8 columns of a split tile: every lane on its own row.
+__device__ __forceinline__ void store8(const Side &s, const WarpTile &t, const float (&v)[8]) {
     if (t.lane >= t.rows) return;
     const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)t.b0 * s.sb;
     if (s.walk == kWalkRows && t.cols == 8) {
@@ -410,41 +479,23 @@ __device__ __forceinline__ void store_side(const Side &s, const CUtensorMap *, W
         if (j < t.cols) store_from_float(s.p, at + j * s.sb, s.dtype, v[j]);
 }
 
-// The lane's bias: of its row, or of column b0 + lane for the others to share.
-__device__ __forceinline__ float lane_bias(const ProductArgs &a, int row0, int b0, int lane) {
-    if (!a.bias) return 0.0f;
-    const int at = (a.bias_along_a ? row0 : b0) + lane;
-    return at < (a.bias_along_a ? a.ma : a.nb) ? load_as_float(a.bias, at, a.bias_dtype) : 0.0f;
-}
-
-template <int W>
-__device__ __forceinline__ void finish_tile(const ProductArgs &a, WarpTile &t, uint32_t bias_smem, float b, float (&v)[W]) {
-    if (a.bias) {
-        if (a.bias_along_a) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) v[j] += b;
-        } else {
-            // lane j's bias to every row, through 128 bytes of shared memory
-            __syncwarp();
-            ptx::st_shared_b32(bias_smem + t.lane * 4, __float_as_uint(b));
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < W; j += 4) {
-                const uint4 b = ptx::ld_shared_v4(bias_smem + j * 4);
-                v[j] += __uint_as_float(b.x), v[j + 1] += __uint_as_float(b.y);
-                v[j + 2] += __uint_as_float(b.z), v[j + 3] += __uint_as_float(b.w);
-            }
-        }
-    }
-    if (a.pre.walk) store_side(a.pre, &a.map_pre, t, v);
-    activate_runtime(v, a.act);
+template <int kAct>
+__device__ __forceinline__ void finish8(const ProductArgs &a, const WarpTile &t, float (&v)[8]) {
+    float r[8];
     if (a.res.walk) {
-        float r[W];
-        load_side(a.res, t, r);
+        const int64_t at = (int64_t)(t.row0 + t.lane) * a.res.sa + (int64_t)t.b0 * a.res.sb;
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] += r[j];
+        for (int j = 0; j < 8; ++j)
+            r[j] = t.lane < t.rows && j < t.cols ? load_as_float(a.res.p, at + j * a.res.sb, a.res.dtype) : 0.0f;
     }
-    store_side(a.d, &a.map_d, t, v);
+    add_bias(a, t, lane_bias(a, t.row0, t.b0, t.lane), v);
+    if (a.pre.walk) store8(a.pre, t, v);
+    activate_all<kAct>(v);
+    if (a.res.walk) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+    }
+    store8(a.d, t, v);
 }
 
 // ---------------------------------------------------------------- kernel
@@ -454,14 +505,17 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &a, WarpTile &t, u
 // 128 x tile_b, or `split` CTAs of a cluster that each sum part of k and
 // then add their partial tiles through distributed shared memory, in order
 // of rank.
-template <bool kPair>
+template <bool kPair, int kAct>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t ring = ptx::smem_addr(smem);
     const uint32_t staging = ring + a.stages * a.stage_bytes;
-    const uint32_t bias_smem = staging + kStagingBytes;
-    SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + a.stages * a.stage_bytes + kStagingBytes + kBiasBytes);
+    const uint32_t bias_smem = staging + kEpilogueWarps * kSlotBytes;
+    SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + (bias_smem - ring) + kBiasBytes);
+    if (ring & 1023) {  // the swizzles count on it (true of every launch without static shared memory)
+        if (threadIdx.x == 0) atomicExch(a.status, (int)CONV_ERR_ALIGNMENT);
+        return;
+    }
     volatile int32_t *abort_flag = &ctl->abort_flag;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -585,10 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int e = warp - 4, quad = warp & 3, part = e >> 2;
         WarpTile wt;
         wt.lane = lane;
-        wt.stage = staging + e * 4096;
-        wt.half = 0;
-        wt.one_store = a.d.dtype == CONV_FLOAT32;
-        const uint32_t my_bias = bias_smem + e * 128;
+        wt.slot = staging + e * kSlotBytes;
+        wt.bias = bias_smem + e * 128;
         int n = 0;
         for (int t = first; t < tiles; t += step, ++n) {
             int ia, ib;
@@ -596,16 +648,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int slot = n & 1;
             const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
             // this warp's biases, loaded while the tile is being summed
-            float bias[kMaxTileB / 64];
+            float bias[2];
 #pragma unroll
-            for (int i = 0; i < kMaxTileB / 64; ++i)
-                bias[i] = part * 32 + i * 64 < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + part * 32 + i * 64, lane) : 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                const int c = (part + 4 * i) * 32;
+                bias[i] = c < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + c, lane) : 0.0f;
+            }
             if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
             if (k_lo == k_hi) {  // no products: the accumulator was never written
                 const uint32_t zero[32] = {};
-                for (int c = part * 32; c < a.tile_b; c += 64) ptx::tmem_st_32x32b_x32(acc + c, zero);
+                for (int c = part * 32; c < a.tile_b; c += 128) ptx::tmem_st_32x32b_x32(acc + c, zero);
                 ptx::tmem_st_wait();
             }
             wt.row0 = row0;
@@ -613,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (!kPair && a.split > 1) {
                 // partial sums to shared memory [column][row], over the
                 // ring: its loads and MMAs are done
-                for (int c = part * 32; c < a.tile_b; c += 64) {
+                for (int c = part * 32; c < a.tile_b; c += 128) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(acc + c, v);
                     ptx::tmem_ld_wait();
@@ -623,27 +677,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 }
                 break;  // one tile per cluster; the rest follows the cluster barrier
             }
-#pragma unroll
-            for (int i = 0; i < kMaxTileB / 64; ++i) {
-                const int c = part * 32 + i * 64;
-                if (c >= a.tile_b) break;
-                uint32_t u[32];
-                ptx::tmem_ld_32x32b_x32(acc + c, u);
-                ptx::tmem_ld_wait();
+#pragma unroll 1
+            for (int c = part * 32; c < a.tile_b; c += 128) {
                 wt.b0 = ib * a.tile_b + c;
                 wt.cols = min(32, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
-                float v[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-                finish_tile<32>(a, wt, my_bias, bias[i], v);
+                finish_chunk<kAct>(a, wt, acc + c, c < 128 ? bias[0] : bias[1]);
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
-                if (kPair) mbar_arrive_cluster(map_to_rank(bar, 0));
-                else ptx::mbar_arrive(bar);
+                mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
             }
         }
         if (lane == 0) ptx::bulk_wait_group_read<0>();
@@ -659,9 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int e = warp - 4;
             WarpTile wt;
             wt.lane = lane;
-            wt.stage = 0;
-            wt.half = 0;
-            wt.one_store = false;
+            wt.slot = 0;  // (unused by 8-column tiles)
+            wt.bias = bias_smem + e * 128;
             const int units = a.tile_b / 8 * 4;
             for (int u = e * a.split + (int)rank; u < units; u += kEpilogueWarps * a.split) {
                 const int quad = u & 3, c = (u >> 2) * 8;
@@ -676,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] += ld_cluster_f32(src + j * kTileA * 4);
                 }
-                finish_tile<8>(a, wt, bias_smem + e * 128, lane_bias(a, wt.row0, wt.b0, lane), v);
+                finish8<kAct>(a, wt, v);
             }
         }
         cluster_sync();  // peers read this CTA's shared memory until here
@@ -721,16 +765,13 @@ bool encode(CUtensorMap *m, int32_t dtype, const void *p, int64_t inner, int64_t
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// TMA strides are below 2^40 bytes.
-bool map_stride_ok(int64_t stride_elems, int64_t size) { return stride_elems * size < ((int64_t)1 << 40); }
-
 Side make_side(const void *p, int64_t sa, int64_t sb, int32_t dtype, int64_t ma, int64_t nb) {
     Side s{const_cast<void *>(p), sa, sb, dtype, kWalkNone};
     if (!p) return s;
     const int64_t size = channel_elem_size(dtype);
     // (TMA stores clip to the matrix in units of 16 bytes: rows of other
     // lengths would be written past their end)
-    if ((sb == 1 || nb == 1) && (nb * size) % 16 == 0 && (sa * size) % 16 == 0 && (uintptr_t)p % 16 == 0 && map_stride_ok(sa, size))
+    if ((sb == 1 || nb == 1) && (nb * size) % 16 == 0 && (sa * size) % 16 == 0 && (uintptr_t)p % 16 == 0)
         s.walk = kWalkRows;
     else if (nb > 1 && (ma == 1 || sb <= sa))
         s.walk = kWalkAlongB;
@@ -764,7 +805,6 @@ conv_status product_launch(const Product &given, void *stream) {
     a.res = make_side(pr.res, pr.res_sa, pr.res_sb, pr.d_dtype, pr.ma, pr.nb);
     a.pre = make_side(pr.pre, pr.pre_sa, pr.pre_sb, pr.in_dtype, pr.ma, pr.nb);
     a.bias = pr.bias, a.bias_dtype = pr.bias_dtype, a.bias_along_a = pr.bias_along_a;
-    a.act = pr.act;
     a.wait_limit_ns = wait_limit_ns();
     a.status = device_status_word();
     if (!a.status) return CONV_ERR_CUDA;
@@ -809,7 +849,7 @@ conv_status product_launch(const Product &given, void *stream) {
     }
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
     a.stage_bytes = 16384 + (int32_t)round_up(a.b_mn ? a.b_boxes * 8192 : a.b_rows * 128, 1024);
-    a.stages = std::min(kMaxStages, 196608 / a.stage_bytes);
+    a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
     const int tile_a = pair ? 256 : 128;
     a.idesc = (1u << 4) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 7) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 10) |
               ((a.a_mn ? 1u : 0u) << 15) | ((a.b_mn ? 1u : 0u) << 16) | ((uint32_t)(a.tile_b >> 3) << 17) |
@@ -825,19 +865,26 @@ conv_status product_launch(const Product &given, void *stream) {
     }
     for (auto [s, m] : {std::pair<Side *, CUtensorMap *>{&a.d, &a.map_d}, {&a.pre, &a.map_pre}})
         if (s->walk == kWalkRows &&
-            !encode(m, s->dtype, s->p, pr.nb, pr.ma, s->sa, 32, 32,
-                    s->dtype == CONV_FLOAT32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            !encode(m, s->dtype, s->p, pr.nb, pr.ma, s->sa, s->dtype == CONV_FLOAT32 ? 16 : 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_64B))
             return CONV_ERR_CUDA;
 
-    const size_t smem = 1024 + (size_t)a.stages * a.stage_bytes + kStagingBytes + kBiasBytes + sizeof(SharedCtl);
-    auto kernel = pair ? product_kernel<true> : product_kernel<false>;
-    static std::atomic<bool> ready[64][2];  // (check_device admits 64 devices)
+    const size_t smem = (size_t)a.stages * a.stage_bytes + kEpilogueWarps * kSlotBytes + kBiasBytes + sizeof(SharedCtl);
+    // the kernel with the call's activation, for CTA pairs or single CTAs
+    typedef void (*Kernel)(ProductArgs);
+    static const Kernel kernels[2][5] = {
+        {product_kernel<false, CONV_ACT_NONE>, product_kernel<false, CONV_ACT_RELU>, product_kernel<false, CONV_ACT_GELU>,
+         product_kernel<false, CONV_ACT_GELU_TANH>, product_kernel<false, CONV_ACT_SILU>},
+        {product_kernel<true, CONV_ACT_NONE>, product_kernel<true, CONV_ACT_RELU>, product_kernel<true, CONV_ACT_GELU>,
+         product_kernel<true, CONV_ACT_GELU_TANH>, product_kernel<true, CONV_ACT_SILU>}};
+    const Kernel kernel = kernels[pair][pr.act];
+    static std::atomic<bool> ready[64][2][5];  // (check_device admits 64 devices)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CONV_ERR_CUDA;
-    if (!ready[dev][pair].load()) {
+    if (!ready[dev][pair][pr.act].load()) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess)
             return CONV_ERR_CUDA;
-        ready[dev][pair].store(true);
+        ready[dev][pair][pr.act].store(true);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
