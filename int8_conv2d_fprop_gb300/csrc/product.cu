@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         ptx::prefetch_tensormap(&a.map_a);
         ptx::prefetch_tensormap(&a.map_b);
         for (int i = 0; i < a.stages; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
             ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -553,17 +553,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
 
-    if (warp == 0 && lane == 0) {
-        // ------------------------------------------------ loads
+    if ((warp == 0 || warp == 3) && lane == 0) {
+        // ------------------------------------------------ loads: operand A by
+        // warp 0, operand B by warp 3 (one thread issuing for both fell behind
+        // the MMAs where an operand takes two boxes per k-step)
+        const bool is_b = warp == 3;
+        const bool mn = is_b ? a.b_mn : a.a_mn;
+        const CUtensorMap *map = is_b ? &a.map_b : &a.map_a;
+        const int boxes = is_b ? a.b_boxes : 2;
+        const uint32_t bytes = (kPair ? 2u : 1u) * (mn ? boxes * 8192u : is_b ? a.b_rows * 128u : 16384u);
         Ring rg;
         int64_t issued = 0;
         bool ok = true;
-        const uint32_t bytes = (kPair ? 2u : 1u) * (16384u + (a.b_mn ? a.b_boxes * 8192u : a.b_rows * 128u));
         for (int t = first; t < tiles && ok; t += step) {
             int ia, ib;
             tile_at(a, t, &ia, &ib);
-            const int a0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0);
-            const int b0 = ib * a.tile_b + (kPair ? rank * a.b_rows : 0);
+            const int own = is_b ? ib * a.tile_b + (kPair ? rank * a.b_rows : 0)
+                                 : ia * kRowsPerTile + (kPair ? rank * kTileA : 0);
             for (int ks = k_lo; ks < k_hi; ++ks) {
                 if (!wait_phase(ptx::smem_addr(&ctl->empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
                     ok = false;
@@ -572,22 +578,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]);
                 if (!kPair || rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
                 if (kPair) bar = map_to_rank(bar, 0);
-                const uint32_t sa = ring + rg.idx * a.stage_bytes, sb = sa + 16384;
+                const uint32_t dst = ring + rg.idx * a.stage_bytes + (is_b ? 16384 : 0);
                 const int k0 = ks * kStepK;
-                auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
-                    if constexpr (kPair) tma_load_2d_pair(dst, m, x, y, bar);
-                    else ptx::tma_load_2d(dst, m, x, y, bar);
+                auto load = [&](uint32_t to, int x, int y) {
+                    if constexpr (kPair) tma_load_2d_pair(to, map, x, y, bar);
+                    else ptx::tma_load_2d(to, map, x, y, bar);
                 };
-                if (a.a_mn) {
-                    load(sa, &a.map_a, a0, k0);
-                    load(sa + 8192, &a.map_a, a0 + 64, k0);
+                if (mn) {
+                    for (int i = 0; i < boxes; ++i) load(dst + i * 8192, own + 64 * i, k0);
                 } else {
-                    load(sa, &a.map_a, k0, a0);
-                }
-                if (a.b_mn) {
-                    for (int i = 0; i < a.b_boxes; ++i) load(sb + i * 8192, &a.map_b, b0 + 64 * i, k0);
-                } else {
-                    load(sb, &a.map_b, k0, b0);
+                    load(dst, k0, own);
                 }
                 ++issued;
                 rg.next(a.stages);
