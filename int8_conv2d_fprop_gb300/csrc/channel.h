@@ -72,6 +72,21 @@ struct Product {
 // elements, the address 16-byte aligned.  (Strides of extents of 1 are 0.)
 bool product_in_place(const void *p, int64_t rows, int64_t rs, int64_t cols, int64_t cs);
 
-conv_status product_launch(const Product &pr, void *stream);
+// Tile shape and split of a product of these extents; part_bytes of workspace
+// hold its partial sums.
+struct ProductPlan {
+    bool swap = false;     // a and b exchanged
+    bool pair = false;     // tiles of CTA pairs (256 rows), else of one CTA (128)
+    int32_t tile_b = 0;
+    int64_t tiles_a = 0, tiles_b = 0;
+    int32_t split = 1;     // CTAs of a cluster that share a tile along k
+    int32_t parts = 1;     // runs of k summed apart and joined by a second kernel
+    size_t part_bytes = 0; // a multiple of 256
+};
+
+ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k);
+
+// workspace: part_bytes of the plan.
+conv_status product_launch(const Product &pr, void *workspace, void *stream);
 
 }  // namespace i8c

@@ -113,6 +113,7 @@ conv_status check_workspace(const void *workspace, size_t have, size_t need) {
 
 struct LinearPlan {
     Packed x, w;
+    size_t part_off = 0;  // partial sums of the product
     size_t bytes = 0;
 };
 
@@ -120,6 +121,8 @@ LinearPlan plan_linear(const conv_matrix_desc *x, const void *x_dev, const conv_
     LinearPlan pl;
     plan_pack(x, x_dev, &pl.bytes, &pl.x);
     plan_pack(w, w_dev, &pl.bytes, &pl.w);
+    pl.part_off = pl.bytes;
+    if (x->rows > 0 && w->rows > 0) pl.bytes += product_plan(x->rows, w->rows, x->cols).part_bytes;
     return pl;
 }
 
@@ -240,7 +243,8 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int
 
 struct GradPlan {
     bool dz = false;  // dz is made in the workspace
-    size_t dz_off = 0, part_off = 0;
+    size_t dz_off = 0, part_off = 0;  // part: column sums of dz
+    size_t sums_off = 0;              // partial sums of the products, one after the other
     int64_t dz_ld = 0, parts = 0, rows_per_part = 0;
     Packed x, w;
     size_t bytes = 0;
@@ -267,6 +271,13 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
     }
     plan_pack(x, x_dev, &pl.bytes, &pl.x);
     plan_pack(w, w_dev, &pl.bytes, &pl.w);
+    pl.sums_off = pl.bytes;
+    if (x->cols > 0) {
+        size_t dx = 0, dw = 0;
+        if (m > 0) dx = product_plan(m, x->cols, n).part_bytes;
+        if (n > 0) dw = product_plan(n, x->cols, m).part_bytes;
+        pl.bytes += std::max(dx, dw);
+    }
     return pl;
 }
 
@@ -368,7 +379,7 @@ conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv
     pr.pre = preact ? preact_dev : nullptr, pr.pre_sa = zr.rs, pr.pre_sb = zr.cs;
     pr.bias = bias_dev, pr.bias_dtype = p->bias_dtype;
     pr.act = p->activation;
-    return product_launch(pr, stream);
+    return product_launch(pr, (char *)workspace + pl.part_off, stream);
 }
 
 conv_status conv_linear_grad_workspace_size(const conv_matrix_desc *dy, const void *dy_dev,
@@ -456,7 +467,7 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         pr.in_dtype = x->dtype;
         const MatRef o = mat_ref(dx, dx_dev);
         pr.d = dx_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dx->dtype;
-        if ((st = product_launch(pr, stream))) return st;
+        if ((st = product_launch(pr, (char *)workspace + pl.sums_off, stream))) return st;
     }
     if (dw && n > 0 && k > 0) {
         MatRef xr;
@@ -468,7 +479,7 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         pr.in_dtype = x->dtype;
         const MatRef o = mat_ref(dw, dw_dev);
         pr.d = dw_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dw->dtype;
-        if ((st = product_launch(pr, stream))) return st;
+        if ((st = product_launch(pr, (char *)workspace + pl.sums_off, stream))) return st;
     }
     return CONV_OK;
 }

@@ -16,6 +16,7 @@
 #include <atomic>
 
 #include "channel.h"
+#include "channel_launch.cuh"
 #include "channel_math.cuh"
 #include "tc_ptx.cuh"
 
@@ -69,6 +70,8 @@ struct ProductArgs {
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
+    int32_t parts;               // runs of k, each summed to `part` (1: none)
+    float *part;                 // [run][tile][128-row half][column][row of 128]
     uint32_t idesc;
     uint64_t wait_limit_ns;
     int *status;
@@ -522,13 +525,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint32_t rank = (kPair || a.split > 1) ? cluster_rank() : 0;
     const int cluster_size = kPair ? 2 : a.split;
     const int first = blockIdx.x / cluster_size, step = gridDim.x / cluster_size;
-    const int tiles = a.tiles_a * a.tiles_b;
+    const int tiles = a.tiles_a * a.tiles_b, units = tiles * a.parts;
     constexpr int kRowsPerTile = kPair ? 2 * kTileA : kTileA;
     int k_lo = 0, k_hi = a.k_steps;
     if (!kPair && a.split > 1) {
         k_lo = (int)((int64_t)a.k_steps * rank / a.split);
         k_hi = (int)((int64_t)a.k_steps * (rank + 1) / a.split);
     }
+
+    // unit u: tile u mod tiles of run u / tiles (the runs of one stretch of k
+    // work side by side, on the same rows of the operands)
+    auto run_of = [&](int u) {
+        if (a.parts > 1) {
+            const int p = u / tiles;
+            k_lo = (int)((int64_t)a.k_steps * p / a.parts);
+            k_hi = (int)((int64_t)a.k_steps * (p + 1) / a.parts);
+            u -= p * tiles;
+        }
+        return u;
+    };
 
     if (threadIdx.x == 0) {
         ptx::prefetch_tensormap(&a.map_a);
@@ -565,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         Ring rg;
         int64_t issued = 0;
         bool ok = true;
-        for (int t = first; t < tiles && ok; t += step) {
+        for (int t = first; t < units && ok; t += step) {
             int ia, ib;
-            tile_at(a, t, &ia, &ib);
+            tile_at(a, run_of(t), &ia, &ib);
             const int own = is_b ? ib * a.tile_b + (kPair ? rank * a.b_rows : 0)
                                  : ia * kRowsPerTile + (kPair ? rank * kTileA : 0);
             for (int ks = k_lo; ks < k_hi; ++ks) {
@@ -613,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         int n = 0;
         bool ok = true;
         const uint32_t adv_a = a.a_mn ? 2048 >> 4 : 32 >> 4, adv_b = a.b_mn ? 2048 >> 4 : 32 >> 4;
-        for (int t = first; t < tiles && ok; t += step, ++n) {
+        for (int t = first; t < units && ok; t += step, ++n) {
             const int slot = n & 1;
+            run_of(t);
             if (!wait_phase(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status)) break;
             ptx::tc_fence_after();
             const uint32_t d = tmem + slot * kMaxTileB;
@@ -642,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         wt.slot = staging + e * kSlotBytes;
         wt.bias = bias_smem + e * 128;
         int n = 0;
-        for (int t = first; t < tiles; t += step, ++n) {
+        for (int t = first; t < units; t += step, ++n) {
             int ia, ib;
-            tile_at(a, t, &ia, &ib);
+            tile_at(a, run_of(t), &ia, &ib);
             const int slot = n & 1;
             const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
             // this warp's biases, loaded while the tile is being summed
@@ -682,6 +698,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 wt.b0 = ib * a.tile_b + c;
                 wt.cols = min(32, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
+                if (a.parts > 1) {
+                    float v[32];
+                    load_sums(acc + c, v);
+                    float *p = a.part + (((int64_t)t * (kPair ? 2 : 1) + (kPair ? rank : 0)) * a.tile_b + c) * kTileA + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
+                    continue;
+                }
                 finish_chunk<kAct>(a, wt, acc + c, c < 128 ? bias[0] : bias[1]);
             }
             ptx::tc_fence_before();
@@ -731,6 +755,47 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     ptx::tc_fence_after();
     if (warp == 2) tmem_dealloc<kPair>(tmem, 512);
+}
+
+// Adds the runs' partial sums, in their order, and finishes the product:
+// 32 rows x 8 columns per warp, lane = row.
+template <int kAct>
+__global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant__ ProductArgs a, int rows_per_tile) {
+    __shared__ __align__(16) float bias[8][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int tiles = a.tiles_a * a.tiles_b;
+    // unit: 8 columns of 32 rows, columns fastest
+    const int per_half = a.tile_b / 8 * 4, halves = rows_per_tile / kTileA;
+    const int u = blockIdx.x * 8 + warp;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    if (u >= tiles * halves * per_half) return;
+    const int th = u / per_half, in = u - th * per_half;
+    const int quad = in / (a.tile_b / 8), c = (in - quad * (a.tile_b / 8)) * 8;
+    const int t = th / halves, half = th - t * halves;
+    int ia, ib;
+    tile_at(a, t, &ia, &ib);
+    WarpTile wt;
+    wt.lane = lane;
+    wt.slot = 0;  // (unused by 8-column tiles)
+    wt.bias = ptx::smem_addr(bias[warp]);
+    wt.row0 = ia * rows_per_tile + half * kTileA + quad * 32;
+    wt.rows = min(32, a.ma - wt.row0);
+    wt.b0 = ib * a.tile_b + c;
+    wt.cols = min(8, a.nb - wt.b0);
+    if (wt.rows <= 0 || wt.cols <= 0) return;
+    const float *p = a.part + ((int64_t)th * a.tile_b + c) * kTileA + quad * 32 + lane;
+    const int64_t run = (int64_t)tiles * halves * a.tile_b * kTileA;
+    float v[8] = {};
+#pragma unroll 4
+    for (int r = 0; r < a.parts; ++r) {
+        float q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = p[r * run + j * kTileA];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += q[j];
+    }
+    finish8<kAct>(a, wt, v);
 }
 
 // ---------------------------------------------------------------- host
@@ -784,13 +849,67 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-conv_status product_launch(const Product &given, void *stream) {
-    if (given.ma == 0 || given.nb == 0) return CONV_OK;
-    Product pr = given;
-    const int sms = device_sm_count();
+// Planned for the 152 SMs of the part this library is for, whatever the
+// device, so that workspace sizes do not depend on it.
+ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
+    constexpr int64_t kSms = 152;
+    ProductPlan pl;
     // Few rows: the long dim becomes the tile's 128 lanes and the few rows its
     // columns, so that no lanes idle and every CTA streams its own weights.
-    if (pr.ma < pr.nb && pr.ma <= 128) {
+    if (ma < nb && ma <= 128) {
+        pl.swap = true;
+        std::swap(ma, nb);
+    }
+    const int64_t k_steps = cdiv(k, kStepK);
+    // Pairs where there are enough tiles to fill the GPU, or enough k-steps in
+    // all of them to fill it with runs of at least 16 k-steps: a pair tile
+    // loads half the operand bytes per product of a 128 x 128 tile.  (The
+    // weight gradient of 50176 rows, 256 -> 1024: 72 us as 128 x 128 tiles in
+    // clusters of 8.)
+    const int64_t wide = nb > 128 ? 256 : 128;
+    const int64_t pair_tiles = cdiv(ma, 256) * cdiv(nb, wide);
+    if (nb > 64 && ma > 128 && (pair_tiles * 2 >= kSms || pair_tiles * k_steps >= kSms / 2 * 16)) {
+        pl.pair = true;
+        pl.tile_b = (int32_t)wide;
+        if (pair_tiles * 2 >= kSms && nb > 128) {
+            // The width that wastes least in the last round of tiles; 32
+            // columns stand for a tile's share of operand A's loads.
+            int64_t best = INT64_MAX;
+            for (int nt = 256; nt >= 128; nt -= 32) {
+                const int64_t rounds = cdiv(cdiv(ma, 256) * cdiv(nb, nt), kSms / 2);
+                if (rounds * (nt + 32) < best) {
+                    best = rounds * (nt + 32);
+                    pl.tile_b = nt;
+                }
+            }
+        }
+        pl.tiles_a = cdiv(ma, 256);
+        pl.tiles_b = cdiv(nb, pl.tile_b);
+        const int64_t tiles = pl.tiles_a * pl.tiles_b;
+        if (tiles * 2 < kSms) {
+            pl.parts = (int32_t)std::max<int64_t>(1, std::min(kSms / 2 / tiles, k_steps / 8));
+            if (pl.parts > 1) pl.part_bytes = (size_t)(pl.parts * tiles * 256 * pl.tile_b * 4);
+        }
+        return pl;
+    }
+    // Single CTAs with narrower tiles, split along k in clusters while that
+    // brings more SMs in.
+    pl.tile_b = (int32_t)std::min<int64_t>(round_up(nb, 32), 256);
+    while (pl.tile_b > 64 && cdiv(ma, kTileA) * cdiv(nb, pl.tile_b) * 2 <= kSms)
+        pl.tile_b = (int32_t)round_up(pl.tile_b / 2, 32);
+    pl.tiles_a = cdiv(ma, kTileA);
+    pl.tiles_b = cdiv(nb, pl.tile_b);
+    const int64_t tiles = pl.tiles_a * pl.tiles_b;
+    while (pl.split < kMaxSplit && tiles * pl.split * 2 <= kSms && k_steps >= pl.split * 4) pl.split *= 2;
+    return pl;
+}
+
+conv_status product_launch(const Product &given, void *workspace, void *stream) {
+    if (given.ma == 0 || given.nb == 0) return CONV_OK;
+    Product pr = given;
+    const ProductPlan pl = product_plan(pr.ma, pr.nb, pr.k);
+    if (pl.tiles_a * pl.tiles_b * pl.parts > INT32_MAX / kMaxSplit) return CONV_ERR_TOO_LARGE;
+    if (pl.swap) {
         std::swap(pr.ma, pr.nb);
         std::swap(pr.a, pr.b);
         std::swap(pr.d_sa, pr.d_sb);
@@ -813,40 +932,17 @@ conv_status product_launch(const Product &given, void *stream) {
     a.a_mn = !(pr.a.s_k == 1 || pr.k <= 1) || (pr.a.s_mn == 1 && pr.k <= 1);
     a.b_mn = !(pr.b.s_k == 1 || pr.k <= 1) || (pr.b.s_mn == 1 && pr.k <= 1);
 
-    // Tile shape: pairs of 256 x 256 where there are enough of them to fill
-    // the GPU, else single CTAs with narrower tiles, split along k while
-    // that brings more SMs in.
-    const int64_t pair_tiles = cdiv(pr.ma, 256) * cdiv(pr.nb, 256);
-    const bool pair = pair_tiles * 2 >= sms && pr.nb > 128;
-    int grid, cluster;
-    a.split = 1;
-    if (pair) {
-        // The width that wastes least in the last round of tiles; 32 columns
-        // stand for a tile's share of operand A's loads.
-        int64_t best = INT64_MAX;
-        for (int nt = 256; nt >= 128; nt -= 32) {
-            const int64_t rounds = cdiv(cdiv(pr.ma, 256) * cdiv(pr.nb, nt), sms / 2);
-            if (rounds * (nt + 32) < best) {
-                best = rounds * (nt + 32);
-                a.tile_b = nt;
-            }
-        }
-        a.tiles_a = (int32_t)cdiv(pr.ma, 256);
-        a.tiles_b = (int32_t)cdiv(pr.nb, a.tile_b);
-        a.b_rows = a.tile_b / 2;
-        cluster = 2;
-        grid = 2 * (int)std::min<int64_t>((int64_t)a.tiles_a * a.tiles_b, sms / 2);
-    } else {
-        a.tile_b = (int32_t)std::min<int64_t>(round_up(pr.nb, 32), 256);
-        while (a.tile_b > 64 && cdiv(pr.ma, kTileA) * cdiv(pr.nb, a.tile_b) * 2 <= sms) a.tile_b = (int32_t)round_up(a.tile_b / 2, 32);
-        a.tiles_a = (int32_t)cdiv(pr.ma, kTileA);
-        a.tiles_b = (int32_t)cdiv(pr.nb, a.tile_b);
-        a.b_rows = a.tile_b;
-        const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b;
-        while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps >= a.split * 4) a.split *= 2;
-        cluster = a.split;
-        grid = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
-    }
+    const bool pair = pl.pair;
+    a.tile_b = pl.tile_b;
+    a.tiles_a = (int32_t)pl.tiles_a;
+    a.tiles_b = (int32_t)pl.tiles_b;
+    a.split = pl.split;
+    a.parts = pl.parts;
+    a.part = (float *)workspace;
+    a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
+    const int64_t units = pl.tiles_a * pl.tiles_b * pl.parts;
+    const int sms = device_sm_count(), cluster = pair ? 2 : a.split;
+    const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
     a.stage_bytes = 16384 + (int32_t)round_up(a.b_mn ? a.b_boxes * 8192 : a.b_rows * 128, 1024);
     a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
@@ -899,6 +995,15 @@ conv_status product_launch(const Product &given, void *stream) {
     cfg.attrs = at;
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return CONV_ERR_CUDA;
+    if (a.parts > 1) {
+        typedef void (*Join)(ProductArgs, int);
+        static const Join joins[5] = {product_join_kernel<CONV_ACT_NONE>, product_join_kernel<CONV_ACT_RELU>,
+                                      product_join_kernel<CONV_ACT_GELU>, product_join_kernel<CONV_ACT_GELU_TANH>,
+                                      product_join_kernel<CONV_ACT_SILU>};
+        const int64_t warps = pl.tiles_a * pl.tiles_b * (tile_a / 32) * (a.tile_b / 8);
+        if (!launch_behind(joins[pr.act], dim3((unsigned)cdiv(warps, 8)), 256, 0, (cudaStream_t)stream, a, tile_a))
+            return CONV_ERR_CUDA;
+    }
     return CONV_OK;
 }
 

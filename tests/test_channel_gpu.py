@@ -96,7 +96,9 @@ def run_linear(ic, m, k, n, dt=BF16, act="none", bias=True, bias_dt=None, residu
 SIZES = [(1, 1, 1), (1, 8, 16), (1, 64, 128), (1, 1000, 257), (1, 4096, 512), (2, 65, 3), (7, 256, 128), (16, 512, 384),
          (17, 129, 130), (33, 64, 1), (64, 1024, 200), (100, 40, 1000), (127, 64, 64), (128, 128, 128), (129, 192, 255),
          (200, 16, 24), (255, 2048, 96), (256, 256, 256), (257, 72, 264), (300, 1, 300), (513, 520, 777),
-         (1000, 333, 70), (2048, 64, 512), (5000, 96, 48)]
+         (1000, 333, 70), (2048, 64, 512), (5000, 96, 48),
+         # few tiles and a long k: summed in runs and joined
+         (300, 20488, 520), (257, 30001, 130)]
 
 
 @pytest.mark.parametrize("m,k,n", SIZES)
@@ -261,7 +263,7 @@ def run_linear_grad(ic, m, k, n, dt=BF16, act="none", types=(None, None, F32), l
 
 
 GRAD_SIZES = [(1, 1, 1), (1, 64, 40), (2, 200, 8), (9, 8, 9), (31, 65, 33), (64, 64, 64), (128, 256, 128),
-              (130, 70, 257), (333, 192, 257), (512, 24, 520), (1000, 128, 64), (4099, 64, 72), (700, 600, 500)]
+              (130, 70, 257), (333, 192, 257), (512, 24, 520), (1000, 128, 64), (4099, 64, 72), (700, 600, 500), (20011, 512, 520)]
 
 
 @pytest.mark.parametrize("m,k,n", GRAD_SIZES)
