@@ -3,7 +3,7 @@
 //
 // One warp loads 64-element k-steps of both operands with TMA (128-byte
 // swizzle) into a ring, one thread issues tcgen05.mma into one of two
-// accumulators in tensor memory, and sixteen warps take the other accumulator
+// accumulators in tensor memory, and twelve warps take the other accumulator
 // through bias, pre-activation, activation and residual to the output.
 // Either operand may have k or its own dim contiguous: only the tensor map,
 // the descriptor strides and the instruction's transpose bits differ, so the
@@ -35,8 +35,10 @@ constexpr int kTileA = 128;        // accumulator lanes of one CTA
 constexpr int kStepK = 64;         // k elements per ring stage: one 128-byte row
 constexpr int kMaxTileB = 256;     // columns of one accumulator
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 640;      // 4 control warps, 16 epilogue warps
-constexpr int kEpilogueWarps = 16;
+constexpr int kThreads = 512;      // 4 control warps, 12 epilogue warps
+constexpr int kEpilogueWarps = 12; // (16 would leave 96 registers per thread, and spill)
+constexpr int kParts = kEpilogueWarps / 4;                             // epilogue warps on a quarter of the lanes
+constexpr int kChunks = (kMaxTileB / 32 + kParts - 1) / kParts;        // 32-column chunks of one of them
 constexpr int kSlotBytes = 2048;   // staging of one epilogue warp
 constexpr int kBiasBytes = kEpilogueWarps * 128;
 constexpr int kRingBytes = 196608;
@@ -664,10 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int slot = n & 1;
             const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
             // this warp's biases, loaded while the tile is being summed
-            float bias[2];
+            float bias[kChunks];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = (part + 4 * i) * 32;
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = (part + kParts * i) * 32;
                 bias[i] = c < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + c, lane) : 0.0f;
             }
             if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) break;
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
             if (k_lo == k_hi) {  // no products: the accumulator was never written
                 const uint32_t zero[32] = {};
-                for (int c = part * 32; c < a.tile_b; c += 128) ptx::tmem_st_32x32b_x32(acc + c, zero);
+                for (int c = part * 32; c < a.tile_b; c += 32 * kParts) ptx::tmem_st_32x32b_x32(acc + c, zero);
                 ptx::tmem_st_wait();
             }
             wt.row0 = row0;
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (!kPair && a.split > 1) {
                 // partial sums to shared memory [column][row], over the
                 // ring: its loads and MMAs are done
-                for (int c = part * 32; c < a.tile_b; c += 128) {
+                for (int c = part * 32; c < a.tile_b; c += 32 * kParts) {
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(acc + c, v);
                     ptx::tmem_ld_wait();
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 break;  // one tile per cluster; the rest follows the cluster barrier
             }
 #pragma unroll 1
-            for (int c = part * 32; c < a.tile_b; c += 128) {
+            for (int i = 0, c = part * 32; c < a.tile_b; ++i, c += 32 * kParts) {
                 wt.b0 = ib * a.tile_b + c;
                 wt.cols = min(32, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
                     continue;
                 }
-                finish_chunk<kAct>(a, wt, acc + c, c < 128 ? bias[0] : bias[1]);
+                finish_chunk<kAct>(a, wt, acc + c, i == 0 ? bias[0] : i == 1 ? bias[1] : bias[kChunks - 1]);
             }
             ptx::tc_fence_before();
             __syncwarp();
