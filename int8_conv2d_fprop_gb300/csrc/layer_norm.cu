@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <type_traits>
 
 #include "channel.h"
@@ -38,10 +39,16 @@ __device__ __forceinline__ float block_sum(float v, float2 *red) { return block_
 // ---------------------------------------------------------------- rows in registers
 // A row is held by a warp (kWarp: eight rows per block) or by the block, 8 kNv
 // elements per thread, so that it is read once and every sum runs over
-// registers.  kVec: aligned rows of a multiple of 8 elements, in groups of 8
-// (one 16-byte vector of a 16-bit type, two of a 32-bit one); otherwise
-// thread t holds elements t, t + T, ... and every access is one element wide,
-// which still makes whole runs per warp.
+// registers.
+//
+// kVec: thread t holds the aligned groups of 8 elements t, t + T, ...: one
+// 16-byte vector of a 16-bit type, two of a 32-bit one.  A row that starts
+// `lead` elements past such a boundary starts with a partial group and ends
+// with one.  Blocks step over the rows in multiples of 8, so a block (or
+// warp) meets the same lead on all its rows whatever the row stride, and its
+// columns stay in the same registers: odd widths cost two partial groups per
+// row.  This wants one lead for all matrices of a call.  Otherwise thread t
+// holds elements t, t + T, ..., one per access.
 template <typename T>
 constexpr bool kIs16 = sizeof(T) == 2;
 
@@ -64,47 +71,56 @@ __device__ __forceinline__ uint32_t bits16(float v, const __nv_bfloat16 *) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Group i of the row that starts at p (element stride 1): T threads to the row.
+// Where a thread's elements lie in its rows.
+template <bool kVec>
+struct Place {
+    int t, threads, cols, lead;
+    // column of element j of the thread's group i; outside the row if not below cols
+    __device__ __forceinline__ int column(int i, int j) const {
+        return kVec ? (i * threads + t) * 8 - lead + j : (i * 8 + j) * threads + t;
+    }
+    __device__ __forceinline__ bool inside(int c) const { return (uint32_t)c < (uint32_t)cols; }
+    __device__ __forceinline__ bool whole(int i) const {
+        return kVec ? inside(column(i, 0)) && inside(column(i, 7)) : inside(column(i, 7));
+    }
+};
+
+// Elements past the boundary of 8 at which p lies.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T *p) {
+    return (int)((uintptr_t)p / sizeof(T)) & 7;
+}
+
+// Group i of the row that starts at p; zeros outside the row.
 template <bool kVec, typename T>
-__device__ __forceinline__ void load_group(const T *p, int i, int t, int threads, int cols, Group<T> &g) {
-    if constexpr (kVec) {
-        const int c = (i * threads + t) * 8;
-        if (c < cols) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p + c);
-            g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
-            if constexpr (!kIs16<T>) {
-                const uint4 b = *reinterpret_cast<const uint4 *>(p + c + 4);
-                g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < (kIs16<T> ? 4 : 8); ++j) g.w[j] = 0;
+__device__ __forceinline__ void load_group(const T *p, const Place<kVec> &at, int i, Group<T> &g) {
+    if (kVec && at.whole(i)) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p + at.column(i, 0));
+        const uint4 a = q[0];
+        g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
+        if constexpr (!kIs16<T>) {
+            const uint4 b = q[1];
+            g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
         }
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = (i * 8 + j) * threads + t;
-            if constexpr (kIs16<T>) {
-                const uint32_t v = c < cols ? reinterpret_cast<const uint16_t *>(p)[c] : 0u;
-                if (j % 2) g.w[j / 2] |= v << 16;
-                else g.w[j / 2] = v;
-            } else {
-                g.w[j] = c < cols ? reinterpret_cast<const uint32_t *>(p)[c] : 0u;
-            }
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if constexpr (kIs16<T>) {
+            const uint32_t v = at.inside(c) ? reinterpret_cast<const uint16_t *>(p)[c] : 0u;
+            if (j % 2) g.w[j / 2] |= v << 16;
+            else g.w[j / 2] = v;
+        } else {
+            g.w[j] = at.inside(c) ? reinterpret_cast<const uint32_t *>(p)[c] : 0u;
         }
     }
 }
 
-template <bool kVec>
-__device__ __forceinline__ int column(int i, int j, int t, int threads) {
-    return kVec ? (i * threads + t) * 8 + j : (i * 8 + j) * threads + t;
-}
-
 template <bool kVec, typename T>
-__device__ __forceinline__ void store_group(T *p, int i, int t, int threads, int cols, const float (&v)[8]) {
-    if constexpr (kVec) {
-        const int c = (i * threads + t) * 8;
-        if (c >= cols) return;
+__device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, const float (&v)[8]) {
+    if (kVec && at.whole(i)) {
+        const int c = at.column(i, 0);
         if constexpr (kIs16<T>) {
             uint32_t w[4];
 #pragma unroll
@@ -114,25 +130,25 @@ __device__ __forceinline__ void store_group(T *p, int i, int t, int threads, int
             *reinterpret_cast<float4 *>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<float4 *>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = column<false>(i, j, t, threads);
-            if (c >= cols) continue;
-            if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)bits16(v[j], p);
-            else p[c] = v[j];
-        }
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if (!at.inside(c)) continue;
+        if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)bits16(v[j], p);
+        else p[c] = v[j];
     }
 }
 
-// 8 values of a parameter vector (any alignment; absent: `fill`).
+// 8 values of a parameter vector (any alignment; absent or outside: `fill`).
 template <bool kVec>
-__device__ __forceinline__ void load_params(const void *p, int32_t dtype, float fill, int i, int t, int threads, int cols,
+__device__ __forceinline__ void load_params(const void *p, int32_t dtype, float fill, const Place<kVec> &at, int i,
                                             float (&v)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int c = column<kVec>(i, j, t, threads);
-        v[j] = p && c < cols ? load_as_float(p, c, dtype) : fill;
+        const int c = at.column(i, j);
+        v[j] = p && at.inside(c) ? load_as_float(p, c, dtype) : fill;
     }
 }
 
@@ -141,6 +157,10 @@ __device__ __forceinline__ float row_sum(float v, float2 *red) {
     if constexpr (kWarp) return warp_sum(v);
     else return block_sum(v, red);
 }
+
+// Threads of a block that holds a row in kNv groups per thread, as registers
+// allow; an SM takes as many blocks as fit that many threads.
+constexpr int max_threads(int nv) { return nv == 1 ? 640 : 512; }
 
 struct NormArgs {
     MatRef x, y;
@@ -153,11 +173,17 @@ struct NormArgs {
 };
 
 template <typename X, typename Y, int kNv, bool kVec, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_rows_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_rows_kernel(const NormArgs a) {
     __shared__ float2 red[32];
-    const int threads = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
     const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
+    const X *x = (const X *)a.x.p;
+    Y *y = (Y *)const_cast<void *>(a.y.p);
+    Place<kVec> at;
+    at.t = kWarp ? threadIdx.x % 32 : threadIdx.x;
+    at.threads = kWarp ? 32 : blockDim.x;
+    at.cols = a.cols;
+    at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;  // parameters in registers over the rows
     float gain[kKeep ? kNv : 1][8], shift[kKeep ? kNv : 1][8];
@@ -166,16 +192,14 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_rows_kernel(cons
     if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            load_params<kVec>(a.gain, a.param_dtype, 1.0f, i, t, threads, a.cols, gain[i]);
-            load_params<kVec>(a.shift, a.param_dtype, 0.0f, i, t, threads, a.cols, shift[i]);
+            load_params(a.gain, a.param_dtype, 1.0f, at, i, gain[i]);
+            load_params(a.shift, a.param_dtype, 0.0f, at, i, shift[i]);
         }
     }
-    const X *x = (const X *)a.x.p;
-    Y *y = (Y *)const_cast<void *>(a.y.p);
     Group<X> next[kNv];
     if (first < a.rows) {
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) load_group<kVec>(x + first * a.x.rs, i, t, threads, a.cols, next[i]);
+        for (int i = 0; i < kNv; ++i) load_group(x + first * a.x.rs, at, i, next[i]);
     }
     for (int64_t r = first; r < a.rows; r += step) {
         float v[kNv][8];
@@ -189,17 +213,22 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_rows_kernel(cons
             }
         if (r + step < a.rows) {
 #pragma unroll
-            for (int i = 0; i < kNv; ++i) load_group<kVec>(x + (r + step) * a.x.rs, i, t, threads, a.cols, next[i]);
+            for (int i = 0; i < kNv; ++i) load_group(x + (r + step) * a.x.rs, at, i, next[i]);
         }
         const float mean = row_sum<kWarp>(s, red) * per;
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kNv; ++i)
+        for (int i = 0; i < kNv; ++i) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] -= mean;
-                if (column<kVec>(i, j, t, threads) < a.cols) s += v[i][j] * v[i][j];
+            for (int j = 0; j < 8; ++j) v[i][j] -= mean;
+            if (!at.whole(i)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!at.inside(at.column(i, j))) v[i][j] = 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
+        }
         const float rstd = rsqrtf(row_sum<kWarp>(s, red) * per + a.eps);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
@@ -207,14 +236,14 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_rows_kernel(cons
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * gain[i][j] + shift[i][j];
             } else {
-                load_params<kVec>(a.gain, a.param_dtype, 1.0f, i, t, threads, a.cols, gain[0]);
-                load_params<kVec>(a.shift, a.param_dtype, 0.0f, i, t, threads, a.cols, shift[0]);
+                load_params(a.gain, a.param_dtype, 1.0f, at, i, gain[0]);
+                load_params(a.shift, a.param_dtype, 0.0f, at, i, shift[0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * gain[0][j] + shift[0][j];
             }
-            store_group<kVec>(y + r * a.y.rs, i, t, threads, a.cols, v[i]);
+            store_group(y + r * a.y.rs, at, i, v[i]);
         }
-        if (t == 0) {
+        if (at.t == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
         }
@@ -234,33 +263,64 @@ struct NormGradArgs {
 // dx of every row and this block's partial sums of dy * n and dy, in
 // registers over its rows.
 template <typename X, int kNv, bool kVec, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_grad_rows_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? 2 : 1)
+    layer_norm_grad_rows_kernel(const NormGradArgs a) {
     __shared__ float2 red[32];
-    extern __shared__ float sums[];  // kWarp: [2][cols]
-    const int threads = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
+    // the gain, placed so that a thread's group is 32 aligned bytes (kWarp:
+    // as it is, since the warps' rows have different leads), if kKeep;
+    // kWarp: [8 warps][2][cols] sums, after the rows
+    extern __shared__ __align__(16) float shared[];
     const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
+    const X *x = (const X *)a.x.p, *dy = (const X *)a.dy.p, *res = (const X *)a.res.p;
+    X *dx = (X *)const_cast<void *>(a.dx.p);
+    Place<kVec> at;
+    at.t = kWarp ? threadIdx.x % 32 : threadIdx.x;
+    at.threads = kWarp ? 32 : blockDim.x;
+    at.cols = a.cols;
+    at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;
     constexpr bool kAhead = kNv * (kIs16<X> ? 1 : 2) <= 2;  // next row's loads in flight during this one
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    float gain[kKeep ? kNv : 1][8];
+    const int shift = kWarp ? 0 : at.lead;
     if constexpr (kKeep) {
-#pragma unroll
-        for (int i = 0; i < kNv; ++i) load_params<kVec>(a.gain, a.param_dtype, 1.0f, i, t, threads, a.cols, gain[i]);
+        for (int c = threadIdx.x; c < (kWarp ? a.cols : kNv * at.threads * 8); c += blockDim.x) {
+            const int col = c - shift;
+            shared[c] = a.gain && at.inside(col) ? load_as_float(a.gain, col, a.param_dtype) : 1.0f;
+        }
+        __syncthreads();
     }
+    auto load_gain = [&](int i, float (&g)[8]) {
+        if constexpr (kKeep && kVec) {
+            const int c = at.column(i, 0) + shift;
+            if (!kWarp || ((at.lead & 3) == 0 && at.whole(i))) {
+                const float4 u = *reinterpret_cast<const float4 *>(shared + c), v = *reinterpret_cast<const float4 *>(shared + c + 4);
+                g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w, g[4] = v.x, g[5] = v.y, g[6] = v.z, g[7] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = at.inside(c + j) ? shared[c + j] : 1.0f;
+            }
+        } else if constexpr (kKeep) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = at.column(i, j);
+                g[j] = at.inside(c) ? shared[c] : 1.0f;
+            }
+        } else {
+            load_params(a.gain, a.param_dtype, 1.0f, at, i, g);
+        }
+    };
     float dg[kNv][8] = {}, db[kNv][8] = {};
-    const X *x = (const X *)a.x.p, *dy = (const X *)a.dy.p, *res = (const X *)a.res.p;
-    X *dx = (X *)const_cast<void *>(a.dx.p);
     Group<X> nx[kNv], ny[kNv], nr[kNv];
     float mu = 0.0f, rs = 0.0f;
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            load_group<kVec>(x + r * a.x.rs, i, t, threads, a.cols, nx[i]);
-            load_group<kVec>(dy + r * a.dy.rs, i, t, threads, a.cols, ny[i]);
-            if (res) load_group<kVec>(res + r * a.res.rs, i, t, threads, a.cols, nr[i]);
+            load_group(x + r * a.x.rs, at, i, nx[i]);
+            load_group(dy + r * a.dy.rs, at, i, ny[i]);
+            if (res) load_group(res + r * a.res.rs, at, i, nr[i]);
         }
         mu = a.mean[r];
         rs = a.rstd[r];
@@ -280,12 +340,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_grad_rows_kernel
         float st = 0.0f, stn = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            if constexpr (!kKeep) load_params<kVec>(a.gain, a.param_dtype, 1.0f, i, t, threads, a.cols, gain[0]);
+            float gain[8];
+            load_gain(i, gain);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 // (outside the row dy is 0, and so is every term)
                 const float d = element(gy[i], j), n = (element(gx[i], j) - m) * rr;
-                const float u = d * gain[kKeep ? i : 0][j];
+                const float u = d * gain[j];
                 st += u;
                 stn += u * n;
                 dg[i][j] += d * n;
@@ -304,47 +365,39 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) layer_norm_grad_rows_kernel
         stn *= per;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            float v[8];
-            if constexpr (!kKeep) load_params<kVec>(a.gain, a.param_dtype, 1.0f, i, t, threads, a.cols, gain[0]);
+            float v[8], gain[8];
+            load_gain(i, gain);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = (element(gx[i], j) - m) * rr;
-                v[j] = rr * (element(gy[i], j) * gain[kKeep ? i : 0][j] - st - n * stn);
+                v[j] = rr * (element(gy[i], j) * gain[j] - st - n * stn);
                 if (res) v[j] += element(gr[i], j);
             }
-            store_group<kVec>(dx + r * a.dx.rs, i, t, threads, a.cols, v);
+            store_group(dx + r * a.dx.rs, at, i, v);
         }
     }
     if (!a.part) return;
     float *part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-    if constexpr (kWarp) {
-        // the eight warps add their sums in order
-        for (int w = 0; w < 8; ++w) {
-            if ((int)threadIdx.x / 32 == w)
+    if constexpr (kWarp) __syncthreads();  // the gain is no longer read
+    float *mine = kWarp ? shared + threadIdx.x / 32 * 2 * a.cols : part;
 #pragma unroll
-                for (int i = 0; i < kNv; ++i)
+    for (int i = 0; i < kNv; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = column<kVec>(i, j, t, threads);
-                        if (c < a.cols) {
-                            sums[c] = (w ? sums[c] : 0.0f) + dg[i][j];
-                            sums[a.cols + c] = (w ? sums[a.cols + c] : 0.0f) + db[i][j];
-                        }
-                    }
-            __syncthreads();
-        }
-        for (int c = threadIdx.x; c < 2 * a.cols; c += 256) part[c] = sums[c];
-    } else {
-#pragma unroll
-        for (int i = 0; i < kNv; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = column<kVec>(i, j, t, threads);
-                if (c < a.cols) {
-                    part[c] = dg[i][j];
-                    part[a.cols + c] = db[i][j];
-                }
+        for (int j = 0; j < 8; ++j) {
+            const int c = at.column(i, j);
+            if (at.inside(c)) {
+                mine[c] = dg[i][j];
+                mine[a.cols + c] = db[i][j];
             }
+        }
+    if constexpr (kWarp) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * a.cols; c += 256) {
+            float s = shared[c];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) s += shared[w * 2 * a.cols + c];
+            part[c] = s;
+        }
     }
 }
 
@@ -458,24 +511,48 @@ __global__ void __launch_bounds__(kThreads) layer_norm_params_any_kernel(const N
 // ---------------------------------------------------------------- launches
 bool unit_columns(const MatRef &m) { return !m.p || m.cs <= 1; }
 
-// How rows of `cols` elements are held: by a warp up to 8 * 32 * nv elements,
-// else by a block of `threads`.
+// Lead of a matrix's rows: 8 values for the rows modulo 8, as base and step.
+struct Lead {
+    int64_t base, step;
+};
+Lead lead_of_rows(const MatRef &m) {
+    const int64_t size = channel_elem_size(m.dtype);
+    return {(int64_t)((uintptr_t)m.p / (uintptr_t)size & 7), m.rs & 7};
+}
+
+// Whether the rows of all matrices (those given) have one lead.
+bool one_lead(std::initializer_list<const MatRef *> all) {
+    const Lead l = lead_of_rows(**all.begin());
+    for (const MatRef *m : all) {
+        if (!m->p) continue;
+        const Lead k = lead_of_rows(*m);
+        if (k.base != l.base || k.step != l.step) return false;
+    }
+    return true;
+}
+
+// How rows are held: by a warp up to 64 groups of 8, else by a block of
+// `threads`, nv groups each.
 struct RowShape {
     int nv = 0, threads = 0;  // nv == 0: not in registers
-    bool warp = false;
+    bool warp = false, vec = false;
 };
 
-RowShape row_shape(int64_t cols) {
+RowShape row_shape(int64_t cols, const MatRef &x, bool vec) {
     RowShape s;
-    if (cols <= 512) {
+    s.vec = vec;
+    const Lead l = lead_of_rows(x);
+    const bool aligned = l.base == 0 && l.step == 0;
+    const int64_t groups = vec && !aligned ? (cols + 14) / 8 : (cols + 7) / 8;
+    if (groups <= 64) {
         s.warp = true;
         s.threads = 256;
-        s.nv = cols <= 256 ? 1 : 2;
+        s.nv = groups <= 32 ? 1 : 2;
         return s;
     }
-    for (int nv = 1; nv <= 4; nv *= 2) {
-        const int64_t threads = round_up((cols + 8 * nv - 1) / (8 * nv), 32);
-        if (threads <= (nv == 1 ? 256 : 512)) {
+    for (int nv = 1; nv <= (vec ? 4 : 2); nv *= 2) {
+        const int64_t threads = round_up((groups + nv - 1) / nv, 32);
+        if (threads <= max_threads(nv)) {
             s.nv = nv;
             s.threads = (int)threads;
             return s;
@@ -484,33 +561,43 @@ RowShape row_shape(int64_t cols) {
     return s;
 }
 
+// Blocks for `rows` rows: all at once, or a multiple of 8 that fills the GPU
+// (so that a block's rows share their lead).
+int64_t row_blocks(int64_t rows, const RowShape &sh, int per_sm, int64_t limit) {
+    const int64_t blocks = sh.warp ? (rows + 7) / 8 : rows;
+    const int64_t most = std::min<int64_t>((int64_t)device_sm_count() * per_sm, limit) / 8 * 8;
+    return std::min(blocks, std::max<int64_t>(most, 8));
+}
+
 template <typename X, typename Y>
-bool launch_norm(const NormArgs &a, const RowShape &sh, bool vec, unsigned grid, cudaStream_t s) {
+bool launch_norm(const NormArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
 #define I8C_NORM(NV, W)                                                                                       \
-    (vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, 0, s, a)          \
+    (sh.vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, 0, s, a)          \
          : launch_behind(layer_norm_rows_kernel<X, Y, NV, false, W>, dim3(grid), sh.threads, 0, s, a))
     if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
-    return sh.nv == 1 ? I8C_NORM(1, false) : sh.nv == 2 ? I8C_NORM(2, false) : I8C_NORM(4, false);
+    if (sh.nv <= 2) return sh.nv == 1 ? I8C_NORM(1, false) : I8C_NORM(2, false);
+    return launch_behind(layer_norm_rows_kernel<X, Y, 4, true, false>, dim3(grid), sh.threads, 0, s, a);
 #undef I8C_NORM
 }
 
 template <typename X>
-bool launch_norm_to(const NormArgs &a, const RowShape &sh, bool vec, unsigned grid, cudaStream_t s) {
+bool launch_norm_to(const NormArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
     switch (a.y.dtype) {
-        case CONV_FLOAT32: return launch_norm<X, float>(a, sh, vec, grid, s);
-        case CONV_FLOAT16: return launch_norm<X, __half>(a, sh, vec, grid, s);
-        default: return launch_norm<X, __nv_bfloat16>(a, sh, vec, grid, s);
+        case CONV_FLOAT32: return launch_norm<X, float>(a, sh, grid, s);
+        case CONV_FLOAT16: return launch_norm<X, __half>(a, sh, grid, s);
+        default: return launch_norm<X, __nv_bfloat16>(a, sh, grid, s);
     }
 }
 
 template <typename X>
-bool launch_norm_grad(const NormGradArgs &a, const RowShape &sh, bool vec, unsigned grid, cudaStream_t s) {
-    const size_t smem = sh.warp ? (size_t)a.cols * 8 : 0;
+bool launch_norm_grad(const NormGradArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
+    const size_t smem = sh.warp ? (size_t)a.cols * (a.part ? 64 : 4) : sh.nv <= 2 ? (size_t)sh.nv * sh.threads * 32 : 0;
 #define I8C_NORM(NV, W)                                                                                        \
-    (vec ? launch_behind(layer_norm_grad_rows_kernel<X, NV, true, W>, dim3(grid), sh.threads, smem, s, a)      \
+    (sh.vec ? launch_behind(layer_norm_grad_rows_kernel<X, NV, true, W>, dim3(grid), sh.threads, smem, s, a)      \
          : launch_behind(layer_norm_grad_rows_kernel<X, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
     if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
-    return sh.nv == 1 ? I8C_NORM(1, false) : sh.nv == 2 ? I8C_NORM(2, false) : I8C_NORM(4, false);
+    if (sh.nv <= 2) return sh.nv == 1 ? I8C_NORM(1, false) : I8C_NORM(2, false);
+    return launch_behind(layer_norm_grad_rows_kernel<X, 4, true, false>, dim3(grid), sh.threads, smem, s, a);
 #undef I8C_NORM
 }
 
@@ -581,19 +668,17 @@ conv_status conv_layer_norm(const conv_matrix_desc *x, const void *x_dev, const 
     a.rows = rows, a.cols = (int32_t)cols;
     a.eps = p->eps, a.scale = p->scale, a.param_dtype = p->param_dtype;
     const cudaStream_t s = (cudaStream_t)stream;
-    const RowShape sh = row_shape(cols);
+    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}));
     bool ok;
     if (sh.nv == 0 || !unit_columns(a.x) || !unit_columns(a.y)) {
         ok = launch_behind(layer_norm_any_kernel, dim3((unsigned)rows), cols > 4096 ? 1024 : 256, 0, s, a);
     } else {
-        const bool vec = cols % 8 == 0 && vector_rows(a.x) && vector_rows(a.y);
-        const int64_t blocks = sh.warp ? (rows + 7) / 8 : rows;
-        const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * (1024 / sh.threads));
+        const unsigned grid = (unsigned)row_blocks(rows, sh, std::max(1, 1024 / sh.threads), INT32_MAX);
         switch (x->dtype) {
-            case CONV_FLOAT32: ok = launch_norm_to<float>(a, sh, vec, grid, s); break;
-            case CONV_FLOAT16: ok = launch_norm_to<__half>(a, sh, vec, grid, s); break;
-            case CONV_BFLOAT16: ok = launch_norm_to<__nv_bfloat16>(a, sh, vec, grid, s); break;
-            default: ok = launch_norm_to<int32_t>(a, sh, vec, grid, s); break;
+            case CONV_FLOAT32: ok = launch_norm_to<float>(a, sh, grid, s); break;
+            case CONV_FLOAT16: ok = launch_norm_to<__half>(a, sh, grid, s); break;
+            case CONV_BFLOAT16: ok = launch_norm_to<__nv_bfloat16>(a, sh, grid, s); break;
+            default: ok = launch_norm_to<int32_t>(a, sh, grid, s); break;
         }
     }
     return ok ? CONV_OK : CONV_ERR_CUDA;
@@ -670,7 +755,7 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     a.gain = gain_dev, a.mean = mean_dev, a.rstd = rstd_dev;
     a.part = dgain_dev || dshift_dev ? (float *)workspace : nullptr;
     a.rows = rows, a.cols = (int32_t)cols, a.param_dtype = p->param_dtype;
-    const RowShape sh = row_shape(cols);
+    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.dy, &a.res, &a.dx}));
     int64_t parts;
     bool ok = true;
     if (sh.nv == 0 || !unit_columns(a.dy) || !unit_columns(a.x) || !unit_columns(a.res) || !unit_columns(a.dx)) {
@@ -681,14 +766,11 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
             ok = ok && launch_behind(layer_norm_params_any_kernel, dim3((unsigned)((cols + 31) / 32), (unsigned)parts),
                                      kThreads, 0, s, a, per);
     } else {
-        const bool vec = cols % 8 == 0 && vector_rows(a.dy) && vector_rows(a.x) && vector_rows(a.res) &&
-                         vector_rows(a.dx);
-        const int64_t blocks = sh.warp ? (rows + 7) / 8 : rows;
-        parts = std::min<int64_t>({blocks, (int64_t)device_sm_count() * std::max(1, 512 / sh.threads), kMaxParts});
+        parts = row_blocks(rows, sh, sh.warp ? 2 : std::max(1, max_threads(sh.nv) / sh.threads), kMaxParts);
         switch (x->dtype) {
-            case CONV_FLOAT32: ok = launch_norm_grad<float>(a, sh, vec, (unsigned)parts, s); break;
-            case CONV_FLOAT16: ok = launch_norm_grad<__half>(a, sh, vec, (unsigned)parts, s); break;
-            default: ok = launch_norm_grad<__nv_bfloat16>(a, sh, vec, (unsigned)parts, s); break;
+            case CONV_FLOAT32: ok = launch_norm_grad<float>(a, sh, (unsigned)parts, s); break;
+            case CONV_FLOAT16: ok = launch_norm_grad<__half>(a, sh, (unsigned)parts, s); break;
+            default: ok = launch_norm_grad<__nv_bfloat16>(a, sh, (unsigned)parts, s); break;
         }
     }
     if (ok && a.part)
