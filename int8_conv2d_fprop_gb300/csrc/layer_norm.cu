@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 #include <type_traits>
@@ -22,19 +23,37 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sums of two values over the block, the same in every thread.
-__device__ __forceinline__ float2 block_sum2(float u, float v, float2 *red) {
-    const int warps = blockDim.x / 32;
-    u = warp_sum(u);
-    v = warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = make_float2(u, v);
-    __syncthreads();
-    const float2 mine = threadIdx.x % 32 < warps ? red[threadIdx.x % 32] : make_float2(0.0f, 0.0f);
-    return make_float2(warp_sum(mine.x), warp_sum(mine.y));
-}
+// Sums of two values over the block (at most 32 warps), the same in every
+// thread and in the same order in all of them, with one barrier: consecutive
+// sums use the two buffers in turn, and no warp can be two sums ahead.
+struct BlockSums {
+    float2 part[2][32];
+};
 
-__device__ __forceinline__ float block_sum(float v, float2 *red) { return block_sum2(v, 0.0f, red).x; }
+struct Summer {
+    BlockSums *s;
+    int turn = 0;
+    __device__ __forceinline__ float2 operator()(float u, float v) {
+        u = warp_sum(u);
+        v = warp_sum(v);
+        float2 *p = s->part[turn];
+        turn ^= 1;
+        if (threadIdx.x % 32 == 0) p[threadIdx.x / 32] = make_float2(u, v);
+        __syncthreads();
+        const int warps = blockDim.x / 32;
+        float2 t = make_float2(0.0f, 0.0f);
+        const float4 *q = reinterpret_cast<const float4 *>(p);
+#pragma unroll 4
+        for (int i = 0; i < warps / 2; ++i) {
+            const float4 w = q[i];
+            t.x += w.x + w.z;
+            t.y += w.y + w.w;
+        }
+        if (warps & 1) t.x += p[warps - 1].x, t.y += p[warps - 1].y;
+        return t;
+    }
+    __device__ __forceinline__ float operator()(float u) { return (*this)(u, 0.0f).x; }
+};
 
 // ---------------------------------------------------------------- rows in registers
 // A row is held by a warp (kWarp: eight rows per block) or by the block, 8 kNv
@@ -47,7 +66,8 @@ __device__ __forceinline__ float block_sum(float v, float2 *red) { return block_
 // with one.  Blocks step over the rows in multiples of 8, so a block (or
 // warp) meets the same lead on all its rows whatever the row stride, and its
 // columns stay in the same registers: odd widths cost two partial groups per
-// row.  This wants one lead for all matrices of a call.  Otherwise thread t
+// row.  This wants one lead for all the matrices a call reads; an output with
+// another one is turned through shared memory, a row at a time.  Otherwise thread t
 // holds elements t, t + T, ..., one per access.
 template <typename T>
 constexpr bool kIs16 = sizeof(T) == 2;
@@ -64,6 +84,17 @@ __device__ __forceinline__ float element(const Group<T> &g, int j) {
     else if constexpr (std::is_same_v<T, __half>)
         return __half2float(__ushort_as_half((unsigned short)(g.w[j / 2] >> (j % 2 * 16))));
     else return __uint_as_float(j % 2 ? g.w[j / 2] & 0xffff0000u : g.w[j / 2] << 16);
+}
+
+// Elements 2j and 2j + 1 as a pair of floats.
+template <typename T>
+__device__ __forceinline__ Pair element2(const Group<T> &g, int j) {
+    if constexpr (std::is_same_v<T, __half>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&g.w[j]));
+        return pair(f.x, f.y);
+    } else {
+        return pair(element(g, 2 * j), element(g, 2 * j + 1));
+    }
 }
 
 __device__ __forceinline__ uint32_t bits16(float v, const __half *) { return __half_as_ushort(__float2half_rn(v)); }
@@ -141,10 +172,63 @@ __device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, 
     }
 }
 
+// The same for an output whose lead differs from the rows read: its groups
+// are put together in shared memory, element c of the row at c + lead.
+template <typename T>
+struct Turn {
+    T *buf;     // shared memory of the row's warp or block: cols + 16 elements
+    int lead;   // of the output's rows
+};
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void turn_group(const Turn<T> &u, const Place<kVec> &at, int i, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if (!at.inside(c)) continue;
+        if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(u.buf)[c + u.lead] = (uint16_t)bits16(v[j], u.buf);
+        else u.buf[c + u.lead] = v[j];
+    }
+}
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_turned(T *p, const Turn<T> &u, const Place<kVec> &at) {
+    for (int g = at.t; g * 8 < at.cols + u.lead; g += at.threads) {
+        const int c = g * 8 - u.lead;
+        if (c >= 0 && c + 8 <= at.cols) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(u.buf + g * 8);
+            uint4 *o = reinterpret_cast<uint4 *>(p + c);
+            o[0] = q[0];
+            if constexpr (!kIs16<T>) o[1] = q[1];
+        } else {
+            for (int j = max(0, -c); j < 8 && c + j < at.cols; ++j) p[c + j] = u.buf[g * 8 + j];
+        }
+    }
+}
+
+template <bool kWarp>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (kWarp) __syncwarp();
+    else __syncthreads();
+}
+
 // 8 values of a parameter vector (any alignment; absent or outside: `fill`).
 template <bool kVec>
 __device__ __forceinline__ void load_params(const void *p, int32_t dtype, float fill, const Place<kVec> &at, int i,
                                             float (&v)[8]) {
+    if (kVec && p && at.whole(i)) {
+        const int c = at.column(i, 0);
+        const char *q = (const char *)p + (int64_t)c * (dtype == CONV_FLOAT32 ? 4 : 2);
+        if ((uintptr_t)q % 16 == 0) {
+            if (dtype == CONV_FLOAT32) {
+                const float4 a = reinterpret_cast<const float4 *>(q)[0], b = reinterpret_cast<const float4 *>(q)[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+                unpack8(*reinterpret_cast<const uint4 *>(q), dtype, v);
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = at.column(i, j);
@@ -152,15 +236,12 @@ __device__ __forceinline__ void load_params(const void *p, int32_t dtype, float 
     }
 }
 
-template <bool kWarp>
-__device__ __forceinline__ float row_sum(float v, float2 *red) {
-    if constexpr (kWarp) return warp_sum(v);
-    else return block_sum(v, red);
-}
+// Elements of a row being turned, a multiple of 16.
+__host__ __device__ constexpr int turn_elems(int cols) { return (cols + 31) / 16 * 16; }
 
 // Threads of a block that holds a row in kNv groups per thread, as registers
-// allow; an SM takes as many blocks as fit that many threads.
-constexpr int max_threads(int nv) { return nv == 1 ? 640 : 512; }
+// allow.
+constexpr int max_threads(int nv) { return nv == 2 ? 320 : 512; }
 
 struct NormArgs {
     MatRef x, y;
@@ -170,11 +251,14 @@ struct NormArgs {
     int32_t cols;
     float eps, scale;
     int32_t param_dtype;
+    int32_t turn;  // y's rows have another lead than x's
 };
 
 template <typename X, typename Y, int kNv, bool kVec, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_rows_kernel(const NormArgs a) {
-    __shared__ float2 red[32];
+    __shared__ __align__(16) BlockSums sums;
+    Summer block_sum{&sums};
+    extern __shared__ __align__(16) float shared[];  // rows being turned
     const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
     const X *x = (const X *)a.x.p;
@@ -184,6 +268,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
     at.threads = kWarp ? 32 : blockDim.x;
     at.cols = a.cols;
     at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
+    const Turn<Y> turn{(Y *)shared + (kWarp ? threadIdx.x / 32 * turn_elems(a.cols) : 0), lead_of(y + first * a.y.rs)};
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;  // parameters in registers over the rows
     float gain[kKeep ? kNv : 1][8], shift[kKeep ? kNv : 1][8];
@@ -215,7 +300,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
 #pragma unroll
             for (int i = 0; i < kNv; ++i) load_group(x + (r + step) * a.x.rs, at, i, next[i]);
         }
-        const float mean = row_sum<kWarp>(s, red) * per;
+        const float mean = (kWarp ? warp_sum(s) : block_sum(s)) * per;
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
@@ -229,7 +314,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
         }
-        const float rstd = rsqrtf(row_sum<kWarp>(s, red) * per + a.eps);
+        const float rstd = rsqrtf((kWarp ? warp_sum(s) : block_sum(s)) * per + a.eps);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             if constexpr (kKeep) {
@@ -241,7 +326,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * gain[0][j] + shift[0][j];
             }
-            store_group(y + r * a.y.rs, at, i, v[i]);
+            if (kVec && a.turn) turn_group(turn, at, i, v[i]);
+            else store_group(y + r * a.y.rs, at, i, v[i]);
+        }
+        if (kVec && a.turn) {
+            row_sync<kWarp>();
+            store_turned(y + r * a.y.rs, turn, at);
+            if (kWarp) __syncwarp();  // (a block's next row has barriers before it writes again)
         }
         if (at.t == 0) {
             if (a.mean) a.mean[r] = mean;
@@ -254,21 +345,66 @@ struct NormGradArgs {
     MatRef dy, x, res, dx;
     const void *gain;
     const float *mean, *rstd;
-    float *part;  // [blocks][2][cols], or NULL
+    float *part;  // [blocks][2][part_cols], or NULL
     int64_t rows;
     int32_t cols;
     int32_t param_dtype;
+    int32_t part_cols;
+    int32_t turn;  // dx's rows have another lead than the matrices read
 };
+
+// Rows on their way: a thread's groups of the next kDepth rows come in by
+// asynchronous copies into slots that only this thread reads, so that the
+// loads in flight cost no registers and no barriers.
+template <typename X>
+constexpr int kDepth = kIs16<X> ? 3 : 2;
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename X>
+struct Slots {
+    uint32_t base;    // this thread's first 16 bytes
+    uint32_t stride;  // 16 bytes of every thread of the block
+    __device__ __forceinline__ uint32_t at(int stage, int matrix, int matrices, int i, int nv) const {
+        return base + ((stage * matrices + matrix) * nv + i) * (kIs16<X> ? 1 : 2) * stride;
+    }
+};
+
+template <typename X>
+__device__ __forceinline__ void fetch_group(const X *p, const Place<true> &at, int i, uint32_t slot, uint32_t stride) {
+    if (at.whole(i)) {
+        copy_async16(slot, p + at.column(i, 0));
+        if constexpr (!kIs16<X>) copy_async16(slot + stride, p + at.column(i, 4));
+        return;
+    }
+    Group<X> g;
+    load_group(p, at, i, g);
+    ptx::st_shared_v4(slot, make_uint4(g.w[0], g.w[1], g.w[2], g.w[3]));
+    if constexpr (!kIs16<X>) ptx::st_shared_v4(slot + stride, make_uint4(g.w[4], g.w[5], g.w[6], g.w[7]));
+}
+
+template <typename X>
+__device__ __forceinline__ void read_group(uint32_t slot, uint32_t stride, Group<X> &g) {
+    const uint4 a = ptx::ld_shared_v4(slot);
+    g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
+    if constexpr (!kIs16<X>) {
+        const uint4 b = ptx::ld_shared_v4(slot + stride);
+        g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
+    }
+}
 
 // dx of every row and this block's partial sums of dy * n and dy, in
 // registers over its rows.
 template <typename X, int kNv, bool kVec, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? 2 : 1)
+__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? (kNv == 1 ? 3 : 2) : kNv == 4 ? 1 : 2)
     layer_norm_grad_rows_kernel(const NormGradArgs a) {
-    __shared__ float2 red[32];
-    // the gain, placed so that a thread's group is 32 aligned bytes (kWarp:
-    // as it is, since the warps' rows have different leads), if kKeep;
-    // kWarp: [8 warps][2][cols] sums, after the rows
+    __shared__ __align__(16) BlockSums sums;
+    Summer block_sum{&sums};
+    // every thread's own gains if kKeep ([group][half][thread] of 16 bytes);
+    // the rows on their way (kAhead); rows being turned; kWarp: at the end
+    // [8 warps][2][cols] sums over all of it
     extern __shared__ __align__(16) float shared[];
     const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
@@ -281,113 +417,180 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? 2 : 1)
     at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;
-    constexpr bool kAhead = kNv * (kIs16<X> ? 1 : 2) <= 2;  // next row's loads in flight during this one
+    constexpr bool kAhead = kVec && kNv <= 2;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    const int shift = kWarp ? 0 : at.lead;
-    if constexpr (kKeep) {
-        for (int c = threadIdx.x; c < (kWarp ? a.cols : kNv * at.threads * 8); c += blockDim.x) {
-            const int col = c - shift;
-            shared[c] = a.gain && at.inside(col) ? load_as_float(a.gain, col, a.param_dtype) : 1.0f;
-        }
-        __syncthreads();
-    }
-    auto load_gain = [&](int i, float (&g)[8]) {
-        if constexpr (kKeep && kVec) {
-            const int c = at.column(i, 0) + shift;
-            if (!kWarp || ((at.lead & 3) == 0 && at.whole(i))) {
-                const float4 u = *reinterpret_cast<const float4 *>(shared + c), v = *reinterpret_cast<const float4 *>(shared + c + 4);
-                g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w, g[4] = v.x, g[5] = v.y, g[6] = v.z, g[7] = v.w;
-            } else {
+    const int gain_elems = kKeep ? kNv * 8 * blockDim.x : 0;
+    const int matrices = res ? 3 : 2;
+    Slots<X> slots;
+    slots.stride = blockDim.x * 16;
+    slots.base = ptx::smem_addr(shared + gain_elems) + threadIdx.x * 16;
+    const uint32_t ring_bytes = kAhead ? kDepth<X> * matrices * kNv * (kIs16<X> ? 1 : 2) * slots.stride : 0;
+    const Turn<X> turn{(X *)((char *)(shared + gain_elems) + ring_bytes) + (kWarp ? threadIdx.x / 32 * turn_elems(a.cols) : 0),
+                       lead_of(dx + first * a.dx.rs)};
+    auto fetch = [&](int64_t r, int stage) {
+        if constexpr (kAhead) {
+            if (r < a.rows) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = at.inside(c + j) ? shared[c + j] : 1.0f;
+                for (int i = 0; i < kNv; ++i) {
+                    fetch_group(x + r * a.x.rs, at, i, slots.at(stage, 0, matrices, i, kNv), slots.stride);
+                    fetch_group(dy + r * a.dy.rs, at, i, slots.at(stage, 1, matrices, i, kNv), slots.stride);
+                    if (res) fetch_group(res + r * a.res.rs, at, i, slots.at(stage, 2, matrices, i, kNv), slots.stride);
+                }
             }
-        } else if constexpr (kKeep) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = at.column(i, j);
-                g[j] = at.inside(c) ? shared[c] : 1.0f;
+    for (int d = 0; d < kDepth<X>; ++d) fetch(first + d * step, d);
+    const uint32_t my_gain = ptx::smem_addr(shared) + threadIdx.x * 16;
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            float g[8];
+            load_params(a.gain, a.param_dtype, 1.0f, at, i, g);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                ptx::st_shared_v4(my_gain + (2 * i + h) * slots.stride,
+                                  make_uint4(__float_as_uint(g[4 * h]), __float_as_uint(g[4 * h + 1]),
+                                             __float_as_uint(g[4 * h + 2]), __float_as_uint(g[4 * h + 3])));
+        }
+    }
+    // gains 4h .. 4h + 3 of group i
+    auto load_gain = [&](int i, Pair (&g)[4]) {
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 w = ptx::ld_shared_v4(my_gain + (2 * i + h) * slots.stride);
+                g[2 * h] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+                g[2 * h + 1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
             }
         } else {
-            load_params(a.gain, a.param_dtype, 1.0f, at, i, g);
+            float f[8];
+            load_params(a.gain, a.param_dtype, 1.0f, at, i, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = pair(f[2 * j], f[2 * j + 1]);
         }
     };
-    float dg[kNv][8] = {}, db[kNv][8] = {};
-    Group<X> nx[kNv], ny[kNv], nr[kNv];
+    Pair dg[kNv][4], db[kNv][4];
+#pragma unroll
+    for (int i = 0; i < kNv; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f);
     float mu = 0.0f, rs = 0.0f;
-    auto fetch = [&](int64_t r) {
-#pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            load_group(x + r * a.x.rs, at, i, nx[i]);
-            load_group(dy + r * a.dy.rs, at, i, ny[i]);
-            if (res) load_group(res + r * a.res.rs, at, i, nr[i]);
-        }
-        mu = a.mean[r];
-        rs = a.rstd[r];
-    };
-    if (kAhead && first < a.rows) fetch(first);
+    if (first < a.rows) mu = a.mean[first], rs = a.rstd[first];
+    int stage = 0;
     for (int64_t r = first; r < a.rows; r += step) {
-        if (!kAhead) fetch(r);
         Group<X> gx[kNv], gy[kNv], gr[kNv];
+        if constexpr (kAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth<X> - 1) : "memory");
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            gx[i] = nx[i];
-            gy[i] = ny[i];
-            gr[i] = nr[i];
-        }
-        const float m = mu, rr = rs;
-        if (kAhead && r + step < a.rows) fetch(r + step);
-        float st = 0.0f, stn = 0.0f;
+            for (int i = 0; i < kNv; ++i) {
+                read_group(slots.at(stage, 0, matrices, i, kNv), slots.stride, gx[i]);
+                read_group(slots.at(stage, 1, matrices, i, kNv), slots.stride, gy[i]);
+                if (res) read_group(slots.at(stage, 2, matrices, i, kNv), slots.stride, gr[i]);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < kNv; ++i) {
-            float gain[8];
-            load_gain(i, gain);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // (outside the row dy is 0, and so is every term)
-                const float d = element(gy[i], j), n = (element(gx[i], j) - m) * rr;
-                const float u = d * gain[j];
-                st += u;
-                stn += u * n;
-                dg[i][j] += d * n;
-                db[i][j] += d;
+            for (int i = 0; i < kNv; ++i) {
+                load_group(x + r * a.x.rs, at, i, gx[i]);
+                load_group(dy + r * a.dy.rs, at, i, gy[i]);
+                if (res) load_group(res + r * a.res.rs, at, i, gr[i]);
             }
         }
+        const float m = mu, rr = rs;
+        if (r + step < a.rows) mu = a.mean[r + step], rs = a.rstd[r + step];
+        // n = x rstd - mean rstd
+        const Pair scale = pair(rr), offset = pair(-m * rr);
+        Pair st2 = pair(0.0f), stn2 = pair(0.0f);
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            Pair gain[4];
+            load_gain(i, gain);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // (outside the row dy is 0, and so is every term)
+                const Pair d = element2(gy[i], j), n = fma2(element2(gx[i], j), scale, offset);
+                const Pair u = mul2(d, gain[j]);
+                st2 = add2(st2, u);
+                stn2 = fma2(u, n, stn2);
+                dg[i][j] = fma2(d, n, dg[i][j]);
+                db[i][j] = add2(db[i][j], d);
+            }
+        }
+        // the slots just read take the row kDepth steps on
+        fetch(r + kDepth<X> * step, stage);
+        if (++stage == kDepth<X>) stage = 0;
         if (!dx) continue;
+        float st, stn, other;
+        split(st2, &st, &other);
+        st += other;
+        split(stn2, &stn, &other);
+        stn += other;
         if constexpr (kWarp) {
             st = warp_sum(st);
             stn = warp_sum(stn);
         } else {
-            const float2 s = block_sum2(st, stn, red);
+            const float2 s = block_sum(st, stn);
             st = s.x, stn = s.y;
         }
-        st *= per;
-        stn *= per;
+        const Pair minus_st = pair(-st * per * rr), minus_stn = pair(-stn * per * rr);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            float v[8], gain[8];
+            float v[8];
+            Pair gain[4];
             load_gain(i, gain);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = (element(gx[i], j) - m) * rr;
-                v[j] = rr * (element(gy[i], j) * gain[j] - st - n * stn);
-                if (res) v[j] += element(gr[i], j);
+            for (int j = 0; j < 4; ++j) {
+                const Pair n = fma2(element2(gx[i], j), scale, offset);
+                Pair w = fma2(mul2(element2(gy[i], j), gain[j]), scale, minus_st);
+                w = fma2(n, minus_stn, w);
+                if (res) w = add2(w, element2(gr[i], j));
+                split(w, &v[2 * j], &v[2 * j + 1]);
             }
-            store_group(dx + r * a.dx.rs, at, i, v);
+            if (kVec && a.turn) turn_group(turn, at, i, v);
+            else store_group(dx + r * a.dx.rs, at, i, v);
+        }
+        if (kVec && a.turn) {
+            row_sync<kWarp>();
+            store_turned(dx + r * a.dx.rs, turn, at);
+            if (kWarp) __syncwarp();  // (a block's next row has barriers before it writes again)
         }
     }
+    if constexpr (kAhead) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.part) return;
-    float *part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
-    if constexpr (kWarp) __syncthreads();  // the gain is no longer read
+    float *part = a.part + (int64_t)blockIdx.x * 2 * a.part_cols;
+    if constexpr (kVec && !kWarp) {
+        // (a block's sums start at its lead: whole groups are aligned)
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            const int c = at.column(i, 0) + at.lead;
+            if (c >= a.cols + at.lead) continue;
+            float g[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split(dg[i][j], &g[2 * j], &g[2 * j + 1]), split(db[i][j], &b[2 * j], &b[2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                *reinterpret_cast<float4 *>(part + c + j) = make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
+                *reinterpret_cast<float4 *>(part + a.part_cols + c + j) = make_float4(b[j], b[j + 1], b[j + 2], b[j + 3]);
+            }
+        }
+        return;
+    }
+    if constexpr (kWarp) __syncthreads();  // nothing in shared memory is read any more
     float *mine = kWarp ? shared + threadIdx.x / 32 * 2 * a.cols : part;
+    const int second = kWarp ? a.cols : a.part_cols;
 #pragma unroll
     for (int i = 0; i < kNv; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = at.column(i, j);
+            float lo, hi;
             if (at.inside(c)) {
-                mine[c] = dg[i][j];
-                mine[a.cols + c] = db[i][j];
+                split(dg[i][j / 2], &lo, &hi);
+                mine[c] = j % 2 ? hi : lo;
+                split(db[i][j / 2], &lo, &hi);
+                mine[second + c] = j % 2 ? hi : lo;
             }
         }
     if constexpr (kWarp) {
@@ -396,48 +599,55 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? 2 : 1)
             float s = shared[c];
 #pragma unroll
             for (int w = 1; w < 8; ++w) s += shared[w * 2 * a.cols + c];
-            part[c] = s;
+            part[c < a.cols ? c : a.part_cols + c - a.cols] = s;
         }
     }
 }
 
-// Adds the blocks' partial sums: 32 columns per block, 32 threads per column.
-__global__ void __launch_bounds__(1024) layer_norm_params_sum_kernel(const float *part, int64_t parts, int64_t cols,
-                                                                     void *dgain, void *dshift, int32_t dtype) {
+// Adds the blocks' partial sums: 32 columns per block, 32 threads per column;
+// blockIdx.y 0: dgain, 1: dshift.  Block i's sums start at (lead + i lead_step)
+// mod 8.
+__global__ void __launch_bounds__(1024) layer_norm_params_sum_kernel(const float *part, int parts, int cols, int part_cols,
+                                                                     int lead, int lead_step, void *dgain, void *dshift,
+                                                                     int32_t dtype) {
     __shared__ float red[32][33];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    const int64_t c = (int64_t)blockIdx.x * 32 + tx;
+    const int c = blockIdx.x * 32 + tx;
+    void *out = blockIdx.y ? dshift : dgain;
     ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    if (!out) return;
     float s = 0.0f;
-    if (c < 2 * cols)
-        for (int64_t i = ty; i < parts; i += 32) s += part[i * 2 * cols + c];
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = ty; i < parts; i += 32)
+            s += part[((int64_t)2 * i + blockIdx.y) * part_cols + c + ((lead + i * lead_step) & 7)];
+    }
     red[ty][tx] = s;
     __syncthreads();
-    const int64_t cc = (int64_t)blockIdx.x * 32 + ty;
+    const int cc = blockIdx.x * 32 + ty;
     s = warp_sum(red[tx][ty]);
-    if (tx == 0 && cc < 2 * cols) {
-        void *out = cc < cols ? dgain : dshift;
-        if (out) store_from_float(out, cc < cols ? cc : cc - cols, dtype, s);
-    }
+    if (tx == 0 && cc < cols) store_from_float(out, cc, dtype, s);
 }
 
 // ---------------------------------------------------------------- any width, any strides
 // Rows too wide for registers and matrices whose columns are not contiguous:
 // a block per row, the row read again for each pass (from L2 mostly).
 __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const NormArgs a) {
-    __shared__ float2 red[32];
+    __shared__ __align__(16) BlockSums sums;
+    Summer block_sum{&sums};
     const MatRef &x = a.x, &y = a.y;
     const int64_t r = blockIdx.x, cols = a.cols;
     ptx::grid_dependency_wait();
     float s = 0.0f;
     for (int64_t c = threadIdx.x; c < cols; c += (int)blockDim.x) s += a.scale * load_as_float(x.p, r * x.rs + c * x.cs, x.dtype);
-    const float mean = block_sum(s, red) / (float)cols;
+    const float mean = block_sum(s) / (float)cols;
     s = 0.0f;
     for (int64_t c = threadIdx.x; c < cols; c += (int)blockDim.x) {
         const float d = a.scale * load_as_float(x.p, r * x.rs + c * x.cs, x.dtype) - mean;
         s += d * d;
     }
-    const float rstd = rsqrtf(block_sum(s, red) / (float)cols + a.eps);
+    const float rstd = rsqrtf(block_sum(s) / (float)cols + a.eps);
     for (int64_t c = threadIdx.x; c < cols; c += (int)blockDim.x) {
         const float d = a.scale * load_as_float(x.p, r * x.rs + c * x.cs, x.dtype) - mean;
         const float g = a.gain ? load_as_float(a.gain, c, a.param_dtype) : 1.0f;
@@ -451,7 +661,8 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const NormArgs a) 
 }
 
 __global__ void __launch_bounds__(1024) layer_norm_dx_any_kernel(const NormGradArgs a) {
-    __shared__ float2 red[32];
+    __shared__ __align__(16) BlockSums sums;
+    Summer block_sum{&sums};
     const MatRef &x = a.x, &dy = a.dy, &res = a.res, &dx = a.dx;
     const int64_t r = blockIdx.x, cols = a.cols;
     ptx::grid_dependency_wait();
@@ -464,7 +675,7 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_any_kernel(const NormGradA
         st += t;
         stn += t * n;
     }
-    const float2 s = block_sum2(st, stn, red);
+    const float2 s = block_sum(st, stn);
     st = s.x / (float)cols;
     stn = s.y / (float)cols;
     for (int64_t c = threadIdx.x; c < cols; c += (int)blockDim.x) {
@@ -502,9 +713,9 @@ __global__ void __launch_bounds__(kThreads) layer_norm_params_any_kernel(const N
             sg += sg_red[i][tx];
             sb += sb_red[i][tx];
         }
-        float *p = a.part + (int64_t)blockIdx.y * 2 * a.cols;
+        float *p = a.part + (int64_t)blockIdx.y * 2 * a.part_cols;
         p[c] = sg;
-        p[a.cols + c] = sb;
+        p[a.part_cols + c] = sb;
     }
 }
 
@@ -529,6 +740,13 @@ bool one_lead(std::initializer_list<const MatRef *> all) {
         if (k.base != l.base || k.step != l.step) return false;
     }
     return true;
+}
+
+// Whether an output row (and the gain beside it) fits the 48 KB of shared
+// memory that a launch has without asking.
+bool turnable(int64_t cols, int32_t out_dtype) {
+    const int64_t rows = cols <= 512 ? 8 : 1;
+    return rows * turn_elems((int)std::min<int64_t>(cols, 1 << 20)) * channel_elem_size(out_dtype) <= 40 << 10;
 }
 
 // How rows are held: by a warp up to 64 groups of 8, else by a block of
@@ -571,12 +789,13 @@ int64_t row_blocks(int64_t rows, const RowShape &sh, int per_sm, int64_t limit) 
 
 template <typename X, typename Y>
 bool launch_norm(const NormArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
+    const size_t smem = a.turn ? (size_t)turn_elems(a.cols) * sizeof(Y) * (sh.warp ? 8 : 1) : 0;
 #define I8C_NORM(NV, W)                                                                                       \
-    (sh.vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, 0, s, a)          \
-         : launch_behind(layer_norm_rows_kernel<X, Y, NV, false, W>, dim3(grid), sh.threads, 0, s, a))
+    (sh.vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, smem, s, a)          \
+         : launch_behind(layer_norm_rows_kernel<X, Y, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
     if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
     if (sh.nv <= 2) return sh.nv == 1 ? I8C_NORM(1, false) : I8C_NORM(2, false);
-    return launch_behind(layer_norm_rows_kernel<X, Y, 4, true, false>, dim3(grid), sh.threads, 0, s, a);
+    return launch_behind(layer_norm_rows_kernel<X, Y, 4, true, false>, dim3(grid), sh.threads, smem, s, a);
 #undef I8C_NORM
 }
 
@@ -589,12 +808,28 @@ bool launch_norm_to(const NormArgs &a, const RowShape &sh, unsigned grid, cudaSt
     }
 }
 
+// A launch with more than 48 KB of shared memory.
+template <void (*kKernel)(NormGradArgs)>
+bool launch_large(dim3 grid, int threads, size_t smem, cudaStream_t s, const NormGradArgs &a) {
+    static std::atomic<bool> ready[64];  // (check_device admits 64 devices)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!ready[dev].load()) {
+        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10) != cudaSuccess) return false;
+        ready[dev].store(true);
+    }
+    return launch_behind(kKernel, grid, threads, smem, s, a);
+}
+
 template <typename X>
 bool launch_norm_grad(const NormGradArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
-    const size_t smem = sh.warp ? (size_t)a.cols * (a.part ? 64 : 4) : sh.nv <= 2 ? (size_t)sh.nv * sh.threads * 32 : 0;
+    const size_t gain = sh.nv <= 2 ? (size_t)sh.nv * sh.threads * 32 : 0;
+    const size_t ring = sh.vec && sh.nv <= 2 ? (size_t)kDepth<X> * (a.res.p ? 3 : 2) * sh.nv * 8 * sizeof(X) * sh.threads : 0;
+    const size_t turn = a.turn ? (size_t)turn_elems(a.cols) * sizeof(X) * (sh.warp ? 8 : 1) : 0;
+    const size_t smem = std::max(gain + ring + turn, sh.warp && a.part ? (size_t)a.cols * 64 : 0);
 #define I8C_NORM(NV, W)                                                                                        \
-    (sh.vec ? launch_behind(layer_norm_grad_rows_kernel<X, NV, true, W>, dim3(grid), sh.threads, smem, s, a)      \
-         : launch_behind(layer_norm_grad_rows_kernel<X, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
+    (sh.vec ? launch_large<layer_norm_grad_rows_kernel<X, NV, true, W>>(dim3(grid), sh.threads, smem, s, a)    \
+            : launch_behind(layer_norm_grad_rows_kernel<X, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
     if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
     if (sh.nv <= 2) return sh.nv == 1 ? I8C_NORM(1, false) : I8C_NORM(2, false);
     return launch_behind(layer_norm_grad_rows_kernel<X, 4, true, false>, dim3(grid), sh.threads, smem, s, a);
@@ -623,9 +858,12 @@ conv_status check_vector(const void *p, int64_t n, int64_t size, const conv_matr
 // most kMaxParts of them whatever the device.
 constexpr int64_t kMaxParts = 608;  // four blocks on each of 152 SMs
 
+// (room for a lead and for whole groups)
+int64_t part_columns(int64_t cols) { return round_up(cols, 8) + 8; }
+
 size_t norm_grad_bytes(int64_t rows, int64_t cols) {
     if (rows == 0) return 0;
-    return (size_t)round_up(std::min(kMaxParts, rows) * 2 * cols * 4, 256);
+    return (size_t)round_up(std::min(kMaxParts, rows) * 2 * part_columns(cols) * 4, 256);
 }
 
 }  // namespace
@@ -668,7 +906,8 @@ conv_status conv_layer_norm(const conv_matrix_desc *x, const void *x_dev, const 
     a.rows = rows, a.cols = (int32_t)cols;
     a.eps = p->eps, a.scale = p->scale, a.param_dtype = p->param_dtype;
     const cudaStream_t s = (cudaStream_t)stream;
-    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}));
+    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}) || turnable(cols, y->dtype));
+    a.turn = !one_lead({&a.x, &a.y});
     bool ok;
     if (sh.nv == 0 || !unit_columns(a.x) || !unit_columns(a.y)) {
         ok = launch_behind(layer_norm_any_kernel, dim3((unsigned)rows), cols > 4096 ? 1024 : 256, 0, s, a);
@@ -755,7 +994,11 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     a.gain = gain_dev, a.mean = mean_dev, a.rstd = rstd_dev;
     a.part = dgain_dev || dshift_dev ? (float *)workspace : nullptr;
     a.rows = rows, a.cols = (int32_t)cols, a.param_dtype = p->param_dtype;
-    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.dy, &a.res, &a.dx}));
+    a.part_cols = (int32_t)part_columns(cols);
+    Lead lead{0, 0};  // of the blocks' sums
+    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.dy, &a.res}) &&
+                                                 (one_lead({&a.x, &a.dx}) || turnable(cols, x->dtype)));
+    a.turn = !one_lead({&a.x, &a.dx});
     int64_t parts;
     bool ok = true;
     if (sh.nv == 0 || !unit_columns(a.dy) || !unit_columns(a.x) || !unit_columns(a.res) || !unit_columns(a.dx)) {
@@ -766,7 +1009,12 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
             ok = ok && launch_behind(layer_norm_params_any_kernel, dim3((unsigned)((cols + 31) / 32), (unsigned)parts),
                                      kThreads, 0, s, a, per);
     } else {
-        parts = row_blocks(rows, sh, sh.warp ? 2 : std::max(1, max_threads(sh.nv) / sh.threads), kMaxParts);
+        parts = row_blocks(rows, sh, sh.warp ? (sh.nv == 1 ? 3 : 2)
+                                         : sh.nv == 1 ? 1024 / sh.threads
+                                         : sh.nv == 2 ? 2
+                                                      : 512 / sh.threads,
+                           kMaxParts);
+        if (sh.vec && !sh.warp) lead = lead_of_rows(a.x);
         switch (x->dtype) {
             case CONV_FLOAT32: ok = launch_norm_grad<float>(a, sh, (unsigned)parts, s); break;
             case CONV_FLOAT16: ok = launch_norm_grad<__half>(a, sh, (unsigned)parts, s); break;
@@ -774,8 +1022,9 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
         }
     }
     if (ok && a.part)
-        ok = launch_behind(layer_norm_params_sum_kernel, dim3((unsigned)((2 * cols + 31) / 32)), 1024, 0, s,
-                           (const float *)workspace, parts, cols, dgain_dev, dshift_dev, p->param_dtype);
+        ok = launch_behind(layer_norm_params_sum_kernel, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, s,
+                           (const float *)workspace, (int)parts, (int)cols, (int)a.part_cols, (int)lead.base,
+                           (int)lead.step, dgain_dev, dshift_dev, p->param_dtype);
     return ok ? CONV_OK : CONV_ERR_CUDA;
 }
 

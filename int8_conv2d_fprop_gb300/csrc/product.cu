@@ -322,16 +322,16 @@ __device__ __noinline__ void any_to_slot(Side s, WarpTile t, int c, int cols) {
     const int64_t at = (int64_t)t.row0 * s.sa + (int64_t)(t.b0 + c + col) * s.sb;
     if (col < cols) {
 #pragma unroll 1
-        for (int r = first; r < t.rows; r += 8 * step) {
-            // (eight loads in flight)
-            uint32_t q[8];
+        for (int r = first; r < t.rows; r += 16 * step) {
+            // (sixteen loads in flight)
+            uint32_t q[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
                 if (r + i * step < t.rows)
                     q[i] = wide ? ((const uint32_t *)s.p)[at + (r + i * step) * s.sa]
                                 : ((const uint16_t *)s.p)[at + (r + i * step) * s.sa];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 16; ++i)
                 if (r + i * step < t.rows) {
                     if (wide) ptx::st_shared_b32(at32(t.slot, r + i * step, col), q[i]);
                     else st_shared_b16(at16(t.slot, r + i * step, col), (uint16_t)q[i]);
@@ -789,13 +789,16 @@ __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant
     const float *p = a.part + ((int64_t)th * a.tile_b + c) * kTileA + quad * 32 + lane;
     const int64_t run = (int64_t)tiles * halves * a.tile_b * kTileA;
     float v[8] = {};
-#pragma unroll 4
-    for (int r = 0; r < a.parts; ++r) {
-        float q[8];
+    for (int r0 = 0; r0 < a.parts; r0 += 8) {
+        float q[8][8];  // 64 loads in flight
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = p[r * run + j * kTileA];
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += q[j];
+            for (int j = 0; j < 8; ++j) q[i][j] = r0 + i < a.parts ? p[(r0 + i) * run + j * kTileA] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += q[i][j];
     }
     finish8<kAct>(a, wt, v);
 }
