@@ -155,7 +155,7 @@ __device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, 
         if constexpr (kIs16<T>) {
             uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = bits16(v[2 * j], p) | bits16(v[2 * j + 1], p) << 16;
+            for (int j = 0; j < 4; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], std::is_same_v<T, __half> ? CONV_FLOAT16 : CONV_BFLOAT16);
             *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
             *reinterpret_cast<float4 *>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
@@ -182,6 +182,24 @@ struct Turn {
 
 template <bool kVec, typename T>
 __device__ __forceinline__ void turn_group(const Turn<T> &u, const Place<kVec> &at, int i, const float (&v)[8]) {
+    if (at.whole(i)) {
+        T *to = u.buf + at.column(i, 0) + u.lead;
+        if constexpr (kIs16<T>) {
+            if (((u.lead ^ at.lead) & 1) == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+                    reinterpret_cast<uint32_t *>(to)[j / 2] =
+                        pack2(v[j], v[j + 1], std::is_same_v<T, __half> ? CONV_FLOAT16 : CONV_BFLOAT16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)bits16(v[j], u.buf);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) to[j] = v[j];
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = at.column(i, j);
@@ -239,9 +257,14 @@ __device__ __forceinline__ void load_params(const void *p, int32_t dtype, float 
 // Elements of a row being turned, a multiple of 16.
 __host__ __device__ constexpr int turn_elems(int cols) { return (cols + 31) / 16 * 16; }
 
-// Threads of a block that holds a row in kNv groups per thread, as registers
-// allow.
-constexpr int max_threads(int nv) { return nv == 2 ? 320 : 512; }
+// Threads of a block that holds a row in kNv groups per thread, and the
+// blocks of that size that registers are kept for.  (More elements per thread
+// share one sum's shuffles and barrier; the gradient's sums take twice the
+// registers.)
+constexpr int norm_threads(int nv) { return nv == 2 ? 256 : 512; }
+constexpr int norm_blocks(int nv) { return nv == 2 ? 3 : 1; }
+constexpr int grad_threads(int nv) { return nv == 1 ? 128 : nv == 2 ? 320 : 512; }
+constexpr int grad_blocks(int nv) { return nv == 1 ? 6 : nv == 2 ? 2 : 1; }
 
 struct NormArgs {
     MatRef x, y;
@@ -255,10 +278,13 @@ struct NormArgs {
 };
 
 template <typename X, typename Y, int kNv, bool kVec, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_rows_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kWarp ? 256 : norm_threads(kNv), kWarp ? (kNv == 4 ? 2 : 1) : norm_blocks(kNv))
+    layer_norm_rows_kernel(const NormArgs a) {
     __shared__ __align__(16) BlockSums sums;
     Summer block_sum{&sums};
-    extern __shared__ __align__(16) float shared[];  // rows being turned
+    // every thread's own gains and shifts unless kKeep ([group][gain, shift]
+    // [half][thread] of 16 bytes), then rows being turned
+    extern __shared__ __align__(16) float shared[];
     const int64_t first = kWarp ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
     const X *x = (const X *)a.x.p;
@@ -268,10 +294,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
     at.threads = kWarp ? 32 : blockDim.x;
     at.cols = a.cols;
     at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
-    const Turn<Y> turn{(Y *)shared + (kWarp ? threadIdx.x / 32 * turn_elems(a.cols) : 0), lead_of(y + first * a.y.rs)};
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;  // parameters in registers over the rows
+    const Turn<Y> turn{(Y *)(shared + (kKeep ? 0 : kNv * 16 * blockDim.x)) +
+                           (kWarp ? threadIdx.x / 32 * turn_elems(a.cols) : 0),
+                       lead_of(y + first * a.y.rs)};
     float gain[kKeep ? kNv : 1][8], shift[kKeep ? kNv : 1][8];
+    const uint32_t slot = ptx::smem_addr(shared) + threadIdx.x * 16, stride = blockDim.x * 16;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if constexpr (kKeep) {
@@ -279,6 +308,21 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
         for (int i = 0; i < kNv; ++i) {
             load_params(a.gain, a.param_dtype, 1.0f, at, i, gain[i]);
             load_params(a.shift, a.param_dtype, 0.0f, at, i, shift[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNv; ++i) {
+            load_params(a.gain, a.param_dtype, 1.0f, at, i, gain[0]);
+            load_params(a.shift, a.param_dtype, 0.0f, at, i, shift[0]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *g = gain[0] + 4 * h, *b = shift[0] + 4 * h;
+                ptx::st_shared_v4(slot + (4 * i + h) * stride, make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]),
+                                                                          __float_as_uint(g[2]), __float_as_uint(g[3])));
+                ptx::st_shared_v4(slot + (4 * i + 2 + h) * stride,
+                                  make_uint4(__float_as_uint(b[0]), __float_as_uint(b[1]), __float_as_uint(b[2]),
+                                             __float_as_uint(b[3])));
+            }
         }
     }
     Group<X> next[kNv];
@@ -321,10 +365,16 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv)) layer_norm_row
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * gain[i][j] + shift[i][j];
             } else {
-                load_params(a.gain, a.param_dtype, 1.0f, at, i, gain[0]);
-                load_params(a.shift, a.param_dtype, 0.0f, at, i, shift[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * gain[0][j] + shift[0][j];
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 g = ptx::ld_shared_v4(slot + (4 * i + h) * stride);
+                    const uint4 b = ptx::ld_shared_v4(slot + (4 * i + 2 + h) * stride);
+                    float *w = v[i] + 4 * h;
+                    w[0] = w[0] * rstd * __uint_as_float(g.x) + __uint_as_float(b.x);
+                    w[1] = w[1] * rstd * __uint_as_float(g.y) + __uint_as_float(b.y);
+                    w[2] = w[2] * rstd * __uint_as_float(g.z) + __uint_as_float(b.z);
+                    w[3] = w[3] * rstd * __uint_as_float(g.w) + __uint_as_float(b.w);
+                }
             }
             if (kVec && a.turn) turn_group(turn, at, i, v[i]);
             else store_group(y + r * a.y.rs, at, i, v[i]);
@@ -398,7 +448,7 @@ __device__ __forceinline__ void read_group(uint32_t slot, uint32_t stride, Group
 // dx of every row and this block's partial sums of dy * n and dy, in
 // registers over its rows.
 template <typename X, int kNv, bool kVec, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? (kNv == 1 ? 3 : 2) : kNv == 4 ? 1 : 2)
+__global__ void __launch_bounds__(kWarp ? 256 : grad_threads(kNv), kWarp ? (kNv == 1 ? 3 : 2) : grad_blocks(kNv))
     layer_norm_grad_rows_kernel(const NormGradArgs a) {
     __shared__ __align__(16) BlockSums sums;
     Summer block_sum{&sums};
@@ -604,13 +654,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : max_threads(kNv), kWarp ? (kNv =
     }
 }
 
-// Adds the blocks' partial sums: 32 columns per block, 32 threads per column;
+// Adds the blocks' partial sums: 32 columns per block, 16 threads per column;
 // blockIdx.y 0: dgain, 1: dshift.  Block i's sums start at (lead + i lead_step)
 // mod 8.
-__global__ void __launch_bounds__(1024) layer_norm_params_sum_kernel(const float *part, int parts, int cols, int part_cols,
-                                                                     int lead, int lead_step, void *dgain, void *dshift,
-                                                                     int32_t dtype) {
-    __shared__ float red[32][33];
+__global__ void __launch_bounds__(512) layer_norm_params_sum_kernel(const float *part, int parts, int cols, int part_cols,
+                                                                    int lead, int lead_step, void *dgain, void *dshift,
+                                                                    int32_t dtype) {
+    __shared__ float red[16][32];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int c = blockIdx.x * 32 + tx;
     void *out = blockIdx.y ? dshift : dgain;
@@ -619,15 +669,15 @@ __global__ void __launch_bounds__(1024) layer_norm_params_sum_kernel(const float
     if (!out) return;
     float s = 0.0f;
     if (c < cols) {
-#pragma unroll 4
-        for (int i = ty; i < parts; i += 32)
+#pragma unroll 8
+        for (int i = ty; i < parts; i += 16)
             s += part[((int64_t)2 * i + blockIdx.y) * part_cols + c + ((lead + i * lead_step) & 7)];
     }
     red[ty][tx] = s;
     __syncthreads();
-    const int cc = blockIdx.x * 32 + ty;
-    s = warp_sum(red[tx][ty]);
-    if (tx == 0 && cc < cols) store_from_float(out, cc, dtype, s);
+    if (ty || c >= cols) return;
+    for (int i = 1; i < 16; ++i) s += red[i][tx];
+    store_from_float(out, c, dtype, s);
 }
 
 // ---------------------------------------------------------------- any width, any strides
@@ -742,35 +792,34 @@ bool one_lead(std::initializer_list<const MatRef *> all) {
     return true;
 }
 
-// Whether an output row (and the gain beside it) fits the 48 KB of shared
-// memory that a launch has without asking.
+// Whether an output row can be turned in shared memory.
 bool turnable(int64_t cols, int32_t out_dtype) {
-    const int64_t rows = cols <= 512 ? 8 : 1;
+    const int64_t rows = cols <= 1024 ? 8 : 1;
     return rows * turn_elems((int)std::min<int64_t>(cols, 1 << 20)) * channel_elem_size(out_dtype) <= 40 << 10;
 }
 
-// How rows are held: by a warp up to 64 groups of 8, else by a block of
-// `threads`, nv groups each.
+// How rows are held: by a warp up to 64 groups of 8 (128 in the forward
+// pass), else by a block of `threads`, nv groups each.
 struct RowShape {
     int nv = 0, threads = 0;  // nv == 0: not in registers
     bool warp = false, vec = false;
 };
 
-RowShape row_shape(int64_t cols, const MatRef &x, bool vec) {
+RowShape row_shape(int64_t cols, const MatRef &x, bool vec, bool grad) {
     RowShape s;
     s.vec = vec;
     const Lead l = lead_of_rows(x);
     const bool aligned = l.base == 0 && l.step == 0;
     const int64_t groups = vec && !aligned ? (cols + 14) / 8 : (cols + 7) / 8;
-    if (groups <= 64) {
+    if (groups <= (grad || !vec ? 64 : 128)) {
         s.warp = true;
         s.threads = 256;
-        s.nv = groups <= 32 ? 1 : 2;
+        s.nv = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
         return s;
     }
-    for (int nv = 1; nv <= (vec ? 4 : 2); nv *= 2) {
+    for (int nv = grad ? 1 : 2; nv <= (vec ? 4 : 2); nv *= 2) {
         const int64_t threads = round_up((groups + nv - 1) / nv, 32);
-        if (threads <= max_threads(nv)) {
+        if (threads <= (grad ? grad_threads(nv) : norm_threads(nv))) {
             s.nv = nv;
             s.threads = (int)threads;
             return s;
@@ -787,15 +836,31 @@ int64_t row_blocks(int64_t rows, const RowShape &sh, int per_sm, int64_t limit) 
     return std::min(blocks, std::max<int64_t>(most, 8));
 }
 
+// A launch with more than 48 KB of shared memory.
+template <auto kKernel, typename Args>
+bool launch_large(dim3 grid, int threads, size_t smem, cudaStream_t s, const Args &a) {
+    static std::atomic<bool> ready[64];  // (check_device admits 64 devices)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!ready[dev].load()) {
+        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10) != cudaSuccess) return false;
+        ready[dev].store(true);
+    }
+    return launch_behind(kKernel, grid, threads, smem, s, a);
+}
+
 template <typename X, typename Y>
 bool launch_norm(const NormArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
-    const size_t smem = a.turn ? (size_t)turn_elems(a.cols) * sizeof(Y) * (sh.warp ? 8 : 1) : 0;
+    const size_t smem = (sh.nv == 4 ? (size_t)sh.threads * 256 : 0) +
+                        (a.turn ? (size_t)turn_elems(a.cols) * sizeof(Y) * (sh.warp ? 8 : 1) : 0);
 #define I8C_NORM(NV, W)                                                                                       \
     (sh.vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, smem, s, a)          \
          : launch_behind(layer_norm_rows_kernel<X, Y, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
+    if (sh.nv == 4)
+        return sh.warp ? launch_large<layer_norm_rows_kernel<X, Y, 4, true, true>>(dim3(grid), sh.threads, smem, s, a)
+                       : launch_large<layer_norm_rows_kernel<X, Y, 4, true, false>>(dim3(grid), sh.threads, smem, s, a);
     if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
-    if (sh.nv <= 2) return sh.nv == 1 ? I8C_NORM(1, false) : I8C_NORM(2, false);
-    return launch_behind(layer_norm_rows_kernel<X, Y, 4, true, false>, dim3(grid), sh.threads, smem, s, a);
+    return I8C_NORM(2, false);
 #undef I8C_NORM
 }
 
@@ -806,19 +871,6 @@ bool launch_norm_to(const NormArgs &a, const RowShape &sh, unsigned grid, cudaSt
         case CONV_FLOAT16: return launch_norm<X, __half>(a, sh, grid, s);
         default: return launch_norm<X, __nv_bfloat16>(a, sh, grid, s);
     }
-}
-
-// A launch with more than 48 KB of shared memory.
-template <void (*kKernel)(NormGradArgs)>
-bool launch_large(dim3 grid, int threads, size_t smem, cudaStream_t s, const NormGradArgs &a) {
-    static std::atomic<bool> ready[64];  // (check_device admits 64 devices)
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (!ready[dev].load()) {
-        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10) != cudaSuccess) return false;
-        ready[dev].store(true);
-    }
-    return launch_behind(kKernel, grid, threads, smem, s, a);
 }
 
 template <typename X>
@@ -906,13 +958,13 @@ conv_status conv_layer_norm(const conv_matrix_desc *x, const void *x_dev, const 
     a.rows = rows, a.cols = (int32_t)cols;
     a.eps = p->eps, a.scale = p->scale, a.param_dtype = p->param_dtype;
     const cudaStream_t s = (cudaStream_t)stream;
-    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}) || turnable(cols, y->dtype));
+    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}) || turnable(cols, y->dtype), false);
     a.turn = !one_lead({&a.x, &a.y});
     bool ok;
     if (sh.nv == 0 || !unit_columns(a.x) || !unit_columns(a.y)) {
         ok = launch_behind(layer_norm_any_kernel, dim3((unsigned)rows), cols > 4096 ? 1024 : 256, 0, s, a);
     } else {
-        const unsigned grid = (unsigned)row_blocks(rows, sh, std::max(1, 1024 / sh.threads), INT32_MAX);
+        const unsigned grid = (unsigned)row_blocks(rows, sh, (sh.nv == 4 ? 512 : sh.warp ? 1024 : 768) / sh.threads, INT32_MAX);
         switch (x->dtype) {
             case CONV_FLOAT32: ok = launch_norm_to<float>(a, sh, grid, s); break;
             case CONV_FLOAT16: ok = launch_norm_to<__half>(a, sh, grid, s); break;
@@ -997,7 +1049,7 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     a.part_cols = (int32_t)part_columns(cols);
     Lead lead{0, 0};  // of the blocks' sums
     const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.dy, &a.res}) &&
-                                                 (one_lead({&a.x, &a.dx}) || turnable(cols, x->dtype)));
+                                                 (one_lead({&a.x, &a.dx}) || turnable(cols, x->dtype)), true);
     a.turn = !one_lead({&a.x, &a.dx});
     int64_t parts;
     bool ok = true;
@@ -1009,11 +1061,8 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
             ok = ok && launch_behind(layer_norm_params_any_kernel, dim3((unsigned)((cols + 31) / 32), (unsigned)parts),
                                      kThreads, 0, s, a, per);
     } else {
-        parts = row_blocks(rows, sh, sh.warp ? (sh.nv == 1 ? 3 : 2)
-                                         : sh.nv == 1 ? 1024 / sh.threads
-                                         : sh.nv == 2 ? 2
-                                                      : 512 / sh.threads,
-                           kMaxParts);
+        const int per_sm = sh.warp ? (sh.nv == 1 ? 3 : 2) : grad_threads(sh.nv) * grad_blocks(sh.nv) / sh.threads;
+        parts = row_blocks(rows, sh, per_sm, kMaxParts);
         if (sh.vec && !sh.warp) lead = lead_of_rows(a.x);
         switch (x->dtype) {
             case CONV_FLOAT32: ok = launch_norm_grad<float>(a, sh, (unsigned)parts, s); break;
@@ -1022,7 +1071,7 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
         }
     }
     if (ok && a.part)
-        ok = launch_behind(layer_norm_params_sum_kernel, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, s,
+        ok = launch_behind(layer_norm_params_sum_kernel, dim3((unsigned)((cols + 31) / 32), 2), 512, 0, s,
                            (const float *)workspace, (int)parts, (int)cols, (int)a.part_cols, (int)lead.base,
                            (int)lead.step, dgain_dev, dshift_dev, p->param_dtype);
     return ok ? CONV_OK : CONV_ERR_CUDA;

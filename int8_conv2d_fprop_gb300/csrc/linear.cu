@@ -14,37 +14,47 @@ namespace i8c {
 namespace {
 
 // ---------------------------------------------------------------- packing
-// Row-contiguous copy of a [rows, cols] matrix of 16-bit elements, rows
-// `ld` elements apart (a multiple of 8; the padding is never read).
-// 32 x 32 tiles through shared memory, so that both a row-contiguous and a
-// column-contiguous source are read in runs.
-__global__ void __launch_bounds__(256) pack_matrix_kernel(const uint16_t *src, int64_t rs, int64_t cs, int64_t rows,
-                                                          int64_t cols, uint16_t *dst, int64_t ld,
-                                                          int64_t col_tiles, bool by_rows) {
+// Row-contiguous copies of up to two [rows, cols] matrices of 16-bit
+// elements, rows `ld` elements apart (a multiple of 8; the padding is never
+// read), in one launch.  32 x 32 tiles through shared memory, so that both a
+// row-contiguous and a column-contiguous source are read in runs.
+struct PackJob {
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t rs, cs, rows, cols, ld;
+    int32_t col_tiles, tiles;
+    int32_t by_rows;  // lanes along the columns
+};
+struct PackJobs {
+    PackJob job[2];
+    int count = 0;
+};
+
+__global__ void __launch_bounds__(256) pack_matrix_kernel(const PackJobs jobs) {
     __shared__ uint16_t tile[32][33];
-    const int64_t r0 = (int64_t)blockIdx.x / col_tiles * 32, c0 = (int64_t)blockIdx.x % col_tiles * 32;
+    const bool second = (int)blockIdx.x >= jobs.job[0].tiles;
+    const PackJob &j = jobs.job[second];
+    const int t = (int)blockIdx.x - (second ? jobs.job[0].tiles : 0);
+    const int64_t r0 = (int64_t)(t / j.col_tiles) * 32, c0 = (int64_t)(t % j.col_tiles) * 32;
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
-        const int r = by_rows ? y + i : x, c = by_rows ? x : y + i;
-        if (r0 + r < rows && c0 + c < cols) tile[r][c] = src[(r0 + r) * rs + (c0 + c) * cs];
+        const int r = j.by_rows ? y + i : x, c = j.by_rows ? x : y + i;
+        if (r0 + r < j.rows && c0 + c < j.cols) tile[r][c] = j.src[(r0 + r) * j.rs + (c0 + c) * j.cs];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 32; i += 8)
-        if (r0 + y + i < rows && c0 + x < cols) dst[(r0 + y + i) * ld + c0 + x] = tile[y + i][x];
+        if (r0 + y + i < j.rows && c0 + x < j.cols) j.dst[(r0 + y + i) * j.ld + c0 + x] = tile[y + i][x];
 }
 
-conv_status pack_matrix(const MatRef &m, int64_t rows, int64_t cols, void *dst, int64_t ld, cudaStream_t s) {
-    const int64_t rt = (rows + 31) / 32, ct = (cols + 31) / 32;
-    if (rt * ct > INT32_MAX) return CONV_ERR_TOO_LARGE;
-    // lanes along the smaller stride (a dim of extent 1 has none)
-    const bool by_rows = rows == 1 || (cols > 1 && m.cs <= m.rs);
-    return launch_behind(pack_matrix_kernel, dim3((unsigned)(rt * ct)), 256, 0, s, (const uint16_t *)m.p, m.rs, m.cs, rows,
-                         cols, (uint16_t *)dst, ld, ct, by_rows)
-               ? CONV_OK : CONV_ERR_CUDA;
+conv_status run_packs(PackJobs &jobs, cudaStream_t s) {
+    if (jobs.count == 0) return CONV_OK;
+    const int64_t tiles = (int64_t)jobs.job[0].tiles + (jobs.count > 1 ? jobs.job[1].tiles : 0);
+    if (tiles > INT32_MAX) return CONV_ERR_TOO_LARGE;
+    return launch_behind(pack_matrix_kernel, dim3((unsigned)tiles), 256, 0, s, jobs) ? CONV_OK : CONV_ERR_CUDA;
 }
 
 struct Packed {  // a packed copy in the workspace, or none
@@ -61,17 +71,27 @@ void plan_pack(const conv_matrix_desc *d, const void *p, size_t *total, Packed *
     *total += k->bytes;
 }
 
-// Operand as the product reads it: in place, or its packed copy (made here).
-conv_status operand(const conv_matrix_desc *d, const void *p, const Packed &k, void *workspace, cudaStream_t s,
+// Operand as the product reads it: in place, or its packed copy, which the
+// jobs then have to make.
+conv_status operand(const conv_matrix_desc *d, const void *p, const Packed &k, void *workspace, PackJobs *jobs,
                     MatRef *m) {
     *m = mat_ref(d, p);
     if (!k.bytes) return CONV_OK;
-    void *dst = (char *)workspace + k.off;
-    conv_status st = pack_matrix(*m, d->rows, d->cols, dst, k.ld, s);
-    m->p = dst;
+    const int64_t rt = (d->rows + 31) / 32, ct = (d->cols + 31) / 32;
+    if (rt * ct > INT32_MAX / 2) return CONV_ERR_TOO_LARGE;
+    PackJob &j = jobs->job[jobs->count++];
+    j.src = (const uint16_t *)p;
+    j.dst = (uint16_t *)((char *)workspace + k.off);
+    j.rs = m->rs, j.cs = m->cs;
+    j.rows = d->rows, j.cols = d->cols;
+    j.ld = k.ld;
+    j.col_tiles = (int32_t)ct, j.tiles = (int32_t)(rt * ct);
+    // lanes along the smaller stride (a dim of extent 1 has none)
+    j.by_rows = d->rows == 1 || (d->cols > 1 && m->cs <= m->rs);
+    m->p = j.dst;
     m->rs = d->rows > 1 ? k.ld : 0;
     m->cs = d->cols > 1 ? 1 : 0;
-    return st;
+    return CONV_OK;
 }
 
 conv_status check_linear_params(const conv_linear_params *p, const conv_matrix_desc *x, bool has_bias) {
@@ -128,12 +148,13 @@ LinearPlan plan_linear(const conv_matrix_desc *x, const void *x_dev, const conv_
 
 // ---------------------------------------------------------------- dz
 // dz = dy * act'(preact) in 16 bits, and the column sums of the unrounded dz
-// over this block's rows.  32 x 8 threads: 32 columns, 8 rows at a time.
+// over this block's rows: 32 columns, a row per warp at a time.  One block to
+// the column's rows writes dbias itself.
 template <int kAct>
-__global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
+__global__ void __launch_bounds__(1024) linear_dz_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
                                                         int64_t rows_per_block, void *dz, int64_t dz_ld,
-                                                        float *part) {
-    __shared__ float red[8][32];
+                                                        float *part, void *dbias, int32_t bias_dtype) {
+    __shared__ float red[32][32];
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + x;
     const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
@@ -141,8 +162,10 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, i
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float sum = 0.0f;
-    if (c < cols)
-        for (int64_t r = r0 + y; r < r1; r += 8) {
+    const int warps = blockDim.x / 32;
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t r = r0 + y; r < r1; r += warps) {
             float v = load_as_float(dy.p, r * dy.rs + c * dy.cs, dy.dtype);
             if constexpr (kAct != CONV_ACT_NONE) {
                 float slope = load_as_float(pre.p, r * pre.rs + c * pre.cs, pre.dtype), unused = 0.0f;
@@ -152,12 +175,14 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(MatRef dy, MatRef pre, i
             if (dz) store_from_float(dz, r * dz_ld + c, dy.dtype, v);
             sum += v;
         }
-    if (!part) return;
+    }
+    if (!part && !dbias) return;
     red[y][x] = sum;
     __syncthreads();
     if (y == 0 && c < cols) {
-        for (int i = 1; i < 8; ++i) sum += red[i][x];
-        part[(int64_t)blockIdx.y * cols + c] = sum;
+        for (int i = 1; i < warps; ++i) sum += red[i][x];
+        if (part) part[(int64_t)blockIdx.y * cols + c] = sum;
+        else store_from_float(dbias, c, bias_dtype, sum);
     }
 }
 
@@ -223,22 +248,22 @@ __global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef p
 
 // Adds the blocks' partial sums: 32 columns per block, 32 threads per column.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int64_t parts, int64_t cols, void *out,
-                                                          int32_t dtype) {
-    __shared__ float red[32][33];
+                                                         int32_t dtype) {
+    __shared__ float red[32][32];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float s = 0.0f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 8
         for (int64_t i = ty; i < parts; i += 32) s += part[i * cols + c];
+    }
     red[ty][tx] = s;
     __syncthreads();
-    const int64_t mine = (int64_t)blockIdx.x * 32 + ty;
-    s = red[tx][ty];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (tx == 0 && mine < cols) store_from_float(out, mine, dtype, s);
+    if (ty || c >= cols) return;
+    for (int i = 1; i < 32; ++i) s += red[i][tx];
+    store_from_float(out, c, dtype, s);
 }
 
 struct GradPlan {
@@ -263,7 +288,8 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
             pl.bytes += (size_t)round_up(m * pl.dz_ld * 2, 256);
         }
         // enough blocks for every SM to hold several, whichever kernel runs
-        const int64_t wanted = std::min<int64_t>(512, std::max<int64_t>(1, 2432 / ((n + 255) / 256)));
+        // (few rows: one block to a column, without a second kernel)
+        const int64_t wanted = m <= 512 ? 1 : std::min<int64_t>(512, std::max<int64_t>(1, 2432 / ((n + 255) / 256)));
         pl.rows_per_part = round_up((m + wanted - 1) / wanted, 8);
         pl.parts = (m + pl.rows_per_part - 1) / pl.rows_per_part;
         pl.part_off = pl.bytes;
@@ -282,28 +308,28 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
 }
 
 template <int kAct>
-void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, bool sums,
-               cudaStream_t s) {
+void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, void *dbias,
+               int32_t bias_dtype, cudaStream_t s) {
     void *dz = pl.dz ? (char *)ws + pl.dz_off : nullptr;
-    float *part = sums ? (float *)((char *)ws + pl.part_off) : nullptr;
-    if (n % 8 == 0 && vector_rows(dy) && vector_rows(pre))
+    float *part = dbias && pl.parts > 1 ? (float *)((char *)ws + pl.part_off) : nullptr;
+    if (pl.parts > 1 && n % 8 == 0 && vector_rows(dy) && vector_rows(pre))
         launch_behind(linear_dz_rows_kernel<kAct>, dim3((unsigned)((n + 255) / 256), (unsigned)pl.parts), 256, 0, s, dy,
                       pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part);
     else
-        launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts), 256, 0, s, dy, pre,
-                      m, n, pl.rows_per_part, dz, pl.dz_ld, part);
+        launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts), pl.parts > 1 ? 256 : 1024,
+                      0, s, dy, pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part, part ? nullptr : dbias, bias_dtype);
 }
 
 conv_status make_dz(const GradPlan &pl, int32_t act, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n,
                     void *ws, void *dbias, int32_t bias_dtype, cudaStream_t s) {
     switch (act) {
-        case CONV_ACT_RELU: launch_dz<CONV_ACT_RELU>(pl, dy, pre, m, n, ws, dbias, s); break;
-        case CONV_ACT_GELU: launch_dz<CONV_ACT_GELU>(pl, dy, pre, m, n, ws, dbias, s); break;
-        case CONV_ACT_GELU_TANH: launch_dz<CONV_ACT_GELU_TANH>(pl, dy, pre, m, n, ws, dbias, s); break;
-        case CONV_ACT_SILU: launch_dz<CONV_ACT_SILU>(pl, dy, pre, m, n, ws, dbias, s); break;
-        default: launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, s); break;
+        case CONV_ACT_RELU: launch_dz<CONV_ACT_RELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_GELU: launch_dz<CONV_ACT_GELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_GELU_TANH: launch_dz<CONV_ACT_GELU_TANH>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_SILU: launch_dz<CONV_ACT_SILU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        default: launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
     }
-    if (dbias)
+    if (dbias && pl.parts > 1)
         launch_behind(column_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, 0, s,
                       (const float *)((char *)ws + pl.part_off), pl.parts, n, dbias, bias_dtype);
     return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
@@ -366,8 +392,10 @@ conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv
     }
     if ((st = check_device())) return st;
     MatRef xr, wr;
-    if ((st = operand(x, x_dev, pl.x, workspace, (cudaStream_t)stream, &xr))) return st;
-    if ((st = operand(w, w_dev, pl.w, workspace, (cudaStream_t)stream, &wr))) return st;
+    PackJobs jobs;
+    if ((st = operand(x, x_dev, pl.x, workspace, &jobs, &xr)) || (st = operand(w, w_dev, pl.w, workspace, &jobs, &wr)) ||
+        (st = run_packs(jobs, (cudaStream_t)stream)))
+        return st;
     Product pr;
     pr.ma = m, pr.nb = n, pr.k = k;
     pr.a = {xr.p, xr.rs, xr.cs};
@@ -457,9 +485,13 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         if (cudaMemsetAsync(dbias_dev, 0, (size_t)(n * channel_elem_size(p->bias_dtype)), s) != cudaSuccess)
             return CONV_ERR_CUDA;
     }
-    if (dx && m > 0 && k > 0) {
-        MatRef wr;
-        if ((st = operand(w, w_dev, pl.w, workspace, s, &wr))) return st;
+    MatRef xr, wr;
+    PackJobs jobs;
+    const bool want_dx = dx && m > 0 && k > 0, want_dw = dw && n > 0 && k > 0;
+    if ((want_dx && (st = operand(w, w_dev, pl.w, workspace, &jobs, &wr))) ||
+        (want_dw && (st = operand(x, x_dev, pl.x, workspace, &jobs, &xr))) || (st = run_packs(jobs, s)))
+        return st;
+    if (want_dx) {
         Product pr;
         pr.ma = m, pr.nb = k, pr.k = n;
         pr.a = {dz.p, dz.rs, dz.cs};
@@ -469,9 +501,7 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         pr.d = dx_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dx->dtype;
         if ((st = product_launch(pr, (char *)workspace + pl.sums_off, stream))) return st;
     }
-    if (dw && n > 0 && k > 0) {
-        MatRef xr;
-        if ((st = operand(x, x_dev, pl.x, workspace, s, &xr))) return st;
+    if (want_dw) {
         Product pr;
         pr.ma = n, pr.nb = k, pr.k = m;
         pr.a = {dz.p, dz.cs, dz.rs};
