@@ -1,8 +1,11 @@
-"""In-tree build of libint8conv.so (nvcc, sm_103a only).
+"""In-tree build of libint8conv.so (nvcc, sm_103a only) and of the channel
+operators' Python binding.
 
 Every translation unit under ``csrc/`` is compiled in parallel into
-``_build/`` and linked into ``libint8conv.so`` next to this file.  Rebuilds
-only when a source or header is newer than the library.
+``_build/`` and linked into ``libint8conv.so`` next to this file;
+``csrc/python/channel_binding.cpp`` is compiled against torch's headers into
+``_channel.so``, which loads the library.  Rebuilds only what is older than a
+source or header.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint8conv.so")
+BINDING_SRC = os.path.join(CSRC, "python", "channel_binding.cpp")
+BINDING = os.path.join(PKG, "_channel.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -47,7 +53,39 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def build_binding() -> None:
+    """_channel.so; needs the library next to it to link with."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-o", tmp, BINDING_SRC, "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           "-L", PKG, "-l:libint8conv.so", "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    build_library(force, verbose, extra_flags)
+    if force or not binding_up_to_date():
+        build_binding()
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

@@ -257,3 +257,18 @@ def test_layer_norm_gradients_are_difference_quotients():
             q[i] = (up - (dy * oc.layer_norm(x, gain, shift)[0]).sum()) / (2 * h)
             arr[i] = keep
         assert np.max(np.abs(q - grad_)) < 1e-7
+
+
+def test_binding_refuses_what_no_descriptor_can_say(ic):
+    torch = pytest.importorskip("torch")
+    x, w = torch.ones(2, 8, dtype=torch.float16), torch.ones(4, 8, dtype=torch.float16)
+    with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+        ic.conv_linear(x, w)
+    with pytest.raises(TypeError):
+        ic.conv_linear([1.0], w)
+    with pytest.raises(ValueError, match="x is required"):
+        ic.conv_layer_norm(None)
+    with pytest.raises(ValueError, match="unknown activation"):
+        ic.conv_linear(x, w, activation="tanh")
+    with pytest.raises(ValueError):
+        ic.conv_layer_norm_grad(x, x, None, None, None, dx=x)
