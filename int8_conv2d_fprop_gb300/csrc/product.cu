@@ -43,6 +43,7 @@ constexpr int kSlotBytes = 2048;   // staging of one epilogue warp
 constexpr int kBiasBytes = kEpilogueWarps * 128;
 constexpr int kRingBytes = 196608;
 constexpr int kMaxSplit = 8;       // portable cluster size
+constexpr int64_t kSms = 152;      // of the part this library is for, whatever the device: plans fix workspace sizes
 
 // How an output, residual or pre-activation matrix is walked.
 enum Walk : int32_t {
@@ -68,6 +69,7 @@ struct ProductArgs {
     int32_t k_steps;
     int32_t tile_b;              // a multiple of 32
     int32_t tiles_a, tiles_b;
+    int32_t rows_a;              // rows of a from one tile to the next (and in it)
     int32_t a_mn, b_mn;          // operand's own dim (not k) contiguous
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
@@ -289,6 +291,7 @@ __device__ __noinline__ void slot_to_any(Side s, WarpTile t, int c, int cols) {
     if (s.walk == kWalkAlongA) {
         const int64_t at = (int64_t)(t.row0 + t.lane) * s.sa + (int64_t)(t.b0 + c) * s.sb;
         if (t.lane < t.rows)
+#pragma unroll 8
             for (int j = 0; j < cols; ++j) {
                 if (wide) ((uint32_t *)s.p)[at + j * s.sb] = ptx::ld_shared_b32(at32(t.slot, t.lane, j));
                 else ((uint16_t *)s.p)[at + j * s.sb] = ld_shared_b16(at16(t.slot, t.lane, j));
@@ -528,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int cluster_size = kPair ? 2 : a.split;
     const int first = blockIdx.x / cluster_size, step = gridDim.x / cluster_size;
     const int tiles = a.tiles_a * a.tiles_b, units = tiles * a.parts;
-    constexpr int kRowsPerTile = kPair ? 2 * kTileA : kTileA;
     int k_lo = 0, k_hi = a.k_steps;
     if (!kPair && a.split > 1) {
         k_lo = (int)((int64_t)a.k_steps * rank / a.split);
@@ -549,7 +551,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
     if (threadIdx.x == 0) {
         ptx::prefetch_tensormap(&a.map_a);
-        ptx::prefetch_tensormap(&a.map_b);
         for (int i = 0; i < a.stages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
             ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
@@ -560,12 +561,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         ctl->abort_flag = 0;
         ptx::fence_mbar_init();
+    } else if (threadIdx.x == 96) {
+        ptx::prefetch_tensormap(&a.map_b);
     }
-    if (warp == 2) tmem_alloc<kPair>(ptx::smem_addr(&ctl->tmem_base), 512);
-    ptx::tc_fence_before();
-    if (kPair || a.split > 1) cluster_sync(); else __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)&ctl->tmem_base;
+    __syncthreads();
+    // Tensor memory is allocated while the first loads are on their way: the
+    // loading warps of a single CTA do not wait for it.  (Those of a pair
+    // signal each other's barriers, which have to be there first.)
+    uint32_t tmem = 0;
+    if (kPair || !(warp == 0 || warp == 3)) {
+        if (warp == 2) tmem_alloc<kPair>(ptx::smem_addr(&ctl->tmem_base), 512);
+        ptx::tc_fence_before();
+        if (kPair) cluster_sync();
+        else asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 64) : "memory");
+        ptx::tc_fence_after();
+        tmem = *(volatile uint32_t *)&ctl->tmem_base;
+    }
     // nothing above reads or writes global memory
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool mn = is_b ? a.b_mn : a.a_mn;
         const CUtensorMap *map = is_b ? &a.map_b : &a.map_a;
         const int boxes = is_b ? a.b_boxes : 2;
-        const uint32_t bytes = (kPair ? 2u : 1u) * (mn ? boxes * 8192u : is_b ? a.b_rows * 128u : 16384u);
+        const uint32_t bytes = (kPair ? 2u : 1u) * (mn ? boxes * 8192u : (is_b ? a.b_rows : kPair ? kTileA : a.rows_a) * 128u);
         Ring rg;
         int64_t issued = 0;
         bool ok = true;
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int ia, ib;
             tile_at(a, run_of(t), &ia, &ib);
             const int own = is_b ? ib * a.tile_b + (kPair ? rank * a.b_rows : 0)
-                                 : ia * kRowsPerTile + (kPair ? rank * kTileA : 0);
+                                 : ia * a.rows_a + (kPair ? rank * kTileA : 0);
             for (int ks = k_lo; ks < k_hi; ++ks) {
                 if (!wait_phase(ptx::smem_addr(&ctl->empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
                     ok = false;
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int ia, ib;
             tile_at(a, run_of(t), &ia, &ib);
             const int slot = n & 1;
-            const int row0 = ia * kRowsPerTile + (kPair ? rank * kTileA : 0) + quad * 32;
+            const int row0 = ia * a.rows_a + (kPair ? rank * kTileA : 0) + quad * 32;
             // this warp's biases, loaded while the tile is being summed
             float bias[kChunks];
 #pragma unroll
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ptx::tmem_st_wait();
             }
             wt.row0 = row0;
-            wt.rows = min(32, a.ma - row0);
+            wt.rows = min(32, min(a.ma, (ia + 1) * a.rows_a) - row0);
             if (!kPair && a.split > 1) {
                 // partial sums to shared memory [column][row], over the
                 // ring: its loads and MMAs are done
@@ -735,16 +746,28 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int units = a.tile_b / 8 * 4;
             for (int u = e * a.split + (int)rank; u < units; u += kEpilogueWarps * a.split) {
                 const int quad = u & 3, c = (u >> 2) * 8;
-                wt.row0 = ia * kTileA + quad * 32;
-                wt.rows = min(32, a.ma - wt.row0);
+                wt.row0 = ia * a.rows_a + quad * 32;
+                wt.rows = min(32, min(a.ma, (ia + 1) * a.rows_a) - wt.row0);
                 wt.b0 = ib * a.tile_b + c;
                 wt.cols = min(8, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
                 float v[8] = {};
-                for (int r = 0; r < a.split; ++r) {
-                    const uint32_t src = map_to_rank(ring + (c * kTileA + quad * 32 + lane) * 4, r);
+#pragma unroll 1
+                for (int r0 = 0; r0 < a.split; r0 += 4) {
+                    float q[4][8];  // 32 loads in flight
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += ld_cluster_f32(src + j * kTileA * 4);
+                    for (int r = 0; r < 4; ++r) {
+                        // (splits are powers of two: of 2 CTAs, the first is read twice and not added)
+                        const uint32_t src = map_to_rank(ring + (c * kTileA + quad * 32 + lane) * 4, r0 + r < a.split ? r0 + r : 0);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) q[r][j] = ld_cluster_f32(src + j * kTileA * 4);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r0 + r < a.split) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] += q[r][j];
+                        }
                 }
                 finish8<kAct>(a, wt, v);
             }
@@ -854,10 +877,12 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Planned for the 152 SMs of the part this library is for, whatever the
-// device, so that workspace sizes do not depend on it.
+// Clusters of one-CTA-per-SM blocks that run at once (as
+// cudaOccupancyMaxActiveClusters counts them on the 152 SMs: processor
+// clusters are not all of one size).
+int64_t active_clusters(int size) { return size == 1 ? kSms : size == 2 ? kSms / 2 : size == 4 ? 36 : 15; }
+
 ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
-    constexpr int64_t kSms = 152;
     ProductPlan pl;
     // Few rows: the long dim becomes the tile's 128 lanes and the few rows its
     // columns, so that no lanes idle and every CTA streams its own weights.
@@ -905,7 +930,7 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
     pl.tiles_a = cdiv(ma, kTileA);
     pl.tiles_b = cdiv(nb, pl.tile_b);
     const int64_t tiles = pl.tiles_a * pl.tiles_b;
-    while (pl.split < kMaxSplit && tiles * pl.split * 2 <= kSms && k_steps >= pl.split * 4) pl.split *= 2;
+    while (pl.split < kMaxSplit && tiles <= active_clusters(pl.split * 2) && k_steps >= pl.split * 4) pl.split *= 2;
     return pl;
 }
 
@@ -941,11 +966,25 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     a.tile_b = pl.tile_b;
     a.tiles_a = (int32_t)pl.tiles_a;
     a.tiles_b = (int32_t)pl.tiles_b;
+    a.rows_a = pair ? 256 : kTileA;
     a.split = pl.split;
     a.parts = pl.parts;
     a.part = (float *)workspace;
+    if (!pair && !a.a_mn && pl.parts == 1) {
+        // Fewer tiles than SMs, each a stream of operand A: shorter tiles for
+        // more SMs (at least 64 rows, which keeps the loads of B the smaller
+        // part; whole 32-row stores where TMA makes them, since it would not
+        // stop at a tile's end).
+        const int64_t most = active_clusters(pl.split) / pl.tiles_b;
+        const bool sent = a.d.walk == kWalkRows || a.pre.walk == kWalkRows;
+        const int64_t rows = round_up(std::max<int64_t>(cdiv(pr.ma, most), 64), sent ? 32 : 4);
+        if (rows < kTileA && pl.tiles_a < most) {
+            a.rows_a = (int32_t)rows;
+            a.tiles_a = (int32_t)cdiv(pr.ma, rows);
+        }
+    }
     a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
-    const int64_t units = pl.tiles_a * pl.tiles_b * pl.parts;
+    const int64_t units = (int64_t)a.tiles_a * a.tiles_b * pl.parts;
     const int sms = device_sm_count(), cluster = pair ? 2 : a.split;
     const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
@@ -959,7 +998,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     if (a.k_steps > 0) {
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         const bool ok_a = a.a_mn ? encode(&a.map_a, pr.in_dtype, pr.a.p, pr.ma, pr.k, pr.a.s_k, 64, kStepK, sw)
-                                 : encode(&a.map_a, pr.in_dtype, pr.a.p, pr.k, pr.ma, pr.a.s_mn, kStepK, kTileA, sw);
+                                 : encode(&a.map_a, pr.in_dtype, pr.a.p, pr.k, pr.ma, pr.a.s_mn, kStepK, pair ? kTileA : a.rows_a, sw);
         const bool ok_b = a.b_mn ? encode(&a.map_b, pr.in_dtype, pr.b.p, pr.nb, pr.k, pr.b.s_k, 64, kStepK, sw)
                                  : encode(&a.map_b, pr.in_dtype, pr.b.p, pr.k, pr.nb, pr.b.s_mn, kStepK, a.b_rows, sw);
         if (!ok_a || !ok_b) return CONV_ERR_CUDA;
