@@ -74,6 +74,7 @@ struct ProductArgs {
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
+    int32_t spin;                // short sums: waits poll (latency counts, and nothing else wants the issue slots)
     int32_t parts;               // runs of k, each summed to `part` (1: none)
     float *part;                 // [run][tile][128-row half][column][row of 128]
     uint32_t idesc;
@@ -192,12 +193,12 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
 // Bounded wait; false when the CTA is giving up (the status word then holds
 // the timeout).
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag, uint64_t limit_ns,
-                                       int *status) {
+                                       int *status, bool spin) {
     const uint64_t t0 = ptx::global_timer_ns();
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (ptx::mbar_try_wait(bar, parity)) return true;
+            if (spin ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (ptx::global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
@@ -207,10 +208,12 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
 }
 
+// spin: poll without suspending (a suspended wait resumes some time after the
+// phase completes).
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag,
-                                           uint64_t limit_ns, int *status) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    return wait_slow(bar, parity, abort_flag, limit_ns, status);
+                                           uint64_t limit_ns, int *status, bool spin = false) {
+    if (spin ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, abort_flag, limit_ns, status, spin);
 }
 
 struct Ring {
@@ -623,11 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         // Every stage is released by the MMAs that read it; the releases
         // reach both CTAs of a pair, so they have to be in before either
-        // leaves.  After a time-out the copies have to land first (in a pair
-        // on the leader's barriers; the cluster barrier below keeps both
-        // CTAs), and no release may come.
+        // leaves.  (A single CTA's are in before its last accumulator is.)
+        // After a time-out the copies have to land first (in a pair on the
+        // leader's barriers; the cluster barrier below keeps both CTAs), and
+        // no release may come.
         const bool drain_copies = *abort_flag && (!kPair || rank == 0);
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < a.stages && (kPair || drain_copies); ++s) {
             const int64_t n = issued / a.stages + (s < issued % a.stages ? 1 : 0);
             if (n == 0) continue;
             const uint32_t bar = ptx::smem_addr(drain_copies ? &ctl->full[s] : &ctl->empty[s]);
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             ptx::tc_fence_after();
             const uint32_t d = tmem + slot * kMaxTileB;
             for (int ks = k_lo; ks < k_hi; ++ks) {
-                if (!wait_phase(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
+                if (!wait_phase(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status, a.spin)) {
                     ok = false;
                     break;
                 }
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 const int c = (part + kParts * i) * 32;
                 bias[i] = c < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + c, lane) : 0.0f;
             }
-            if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) break;
+            if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status, a.spin)) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
             if (k_lo == k_hi) {  // no products: the accumulator was never written
@@ -984,6 +988,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
         }
     }
     a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
+    a.spin = !pair && a.k_steps <= 32 * a.split;
     const int64_t units = (int64_t)a.tiles_a * a.tiles_b * pl.parts;
     const int sms = device_sm_count(), cluster = pair ? 2 : a.split;
     const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
