@@ -84,6 +84,10 @@ struct ProductPlan {
     size_t part_bytes = 0; // a multiple of 256
 };
 
+// The product of up to four rows of a by CUDA cores (product_rows.cu).
+bool product_rows_applies(const Product &pr);
+conv_status product_rows_launch(const Product &pr, void *stream);
+
 ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k);
 
 // workspace: part_bytes of the plan.

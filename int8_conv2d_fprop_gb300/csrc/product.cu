@@ -940,6 +940,7 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
 
 conv_status product_launch(const Product &given, void *workspace, void *stream) {
     if (given.ma == 0 || given.nb == 0) return CONV_OK;
+    if (product_rows_applies(given)) return product_rows_launch(given, stream);
     Product pr = given;
     const ProductPlan pl = product_plan(pr.ma, pr.nb, pr.k);
     if (pl.tiles_a * pl.tiles_b * pl.parts > INT32_MAX / kMaxSplit) return CONV_ERR_TOO_LARGE;

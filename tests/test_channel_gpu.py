@@ -98,7 +98,9 @@ SIZES = [(1, 1, 1), (1, 8, 16), (1, 64, 128), (1, 1000, 257), (1, 4096, 512), (2
          (200, 16, 24), (255, 2048, 96), (256, 256, 256), (257, 72, 264), (300, 1, 300), (513, 520, 777),
          (1000, 333, 70), (2048, 64, 512), (5000, 96, 48),
          # few tiles and a long k: summed in runs and joined
-         (300, 20488, 520), (257, 30001, 130)]
+         (300, 20488, 520), (257, 30001, 130),
+         # up to four rows
+         (1, 72, 64), (2, 67, 65), (3, 4096, 300), (4, 1003, 1000), (1, 8200, 67), (4, 64, 64), (5, 64, 64)]
 
 
 @pytest.mark.parametrize("m,k,n", SIZES)
@@ -109,7 +111,7 @@ def test_linear_sizes(ic, m, k, n, dt):
 
 @pytest.mark.parametrize("act,dt,out", list(itertools.product(ACTS, (BF16, F16), (None, F32))))
 def test_linear_activations_and_types(ic, act, dt, out):
-    for m in (3, 150):
+    for m in (3, 7, 150):
         run_linear(ic, m, 200, 136, dt, act, bias_dt=F32, residual=True, preact=True, out_dt=out)
         run_linear(ic, m, 64, 40, dt, act, bias=False, out_dt=out, scale=20.0)
 
@@ -125,14 +127,14 @@ LAYOUTS = ("rows", "padded", "odd", "shifted", "cols", "cols_odd", "spread")
 
 @pytest.mark.parametrize("lx,lw", list(itertools.product(LAYOUTS, LAYOUTS)))
 def test_linear_operand_layouts(ic, lx, lw):
-    for m, k, n in ((5, 72, 136), (140, 136, 300), (9, 67, 45), (131, 70, 139), (260, 131, 261)):
+    for m, k, n in ((2, 72, 136), (3, 67, 77), (5, 72, 136), (140, 136, 300), (9, 67, 45), (131, 70, 139), (260, 131, 261)):
         run_linear(ic, m, k, n, F16, "relu", lx=lx, lw=lw)
 
 
 @pytest.mark.parametrize("ly", LAYOUTS)
 @pytest.mark.parametrize("out", [BF16, F32])
 def test_linear_output_layouts(ic, ly, out):
-    for m, k, n in ((1, 64, 33), (9, 72, 137), (140, 136, 301), (300, 64, 520)):
+    for m, k, n in ((1, 64, 33), (2, 72, 133), (9, 72, 137), (140, 136, 301), (300, 64, 520)):
         run_linear(ic, m, k, n, BF16, "silu", residual=True, preact=True, ly=ly, out_dt=out)
 
 
