@@ -71,6 +71,7 @@ struct ProductArgs {
     int32_t tiles_a, tiles_b;
     int32_t rows_a;              // rows of a from one tile to the next (and in it)
     int32_t a_mn, b_mn;          // operand's own dim (not k) contiguous
+    int32_t a_blocks, b_blocks;  // own dim contiguous and whole blocks of 64: all of a k-step's boxes in one load
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
@@ -125,6 +126,21 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap,
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *tmap, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -592,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool mn = is_b ? a.b_mn : a.a_mn;
         const CUtensorMap *map = is_b ? &a.map_b : &a.map_a;
         const int boxes = is_b ? a.b_boxes : 2;
+        const bool blocks = is_b ? a.b_blocks : a.a_blocks;
         const uint32_t bytes = (kPair ? 2u : 1u) * (mn ? boxes * 8192u : (is_b ? a.b_rows : kPair ? kTileA : a.rows_a) * 128u);
         Ring rg;
         int64_t issued = 0;
@@ -615,7 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     if constexpr (kPair) tma_load_2d_pair(to, map, x, y, bar);
                     else ptx::tma_load_2d(to, map, x, y, bar);
                 };
-                if (mn) {
+                if (mn && blocks) {
+                    if constexpr (kPair) tma_load_3d_pair(dst, map, 0, k0, own / 64, bar);
+                    else tma_load_3d(dst, map, 0, k0, own / 64, bar);
+                } else if (mn) {
                     for (int i = 0; i < boxes; ++i) load(dst + i * 8192, own + 64 * i, k0);
                 } else {
                     load(dst, k0, own);
@@ -862,6 +882,20 @@ bool encode(CUtensorMap *m, int32_t dtype, const void *p, int64_t inner, int64_t
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of an operand whose own dim is contiguous and made of whole blocks of
+// 64: [block][k][64], `boxes` blocks of 64 k per load.
+bool encode_blocks(CUtensorMap *m, int32_t dtype, const void *p, int64_t own, int64_t k, int64_t stride, int boxes) {
+    auto enc = tiled_encoder();
+    if (!enc) return false;
+    if (k == 1) stride = round_up(own, 8);
+    const cuuint64_t dims[3] = {64, (cuuint64_t)k, (cuuint64_t)(own / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)(stride * 2), 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kStepK, (cuuint32_t)boxes}, ones[3] = {1, 1, 1};
+    return enc(m, dtype == CONV_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 Side make_side(const void *p, int64_t sa, int64_t sb, int32_t dtype, int64_t ma, int64_t nb) {
     Side s{const_cast<void *>(p), sa, sb, dtype, kWalkNone};
     if (!p) return s;
@@ -905,18 +939,8 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
     if (nb > 64 && ma > 128 && (pair_tiles * 2 >= kSms || pair_tiles * k_steps >= kSms / 2 * 16)) {
         pl.pair = true;
         pl.tile_b = (int32_t)wide;
-        if (pair_tiles * 2 >= kSms && nb > 128) {
-            // The width that wastes least in the last round of tiles; 32
-            // columns stand for a tile's share of operand A's loads.
-            int64_t best = INT64_MAX;
-            for (int nt = 256; nt >= 128; nt -= 32) {
-                const int64_t rounds = cdiv(cdiv(ma, 256) * cdiv(nb, nt), kSms / 2);
-                if (rounds * (nt + 32) < best) {
-                    best = rounds * (nt + 32);
-                    pl.tile_b = nt;
-                }
-            }
-        }
+        // (a k-step takes 0.34 us at 256 columns and still 0.31 at 192 and 0.30
+        // at 128: narrower tiles for a fuller last round do not pay)
         pl.tiles_a = cdiv(ma, 256);
         pl.tiles_b = cdiv(nb, pl.tile_b);
         const int64_t tiles = pl.tiles_a * pl.tiles_b;
@@ -1003,9 +1027,14 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
 
     if (a.k_steps > 0) {
         const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-        const bool ok_a = a.a_mn ? encode(&a.map_a, pr.in_dtype, pr.a.p, pr.ma, pr.k, pr.a.s_k, 64, kStepK, sw)
+        // (blocks as the outermost dim step by 128 bytes; a tile starts on one)
+        a.a_blocks = a.a_mn && pr.ma % 64 == 0;
+        a.b_blocks = a.b_mn && pr.nb % 64 == 0 && a.tile_b % 64 == 0 && a.b_rows % 64 == 0;
+        const bool ok_a = a.a_blocks ? encode_blocks(&a.map_a, pr.in_dtype, pr.a.p, pr.ma, pr.k, pr.a.s_k, 2)
+                          : a.a_mn ? encode(&a.map_a, pr.in_dtype, pr.a.p, pr.ma, pr.k, pr.a.s_k, 64, kStepK, sw)
                                  : encode(&a.map_a, pr.in_dtype, pr.a.p, pr.k, pr.ma, pr.a.s_mn, kStepK, pair ? kTileA : a.rows_a, sw);
-        const bool ok_b = a.b_mn ? encode(&a.map_b, pr.in_dtype, pr.b.p, pr.nb, pr.k, pr.b.s_k, 64, kStepK, sw)
+        const bool ok_b = a.b_blocks ? encode_blocks(&a.map_b, pr.in_dtype, pr.b.p, pr.nb, pr.k, pr.b.s_k, a.b_boxes)
+                          : a.b_mn ? encode(&a.map_b, pr.in_dtype, pr.b.p, pr.nb, pr.k, pr.b.s_k, 64, kStepK, sw)
                                  : encode(&a.map_b, pr.in_dtype, pr.b.p, pr.k, pr.nb, pr.b.s_mn, kStepK, a.b_rows, sw);
         if (!ok_a || !ok_b) return CONV_ERR_CUDA;
     }
