@@ -80,7 +80,8 @@ struct ProductPlan {
     int32_t tile_b = 0;
     int64_t tiles_a = 0, tiles_b = 0;
     int32_t split = 1;     // CTAs of a cluster that share a tile along k
-    int32_t parts = 1;     // runs of k summed apart and joined by a second kernel
+    int32_t parts = 1;     // runs of k, summed apart and joined by a second kernel, ...
+    int64_t full = 0;      // ... of the tiles from this one on
     size_t part_bytes = 0; // a multiple of 256
 };
 

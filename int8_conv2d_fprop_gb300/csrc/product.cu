@@ -76,7 +76,8 @@ struct ProductArgs {
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
     int32_t spin;                // short sums: waits poll (latency counts, and nothing else wants the issue slots)
-    int32_t parts;               // runs of k, each summed to `part` (1: none)
+    int32_t parts;               // runs of k, each summed to `part` (1: none),
+    int32_t full;                // of the tiles from this one on
     float *part;                 // [run][tile][128-row half][column][row of 128]
     uint32_t idesc;
     uint64_t wait_limit_ns;
@@ -549,21 +550,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint32_t rank = (kPair || a.split > 1) ? cluster_rank() : 0;
     const int cluster_size = kPair ? 2 : a.split;
     const int first = blockIdx.x / cluster_size, step = gridDim.x / cluster_size;
-    const int tiles = a.tiles_a * a.tiles_b, units = tiles * a.parts;
+    const int tiles = a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
     int k_lo = 0, k_hi = a.k_steps;
     if (!kPair && a.split > 1) {
         k_lo = (int)((int64_t)a.k_steps * rank / a.split);
         k_hi = (int)((int64_t)a.k_steps * (rank + 1) / a.split);
     }
 
-    // unit u: tile u mod tiles of run u / tiles (the runs of one stretch of k
-    // work side by side, on the same rows of the operands)
+    // unit u: a whole tile, then the runs of the cut tiles (the runs of one
+    // stretch of k side by side, on the same rows of the operands); sets the
+    // k-steps, returns the tile
     auto run_of = [&](int u) {
         if (a.parts > 1) {
-            const int p = u / tiles;
-            k_lo = (int)((int64_t)a.k_steps * p / a.parts);
-            k_hi = (int)((int64_t)a.k_steps * (p + 1) / a.parts);
-            u -= p * tiles;
+            k_lo = 0, k_hi = a.k_steps;
+            if (u >= a.full) {
+                const int cut = tiles - a.full, p = (u - a.full) / cut;
+                k_lo = (int)((int64_t)a.k_steps * p / a.parts);
+                k_hi = (int)((int64_t)a.k_steps * (p + 1) / a.parts);
+                u -= p * cut;
+            }
         }
         return u;
     };
@@ -735,10 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 wt.b0 = ib * a.tile_b + c;
                 wt.cols = min(32, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
-                if (a.parts > 1) {
+                if (t >= a.full) {
                     float v[32];
                     load_sums(acc + c, v);
-                    float *p = a.part + (((int64_t)t * (kPair ? 2 : 1) + (kPair ? rank : 0)) * a.tile_b + c) * kTileA + quad * 32 + lane;
+                    float *p = a.part + (((int64_t)(t - a.full) * (kPair ? 2 : 1) + (kPair ? rank : 0)) * a.tile_b + c) * kTileA + quad * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
                     continue;
@@ -812,7 +817,7 @@ template <int kAct>
 __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant__ ProductArgs a, int rows_per_tile) {
     __shared__ __align__(16) float bias[8][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int tiles = a.tiles_a * a.tiles_b;
+    const int tiles = a.tiles_a * a.tiles_b - a.full;  // those cut
     // unit: 8 columns of 32 rows, columns fastest
     const int per_half = a.tile_b / 8 * 4, halves = rows_per_tile / kTileA;
     const int u = blockIdx.x * 8 + warp;
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant
     const int quad = in / (a.tile_b / 8), c = (in - quad * (a.tile_b / 8)) * 8;
     const int t = th / halves, half = th - t * halves;
     int ia, ib;
-    tile_at(a, t, &ia, &ib);
+    tile_at(a, a.full + t, &ia, &ib);
     WarpTile wt;
     wt.lane = lane;
     wt.slot = 0;  // (unused by 8-column tiles)
@@ -944,9 +949,19 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
         pl.tiles_a = cdiv(ma, 256);
         pl.tiles_b = cdiv(nb, pl.tile_b);
         const int64_t tiles = pl.tiles_a * pl.tiles_b;
-        if (tiles * 2 < kSms) {
-            pl.parts = (int32_t)std::max<int64_t>(1, std::min(kSms / 2 / tiles, k_steps / 8));
-            if (pl.parts > 1) pl.part_bytes = (size_t)(pl.parts * tiles * 256 * pl.tile_b * 4);
+        // Fewer tiles than pairs: all of them in runs.  A last round that
+        // leaves half the pairs idle or more: its tiles in runs, where that
+        // saves more than the joining kernel takes (about 8 us, 24 k-steps).
+        const int64_t last = tiles % (kSms / 2);
+        int64_t parts = 1;
+        if (tiles * 2 < kSms) parts = std::min(kSms / 2 / tiles, k_steps / 8);
+        else if (last > 0) parts = std::min<int64_t>(kSms / 2 / last, 8);
+        if (parts > 1 && tiles * 2 >= kSms && k_steps - k_steps / parts < 40) parts = 1;
+        pl.full = tiles;
+        if (parts > 1) {
+            pl.parts = (int32_t)parts;
+            pl.full = tiles * 2 < kSms ? 0 : tiles - last;
+            pl.part_bytes = (size_t)(parts * (tiles - pl.full) * 256 * pl.tile_b * 4);
         }
         return pl;
     }
@@ -967,7 +982,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     if (product_rows_applies(given)) return product_rows_launch(given, stream);
     Product pr = given;
     const ProductPlan pl = product_plan(pr.ma, pr.nb, pr.k);
-    if (pl.tiles_a * pl.tiles_b * pl.parts > INT32_MAX / kMaxSplit) return CONV_ERR_TOO_LARGE;
+    if (pl.tiles_a * pl.tiles_b > INT32_MAX / kMaxSplit) return CONV_ERR_TOO_LARGE;
     if (pl.swap) {
         std::swap(pr.ma, pr.nb);
         std::swap(pr.a, pr.b);
@@ -1014,7 +1029,9 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     }
     a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
     a.spin = !pair && a.k_steps <= 32 * a.split;
-    const int64_t units = (int64_t)a.tiles_a * a.tiles_b * pl.parts;
+    const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b;
+    a.full = (int32_t)(pl.parts > 1 ? pl.full : tiles);
+    const int64_t units = a.full + (tiles - a.full) * pl.parts;
     const int sms = device_sm_count(), cluster = pair ? 2 : a.split;
     const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
@@ -1079,7 +1096,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
         static const Join joins[5] = {product_join_kernel<CONV_ACT_NONE>, product_join_kernel<CONV_ACT_RELU>,
                                       product_join_kernel<CONV_ACT_GELU>, product_join_kernel<CONV_ACT_GELU_TANH>,
                                       product_join_kernel<CONV_ACT_SILU>};
-        const int64_t warps = pl.tiles_a * pl.tiles_b * (tile_a / 32) * (a.tile_b / 8);
+        const int64_t warps = (tiles - a.full) * (tile_a / 32) * (a.tile_b / 8);
         if (!launch_behind(joins[pr.act], dim3((unsigned)cdiv(warps, 8)), 256, 0, (cudaStream_t)stream, a, tile_a))
             return CONV_ERR_CUDA;
     }

@@ -265,7 +265,9 @@ def run_linear_grad(ic, m, k, n, dt=BF16, act="none", types=(None, None, F32), l
 
 
 GRAD_SIZES = [(1, 1, 1), (1, 64, 40), (2, 200, 8), (9, 8, 9), (31, 65, 33), (64, 64, 64), (128, 256, 128),
-              (130, 70, 257), (333, 192, 257), (512, 24, 520), (1000, 128, 64), (4099, 64, 72), (700, 600, 500), (20011, 512, 520)]
+              (130, 70, 257), (333, 192, 257), (512, 24, 520), (1000, 128, 64), (4099, 64, 72), (700, 600, 500), (20011, 512, 520),
+              # a last round of tiles cut into runs
+              (5130, 2100, 2568)]
 
 
 @pytest.mark.parametrize("m,k,n", GRAD_SIZES)
