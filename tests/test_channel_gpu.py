@@ -568,3 +568,48 @@ def test_layer_norm_grad_is_the_difference_quotient(ic):
             cut = 64 * h * h * float(dy.abs().sum(1).max() * rstd.max() ** 3) if which == 0 else 0.0
             rounding = float((dy.abs().double() * (f[0].abs() + 4)).sum()) * 2.0 ** -20 / (2 * h)
             assert abs(quotient - gradient) <= cut + rounding + 2.0 ** -18 * abs(gradient)
+
+
+# ---------------------------------------------------------------- together
+def test_convolution_and_channel_block(ic):
+    """The example's block against float32 autograd: every stored tensor on the
+    way is rounded to bfloat16 (2^-9 of its norm at random), and a gradient has
+    at most six such tensors behind it."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import channel_block
+    for shape in ((2, 64, 14, 96, 384), (1, 32, 9, 40, 136)):
+        for name, far in channel_block.compare(*shape).items():
+            assert far < 6 * 2.0 ** -8, (name, far)
+
+
+def test_offsets_beyond_32_bits(ic):
+    """Rows 2^31 + 16 elements apart: byte offsets pass 32 bits and element
+    offsets pass 31."""
+    ld, m, c = (1 << 31) + 16, 3, 72
+    buf = torch.empty((m - 1) * ld + 4096, device="cuda", dtype=BF16)
+    x = buf.as_strided((m, c), (ld, 1))
+    out = torch.empty((m - 1) * ld + 4096, device="cuda", dtype=BF16).as_strided((m, 104), (ld, 1))
+    g = gen(60)
+    v, w = randn(g, m, c).to(BF16), randn(g, 104, c).to(BF16)
+    x.copy_(v)
+    assert torch.equal(ic.conv_linear(x, w, out=out), ic.conv_linear(v, w))
+    many = torch.empty(200, c, device="cuda", dtype=BF16)
+    many[:] = v[1]
+    assert torch.equal(ic.conv_linear(many, w)[0], ic.conv_linear(torch.cat([v, many]), w)[1])
+    y = out[:, :c]
+    assert torch.equal(ic.conv_layer_norm(x, out=y), ic.conv_layer_norm(v))
+    mean, rstd = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    ic.conv_layer_norm(v, mean=mean, rstd=rstd)
+    dy = randn(g, m, c).to(BF16)
+    a, b = [torch.empty_like(v)] + [torch.empty(c, device="cuda") for _ in range(2)], torch.empty(c, device="cuda")
+    ic.conv_layer_norm_grad(dy, v, None, mean, rstd, dx=a[0], dgain=a[1], dshift=a[2])
+    ic.conv_layer_norm_grad(dy, x, None, mean, rstd, dx=y, dgain=b)
+    assert torch.equal(y, a[0]) and torch.equal(b, a[1])
+    dx, dw = out[:, :c], torch.empty_like(w)
+    dz = randn(g, m, 104).to(BF16)
+    ic.conv_linear_grad(dz, x, w, dx=dx, dw=dw)
+    want = torch.empty_like(v), torch.empty_like(w)
+    ic.conv_linear_grad(dz, v, w, dx=want[0], dw=want[1])
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
