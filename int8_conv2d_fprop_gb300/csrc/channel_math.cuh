@@ -47,6 +47,13 @@ __device__ __forceinline__ void unpack2(uint32_t w, int32_t dtype, float *lo, fl
     }
 }
 
+// The same with the type known: for loops that branch on it once.
+template <bool kHalf>
+__device__ __forceinline__ uint4 pack8(const float *v) {
+    constexpr int32_t t = kHalf ? CONV_FLOAT16 : CONV_BFLOAT16;
+    return make_uint4(pack2(v[0], v[1], t), pack2(v[2], v[3], t), pack2(v[4], v[5], t), pack2(v[6], v[7], t));
+}
+
 __device__ __forceinline__ uint4 pack8(const float *v, int32_t dtype) {
     return make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype),
                       pack2(v[6], v[7], dtype));

@@ -73,6 +73,7 @@ struct ProductArgs {
     int32_t a_mn, b_mn;          // operand's own dim (not k) contiguous
     int32_t a_blocks, b_blocks;  // own dim contiguous and whole blocks of 64: all of a k-step's boxes in one load
     int32_t b_rows, b_boxes;     // rows of B per CTA; TMA boxes per k-step
+    int32_t slots;               // staging slots of an epilogue warp: 2 where a residual is loaded ahead
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
     int32_t spin;                // short sums: waits poll (latency counts, and nothing else wants the issue slots)
@@ -381,8 +382,13 @@ __device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *ma
     const bool rows = s.walk == kWalkRows && t.cols == 32;
     if (s.dtype != CONV_FLOAT32) {
         free_slot(t);
+        if (s.dtype == CONV_FLOAT16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane, i), pack8(v + 8 * i, s.dtype));
+            for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane, i), pack8<true>(v + 8 * i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane, i), pack8<false>(v + 8 * i));
+        }
         if (rows) {
             send_slot(map, t, 0);
         } else {
@@ -476,15 +482,45 @@ __device__ __forceinline__ void load_sums(uint32_t acc, float (&v)[32]) {
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
 }
 
-// 32 rows x 32 columns of sums at `acc` in tensor memory.
+// A 16-bit residual with aligned rows, where the sums are short: the warp's
+// second slot takes it by asynchronous copies, a chunk ahead of its use.
+__device__ __forceinline__ void fetch_residual(const ProductArgs &a, const WarpTile &t, int row0, int rows, int b0) {
+    if (a.slots == 2 && b0 + 32 <= a.nb) {
+        const char *p = (const char *)a.res.p + ((int64_t)(row0 + t.lane / 4) * a.res.sa + b0) * 2 + (t.lane & 3) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t.lane / 4 + 8 * i < rows)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 piece(t.slot + kSlotBytes, t.lane / 4 + 8 * i, t.lane & 3)),
+                             "l"(p + (int64_t)(8 * i) * a.res.sa * 2)
+                             : "memory");
+    }
+}
+
+// 32 rows x 32 columns of sums at `acc` in tensor memory; next: the columns
+// from this chunk to the warp's next one in the tile, 0 at the last.
 template <int kAct>
-__device__ __forceinline__ void finish_chunk(const ProductArgs &a, const WarpTile &t, uint32_t acc, float bias) {
+__device__ __forceinline__ void finish_chunk(const ProductArgs &a, const WarpTile &t, uint32_t acc, float bias, int next) {
     float v[32];
     load_sums(acc, v);
     add_bias(a, t, bias, v);
     if (a.pre.walk) store_chunk(a.pre, &a.map_pre, t, v);
     activate_all<kAct>(v);
-    if (a.res.walk) add_chunk(a.res, t, v);
+    if (a.slots == 2 && t.cols == 32) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float r[8];
+            unpack8(ptx::ld_shared_v4(piece(t.slot + kSlotBytes, t.lane, i)), a.res.dtype, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
+        }
+        __syncwarp();
+        if (next) fetch_residual(a, t, t.row0, t.rows, t.b0 + next);
+    } else if (a.res.walk) {
+        add_chunk(a.res, t, v);
+    }
     store_chunk(a.d, &a.map_d, t, v);
 }
 
@@ -538,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t ring = ptx::smem_addr(smem);
     const uint32_t staging = ring + a.stages * a.stage_bytes;
-    const uint32_t bias_smem = staging + kEpilogueWarps * kSlotBytes;
+    const uint32_t bias_smem = staging + kEpilogueWarps * kSlotBytes * a.slots;
     SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + (bias_smem - ring) + kBiasBytes);
     if (ring & 1023) {  // the swizzles count on it (true of every launch without static shared memory)
         if (threadIdx.x == 0) atomicExch(a.status, (int)CONV_ERR_ALIGNMENT);
@@ -697,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const int e = warp - 4, quad = warp & 3, part = e >> 2;
         WarpTile wt;
         wt.lane = lane;
-        wt.slot = staging + e * kSlotBytes;
+        wt.slot = staging + e * kSlotBytes * a.slots;
         wt.bias = bias_smem + e * 128;
         int n = 0;
         for (int t = first; t < units; t += step, ++n) {
@@ -712,6 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 const int c = (part + kParts * i) * 32;
                 bias[i] = c < a.tile_b ? lane_bias(a, row0, ib * a.tile_b + c, lane) : 0.0f;
             }
+            const int rows = min(32, min(a.ma, (ia + 1) * a.rows_a) - row0);
+            if (part * 32 < a.tile_b) fetch_residual(a, wt, row0, rows, ib * a.tile_b + part * 32);
             if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status, a.spin)) break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
@@ -721,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ptx::tmem_st_wait();
             }
             wt.row0 = row0;
-            wt.rows = min(32, min(a.ma, (ia + 1) * a.rows_a) - row0);
+            wt.rows = rows;
             if (!kPair && a.split > 1) {
                 // partial sums to shared memory [column][row], over the
                 // ring: its loads and MMAs are done
@@ -748,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
                     continue;
                 }
-                finish_chunk<kAct>(a, wt, acc + c, i == 0 ? bias[0] : i == 1 ? bias[1] : bias[kChunks - 1]);
+                finish_chunk<kAct>(a, wt, acc + c, i == 0 ? bias[0] : i == 1 ? bias[1] : bias[kChunks - 1],
+                                   c + 32 * kParts < a.tile_b ? 32 * kParts : 0);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -757,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) ptx::bulk_wait_group_read<0>();
     }
 
@@ -1036,7 +1076,10 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
     a.stage_bytes = 16384 + (int32_t)round_up(a.b_mn ? a.b_boxes * 8192 : a.b_rows * 128, 1024);
-    a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
+    // (long sums hide the epilogue and want the slots' stage of the ring: 4 / 5
+    // / 6 stages take 695 / 621 / 582 us at 8192 x 4096 x 16384)
+    a.slots = a.res.walk == kWalkRows && a.res.dtype != CONV_FLOAT32 && a.split == 1 && pl.parts == 1 && a.k_steps <= 24 ? 2 : 1;
+    a.stages = std::min(kMaxStages, (kRingBytes - (a.slots - 1) * kEpilogueWarps * kSlotBytes) / a.stage_bytes);
     const int tile_a = pair ? 256 : 128;
     a.idesc = (1u << 4) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 7) | ((pr.in_dtype == CONV_BFLOAT16 ? 1u : 0u) << 10) |
               ((a.a_mn ? 1u : 0u) << 15) | ((a.b_mn ? 1u : 0u) << 16) | ((uint32_t)(a.tile_b >> 3) << 17) |
@@ -1061,7 +1104,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
                     CU_TENSOR_MAP_SWIZZLE_64B))
             return CONV_ERR_CUDA;
 
-    const size_t smem = (size_t)a.stages * a.stage_bytes + kEpilogueWarps * kSlotBytes + kBiasBytes + sizeof(SharedCtl);
+    const size_t smem = (size_t)a.stages * a.stage_bytes + kEpilogueWarps * kSlotBytes * a.slots + kBiasBytes + sizeof(SharedCtl);
     // the kernel with the call's activation, for CTA pairs or single CTAs
     typedef void (*Kernel)(ProductArgs);
     static const Kernel kernels[2][5] = {
