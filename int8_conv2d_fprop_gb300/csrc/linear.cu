@@ -14,60 +14,114 @@ namespace i8c {
 namespace {
 
 // ---------------------------------------------------------------- packing
-// Row-contiguous copies of up to two [rows, cols] matrices of 16-bit
-// elements, rows `ld` elements apart (a multiple of 8; the padding is never
-// read), in one launch.  32 x 32 tiles through shared memory, so that both a
-// row-contiguous and a column-contiguous source are read in runs.
+// Copies of up to two matrices of 16-bit elements as lines of `len` elements
+// `ld` apart (a multiple of 8, so that every line is 16-byte aligned; the
+// padding is never read), in one launch.  A line is a row, or a column where
+// columns have the smaller stride: the product takes either order, so nothing
+// is transposed.  Lines whose elements are adjacent are read in aligned
+// 16-byte vectors, a neighbour's half joined on by shifts; vectors that reach
+// past the matrix are read by elements.
 struct PackJob {
     const uint16_t *src;
     uint16_t *dst;
-    int64_t rs, cs, rows, cols, ld;
-    int32_t col_tiles, tiles;
-    int32_t by_rows;  // lanes along the columns
+    int64_t line_stride, elem_stride, lines, len, ld;
+    const uint16_t *end;  // of the matrix's elements
+    int32_t pieces;       // pieces of 1024 elements per line
+    int32_t blocks;       // eight pieces each
 };
 struct PackJobs {
     PackJob job[2];
     int count = 0;
 };
 
+template <int kWord>
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, bool odd) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = odd ? __funnelshift_r(w[kWord + i], w[kWord + i + 1], 16) : w[kWord + i];
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 __global__ void __launch_bounds__(256) pack_matrix_kernel(const PackJobs jobs) {
-    __shared__ uint16_t tile[32][33];
-    const bool second = (int)blockIdx.x >= jobs.job[0].tiles;
+    const bool second = (int)blockIdx.x >= jobs.job[0].blocks;
     const PackJob &j = jobs.job[second];
-    const int t = (int)blockIdx.x - (second ? jobs.job[0].tiles : 0);
-    const int64_t r0 = (int64_t)(t / j.col_tiles) * 32, c0 = (int64_t)(t % j.col_tiles) * 32;
-    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const int64_t p = (int64_t)((int)blockIdx.x - (second ? jobs.job[0].blocks : 0)) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const int64_t line = p / j.pieces, c0 = (p - line * j.pieces) * 1024;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        const int r = j.by_rows ? y + i : x, c = j.by_rows ? x : y + i;
-        if (r0 + r < j.rows && c0 + c < j.cols) tile[r][c] = j.src[(r0 + r) * j.rs + (c0 + c) * j.cs];
+    if (line >= j.lines) return;
+    const uint16_t *src = j.src + line * j.line_stride;
+    uint16_t *dst = j.dst + line * j.ld;
+    if (j.elem_stride > 1) {
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const int64_t c = c0 + i * 32 + lane;
+            if (c < j.len) dst[c] = src[c * j.elem_stride];
+        }
+        return;
     }
-    __syncthreads();
+    const int lead = (int)((uintptr_t)src / 2 & 7);  // elements past a 16-byte boundary, on the whole line
+    const uint16_t *base = src - lead;
+    uint4 q[4], last[4];
+    bool whole[4];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (r0 + y + i < j.rows && c0 + x < j.cols) j.dst[(r0 + y + i) * j.ld + c0 + x] = tile[y + i][x];
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = c0 + i * 256 + lane * 8;
+        // (the vector at c, and beyond it the one at c + 8 unless lead is 0)
+        const uint16_t *v = base + c;
+        const bool mine = v >= j.src && v + 8 <= j.end, next = lead == 0 || v + 16 <= j.end;
+        whole[i] = c < j.len && mine && next;
+        q[i] = mine ? ptx::ld_nc_v4(v) : make_uint4(0, 0, 0, 0);
+        last[i] = lane == 31 && whole[i] && lead ? ptx::ld_nc_v4(v + 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = c0 + i * 256 + lane * 8;
+        uint4 n;
+        n.x = __shfl_down_sync(0xffffffffu, q[i].x, 1);
+        n.y = __shfl_down_sync(0xffffffffu, q[i].y, 1);
+        n.z = __shfl_down_sync(0xffffffffu, q[i].z, 1);
+        n.w = __shfl_down_sync(0xffffffffu, q[i].w, 1);
+        if (lane == 31) n = last[i];
+        if (whole[i]) {
+            const bool odd = lead & 1;
+            uint4 o;
+            switch (lead >> 1) {  // the same for the whole warp
+                case 0: o = shifted<0>(q[i], n, odd); break;
+                case 1: o = shifted<1>(q[i], n, odd); break;
+                case 2: o = shifted<2>(q[i], n, odd); break;
+                default: o = shifted<3>(q[i], n, odd); break;
+            }
+            *reinterpret_cast<uint4 *>(dst + c) = o;
+        } else {
+            for (int e = 0; e < 8 && c + e < j.len; ++e) dst[c + e] = src[c + e];
+        }
+    }
 }
 
 conv_status run_packs(PackJobs &jobs, cudaStream_t s) {
     if (jobs.count == 0) return CONV_OK;
-    const int64_t tiles = (int64_t)jobs.job[0].tiles + (jobs.count > 1 ? jobs.job[1].tiles : 0);
-    if (tiles > INT32_MAX) return CONV_ERR_TOO_LARGE;
-    return launch_behind(pack_matrix_kernel, dim3((unsigned)tiles), 256, 0, s, jobs) ? CONV_OK : CONV_ERR_CUDA;
+    const int64_t blocks = (int64_t)jobs.job[0].blocks + (jobs.count > 1 ? jobs.job[1].blocks : 0);
+    if (blocks > INT32_MAX) return CONV_ERR_TOO_LARGE;
+    return launch_behind(pack_matrix_kernel, dim3((unsigned)blocks), 256, 0, s, jobs) ? CONV_OK : CONV_ERR_CUDA;
 }
 
 struct Packed {  // a packed copy in the workspace, or none
     size_t off = 0, bytes = 0;
     int64_t ld = 0;
+    bool by_rows = false;  // lines are rows, else columns
 };
 
 void plan_pack(const conv_matrix_desc *d, const void *p, size_t *total, Packed *k) {
     *k = Packed();
     if (d->rows == 0 || d->cols == 0 || product_in_place(p, d->rows, d->row_stride, d->cols, d->col_stride)) return;
-    k->ld = round_up(d->cols, 8);
+    // along the smaller stride (a dim of extent 1 has none)
+    k->by_rows = d->rows == 1 || (d->cols > 1 && d->col_stride <= d->row_stride);
+    k->ld = round_up(k->by_rows ? d->cols : d->rows, 8);
     k->off = *total;
-    k->bytes = (size_t)round_up(d->rows * k->ld * 2, 256);
+    k->bytes = (size_t)round_up((k->by_rows ? d->rows : d->cols) * k->ld * 2, 256);
     *total += k->bytes;
 }
 
@@ -77,20 +131,22 @@ conv_status operand(const conv_matrix_desc *d, const void *p, const Packed &k, v
                     MatRef *m) {
     *m = mat_ref(d, p);
     if (!k.bytes) return CONV_OK;
-    const int64_t rt = (d->rows + 31) / 32, ct = (d->cols + 31) / 32;
-    if (rt * ct > INT32_MAX / 2) return CONV_ERR_TOO_LARGE;
     PackJob &j = jobs->job[jobs->count++];
     j.src = (const uint16_t *)p;
     j.dst = (uint16_t *)((char *)workspace + k.off);
-    j.rs = m->rs, j.cs = m->cs;
-    j.rows = d->rows, j.cols = d->cols;
+    j.lines = k.by_rows ? d->rows : d->cols;
+    j.len = k.by_rows ? d->cols : d->rows;
+    j.line_stride = k.by_rows ? m->rs : m->cs;
+    j.elem_stride = k.by_rows ? m->cs : m->rs;
     j.ld = k.ld;
-    j.col_tiles = (int32_t)ct, j.tiles = (int32_t)(rt * ct);
-    // lanes along the smaller stride (a dim of extent 1 has none)
-    j.by_rows = d->rows == 1 || (d->cols > 1 && m->cs <= m->rs);
+    j.end = j.src + matrix_extent_bytes(d) / 2;
+    j.pieces = (int32_t)((j.len + 1023) / 1024);
+    const int64_t blocks = (j.lines * j.pieces + 7) / 8;
+    if (blocks > INT32_MAX / 2) return CONV_ERR_TOO_LARGE;
+    j.blocks = (int32_t)blocks;
     m->p = j.dst;
-    m->rs = d->rows > 1 ? k.ld : 0;
-    m->cs = d->cols > 1 ? 1 : 0;
+    m->rs = d->rows > 1 ? (k.by_rows ? k.ld : 1) : 0;
+    m->cs = d->cols > 1 ? (k.by_rows ? 1 : k.ld) : 0;
     return CONV_OK;
 }
 
