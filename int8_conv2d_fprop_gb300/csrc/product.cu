@@ -307,6 +307,50 @@ __device__ __forceinline__ void rows_to_slot(const WarpTile &t, const char *p, i
 // The same for any strides, an element at a time, `cols` columns from column
 // b0 + c on: lanes along the rows, or along the columns (32 of 16 bits, or 16
 // of 32 bits and two rows).
+// 16-bit rows, two at a time, in 32-bit words where a row's alignment has
+// them: lane w of a row takes columns 2w - odd and the next, and the last lane
+// the column that is left.  p: the first row's first element.
+__device__ __noinline__ void slot_to_words(uint16_t *p, int64_t row, int rows, int cols, uint32_t slot) {
+    const int lane = threadIdx.x % 32, w = lane & 15;
+#pragma unroll 2
+    for (int r = lane >> 4; r < rows; r += 2) {
+        uint16_t *q = p + r * row;
+        const int e = 2 * w - (int)((uintptr_t)q >> 1 & 1);
+        const uint32_t lo = e >= 0 ? ld_shared_b16(at16(slot, r, e)) : 0u, hi = ld_shared_b16(at16(slot, r, e + 1));
+        if (e >= 0 && e + 1 < cols) *reinterpret_cast<uint32_t *>(q + e) = lo | hi << 16;
+        else if (e >= 0 && e < cols) q[e] = (uint16_t)lo;
+        else if (e < 0) q[0] = (uint16_t)hi;
+        if (e == 29 && cols == 32) q[31] = ld_shared_b16(at16(slot, r, 31));
+    }
+}
+__device__ __noinline__ void words_to_slot(const uint16_t *p, int64_t row, int rows, int cols, uint32_t slot) {
+    const int lane = threadIdx.x % 32, w = lane & 15;
+#pragma unroll 1
+    for (int r0 = lane >> 4; r0 < rows; r0 += 16) {
+        uint32_t v[8];  // loads in flight
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t *q = p + (r0 + 2 * i) * row;
+            const int e = 2 * w - (int)((uintptr_t)q >> 1 & 1);
+            v[i] = 0;
+            if (r0 + 2 * i >= rows) continue;
+            if (e >= 0 && e + 1 < cols) v[i] = *reinterpret_cast<const uint32_t *>(q + e);
+            else if (e >= 0 && e < cols) v[i] = q[e];
+            else if (e < 0) v[i] = (uint32_t)q[0] << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 2 * i;
+            const uint16_t *q = p + r * row;
+            const int e = 2 * w - (int)((uintptr_t)q >> 1 & 1);
+            if (r >= rows) continue;
+            if (e >= 0) st_shared_b16(at16(slot, r, e), (uint16_t)v[i]);
+            st_shared_b16(at16(slot, r, e + 1), (uint16_t)(v[i] >> 16));
+            if (e == 29 && cols == 32) st_shared_b16(at16(slot, r, 31), q[31]);
+        }
+    }
+}
+
 __device__ __noinline__ void slot_to_any(Side s, WarpTile t, int c, int cols) {
     const bool wide = s.dtype == CONV_FLOAT32;
     if (s.walk == kWalkAlongA) {
@@ -393,7 +437,10 @@ __device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *ma
             send_slot(map, t, 0);
         } else {
             __syncwarp();
-            slot_to_any(s, t, 0, t.cols);
+            if (s.walk != kWalkAlongA && s.sb == 1)
+                slot_to_words((uint16_t *)s.p + (int64_t)t.row0 * s.sa + t.b0, s.sa, t.rows, t.cols, t.slot);
+            else
+                slot_to_any(s, t, 0, t.cols);
         }
         return;
     }
@@ -421,6 +468,8 @@ __device__ __forceinline__ void add_chunk(const Side &s, const WarpTile &t, floa
     if (s.dtype != CONV_FLOAT32) {
         free_slot(t);
         if (rows) rows_to_slot(t, (const char *)s.p + ((int64_t)t.row0 * s.sa + t.b0) * 2, s.sa * 2);
+        else if (s.walk != kWalkAlongA && s.sb == 1)
+            words_to_slot((const uint16_t *)s.p + (int64_t)t.row0 * s.sa + t.b0, s.sa, t.rows, t.cols, t.slot);
         else any_to_slot(s, t, 0, t.cols);
         __syncwarp();
 #pragma unroll
