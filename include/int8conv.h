@@ -56,14 +56,16 @@ typedef enum {
     CONV_OK = 0,
     CONV_ERR_NULL_PTR = 1,            /* a required pointer is NULL */
     CONV_ERR_RANK = 2,                /* a descriptor's rank is not 4 */
-    CONV_ERR_DTYPE = 3,               /* image/filter not INT8; output not INT32 (INT8 with CONV_EPILOGUE_INT8_OUT) */
+    CONV_ERR_DTYPE = 3,               /* image/filter not INT8; output not INT32 (INT8 with CONV_EPILOGUE_INT8_OUT);
+                                         a channel operator's matrix of another type than it takes */
     CONV_ERR_SHAPE_MISMATCH = 4,      /* C, K, N or the output dims disagree */
     CONV_ERR_BAD_STRIDES = 5,         /* non-positive stride of a dim > 1, or elements alias */
     CONV_ERR_BUFFER_TOO_SMALL = 6,    /* descriptor's capacity_bytes below its extent */
     CONV_ERR_BAD_PARAM = 7,           /* stride/dilation < 1, padding < 0, empty output, bad mode */
     CONV_ERR_OVERFLOW_RISK = 8,       /* C*R*S*2^14 > 2^31-1: int32 could overflow */
     CONV_ERR_UNSUPPORTED_COMPUTE = 9, /* compute_dtype other than CONV_INT32 */
-    CONV_ERR_ALIGNMENT = 10,          /* a forced algorithm cannot take these pointers/strides */
+    CONV_ERR_ALIGNMENT = 10,          /* a forced algorithm cannot take these pointers/strides; an address that
+                                         is no multiple of its element's size (channel operators) */
     CONV_ERR_CUDA = 11,               /* a CUDA runtime call failed */
     CONV_ERR_DEVICE_TIMEOUT = 12,     /* a kernel gave up waiting (see conv_device_status) */
     CONV_ERR_WORKSPACE = 13,          /* workspace NULL or smaller than conv_fprop_workspace_size */
@@ -494,6 +496,7 @@ typedef struct {
 /* Activations of conv_linear:
  *   CONV_ACT_RELU       max(0, z)
  *   CONV_ACT_GELU       z * Phi(z), Phi the standard normal distribution
+ *                       (0 at minus infinity, its limit)
  *   CONV_ACT_GELU_TANH  z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3)))
  *   CONV_ACT_SILU       z / (1 + exp(-z)) */
 typedef enum {
@@ -530,7 +533,9 @@ typedef struct {
  * when that is 0).  It holds a packed copy of each of x and w that the
  * tensor-memory accelerator cannot read in place: unless one of the
  * strides is 1, the other one a multiple of 8 elements and the address
- * 16-byte aligned.  x_dev and w_dev of the size query are the addresses the
+ * 16-byte aligned; and the partial sums of products whose reduction is cut
+ * into runs (long reductions with few output tiles, or a short last round of
+ * tiles).  x_dev and w_dev of the size query are the addresses the
  * call will use (read only for their alignment; NULL counts as aligned).
  * Asynchronous on `stream`; nothing is allocated and nothing synchronises.
  * Results are the same from run to run: no sum's order depends on timing.
@@ -566,8 +571,8 @@ conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv
  * dx = 0.
  *
  * The workspace (conv_linear_grad_workspace_size bytes, 256-byte aligned)
- * holds dz where it is not dy itself, the partial sums of dbias and packed
- * copies as for conv_linear; the size query takes the same descriptors and
+ * holds dz where it is not dy itself, the partial sums of dbias, and packed
+ * copies and partial sums as for conv_linear; the size query takes the same descriptors and
  * addresses as the call.  Errors, asynchrony and repeatability as for
  * conv_linear.
  */

@@ -298,14 +298,16 @@ const char *conv_status_string(conv_status s) {
         case CONV_ERR_NULL_PTR: return "CONV_ERR_NULL_PTR: a required pointer is NULL";
         case CONV_ERR_RANK: return "CONV_ERR_RANK: descriptor rank is not 4";
         case CONV_ERR_DTYPE:
-            return "CONV_ERR_DTYPE: image/filter must be INT8, output INT32 (INT8 only with CONV_EPILOGUE_INT8_OUT)";
+            return "CONV_ERR_DTYPE: image/filter must be INT8, output INT32 (INT8 only with CONV_EPILOGUE_INT8_OUT); "
+                   "channel operators: a matrix's type is not among those the call takes";
         case CONV_ERR_SHAPE_MISMATCH: return "CONV_ERR_SHAPE_MISMATCH: dims of image, filter and output disagree";
         case CONV_ERR_BAD_STRIDES: return "CONV_ERR_BAD_STRIDES: non-positive or aliasing strides";
         case CONV_ERR_BUFFER_TOO_SMALL: return "CONV_ERR_BUFFER_TOO_SMALL: buffer smaller than the descriptor's extent";
         case CONV_ERR_BAD_PARAM: return "CONV_ERR_BAD_PARAM: bad stride, dilation, padding, mode, flag or empty output";
         case CONV_ERR_OVERFLOW_RISK: return "CONV_ERR_OVERFLOW_RISK: C*R*S*2^14 exceeds int32";
         case CONV_ERR_UNSUPPORTED_COMPUTE: return "CONV_ERR_UNSUPPORTED_COMPUTE: compute type must be INT32";
-        case CONV_ERR_ALIGNMENT: return "CONV_ERR_ALIGNMENT: the forced algorithm cannot take these pointers or strides";
+        case CONV_ERR_ALIGNMENT: return "CONV_ERR_ALIGNMENT: the forced algorithm cannot take these pointers or strides, or an address is no multiple "
+                                          "of its element's size";
         case CONV_ERR_CUDA: return "CONV_ERR_CUDA: a CUDA runtime call failed";
         case CONV_ERR_DEVICE_TIMEOUT: return "CONV_ERR_DEVICE_TIMEOUT: a kernel gave up waiting";
         case CONV_ERR_WORKSPACE: return "CONV_ERR_WORKSPACE: workspace missing or too small";

@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(1024) linear_dz_kernel(MatRef dy, MatRef pre, 
 
 // The same for rows of 16-byte vectors (columns contiguous and a multiple of
 // 8, aligned rows): 32 x 8 threads of 8 columns each, four rows in flight per
-// thread.
+// thread.  A stream (50176 x 1024 GELU: 60 us, 5.2 TB/s of dy, preact and
+// dz); the slope's arithmetic takes about half the issue slots.
 template <int kAct>
 __global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
                                                              int64_t rows_per_block, void *dz, int64_t dz_ld,
