@@ -8,7 +8,8 @@
 namespace i8c {
 
 // Every launch may start while the stream's previous kernel ends (it waits
-// for that kernel before it touches memory).
+// for that kernel before it touches memory; none of these kernels uses
+// non-coherent loads, which would want their data final at the start).
 template <typename... P, typename... A>
 inline bool launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};

@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(256) pack_matrix_kernel(const PackJobs jobs) {
         const uint16_t *v = base + c;
         const bool mine = v >= j.src && v + 8 <= j.end, next = lead == 0 || v + 16 <= j.end;
         whole[i] = c < j.len && mine && next;
-        q[i] = mine ? ptx::ld_nc_v4(v) : make_uint4(0, 0, 0, 0);
-        last[i] = lane == 31 && whole[i] && lead ? ptx::ld_nc_v4(v + 8) : make_uint4(0, 0, 0, 0);
+        q[i] = mine ? *reinterpret_cast<const uint4 *>(v) : make_uint4(0, 0, 0, 0);
+        last[i] = lane == 31 && whole[i] && lead ? *reinterpret_cast<const uint4 *>(v + 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -242,12 +242,48 @@ __global__ void __launch_bounds__(1024) linear_dz_kernel(MatRef dy, MatRef pre, 
     }
 }
 
-// The same for rows of 16-byte vectors (columns contiguous and a multiple of
-// 8, aligned rows): 32 x 8 threads of 8 columns each, four rows in flight per
-// thread.  A stream (50176 x 1024 GELU: 60 us, 5.2 TB/s of dy, preact and
-// dz); the slope's arithmetic takes about half the issue slots.
-template <int kAct>
-__global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef pre, int64_t rows, int64_t cols,
+// Elements c .. c + 7 of a row, c = 8 lane + a multiple of 256, for a warp that
+// is on one row: the aligned vector and the next lane's, joined by shifts.
+// Vectors reach into the row's neighbours but not past the matrix, [lo, hi);
+// where they would, the elements are read one by one (0 past cols).
+__device__ __forceinline__ uint4 load8_shifted(const uint16_t *row, int64_t c, int64_t cols, const uint16_t *lo,
+                                               const uint16_t *hi) {
+    const int lane = threadIdx.x % 32, lead = (int)((uintptr_t)row / 2 & 7);
+    const uint16_t *v = row - lead + c;
+    const bool mine = v >= lo && v + 8 <= hi, whole = mine && (lead == 0 || v + 16 <= hi);
+    const uint4 q = mine ? *reinterpret_cast<const uint4 *>(v) : make_uint4(0, 0, 0, 0);
+    uint4 n;
+    n.x = __shfl_down_sync(0xffffffffu, q.x, 1);
+    n.y = __shfl_down_sync(0xffffffffu, q.y, 1);
+    n.z = __shfl_down_sync(0xffffffffu, q.z, 1);
+    n.w = __shfl_down_sync(0xffffffffu, q.w, 1);
+    if (lane == 31 && whole && lead) n = *reinterpret_cast<const uint4 *>(v + 8);
+    const bool odd = lead & 1;
+    uint4 o;
+    switch (lead >> 1) {  // the same for the whole warp
+        case 0: o = shifted<0>(q, n, odd); break;
+        case 1: o = shifted<1>(q, n, odd); break;
+        case 2: o = shifted<2>(q, n, odd); break;
+        default: o = shifted<3>(q, n, odd); break;
+    }
+    if (!whole) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < cols) w[e / 2] |= (uint32_t)row[c + e] << (e % 2 * 16);
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return o;
+}
+
+// The same for rows of adjacent elements: 32 x 8 threads of 8 columns each, a
+// row per warp, several rows in flight.  kShift: rows of any alignment and
+// length, else 16-byte aligned ones of a multiple of 8.  A stream (50176 x
+// 1024 GELU: 60 us, 5.2 TB/s of dy, preact and dz); the slope's arithmetic
+// takes about half the issue slots.
+template <int kAct, bool kShift>
+__global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef pre, const uint16_t *dy_end,
+                                                             const uint16_t *pre_end, int64_t rows, int64_t cols,
                                                              int64_t rows_per_block, void *dz, int64_t dz_ld,
                                                              float *part) {
     __shared__ float red[8][256];
@@ -255,19 +291,25 @@ __global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef p
     const int64_t c = (int64_t)blockIdx.x * 256 + x * 8;
     const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
     const int64_t r1 = r0 + rows_per_block < rows ? r0 + rows_per_block : rows;
+    const uint16_t *const g0 = (const uint16_t *)dy.p, *const z0 = (const uint16_t *)pre.p;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float sum[8] = {};
-    if (c < cols) {
-        constexpr int kRows = 4;
+    if (kShift || c < cols) {
+        constexpr int kRows = kShift ? 2 : 4;
         for (int64_t r = r0 + y; r < r1; r += 8 * kRows) {
             uint4 g[kRows], z[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                if (r + 8 * i >= r1) break;
-                g[i] = *reinterpret_cast<const uint4 *>((const uint16_t *)dy.p + (r + 8 * i) * dy.rs + c);
-                if constexpr (kAct != CONV_ACT_NONE)
-                    z[i] = *reinterpret_cast<const uint4 *>((const uint16_t *)pre.p + (r + 8 * i) * pre.rs + c);
+                if (r + 8 * i >= r1) break;  // (the whole warp)
+                const uint16_t *gr = g0 + (r + 8 * i) * dy.rs, *zr = z0 + (r + 8 * i) * pre.rs;
+                if constexpr (kShift) {
+                    g[i] = load8_shifted(gr, c, cols, g0, dy_end);
+                    if constexpr (kAct != CONV_ACT_NONE) z[i] = load8_shifted(zr, c, cols, z0, pre_end);
+                } else {
+                    g[i] = *reinterpret_cast<const uint4 *>(gr + c);
+                    if constexpr (kAct != CONV_ACT_NONE) z[i] = *reinterpret_cast<const uint4 *>(zr + c);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -284,9 +326,11 @@ __global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef p
                         v[j + 1] *= p[j + 1];
                     }
                 }
+                // (past the last column stand a neighbour's elements: their
+                // sums are not written, their dz lies in the padding)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += v[j];
-                if (dz)
+                if (dz && (!kShift || c < cols))
                     *reinterpret_cast<uint4 *>((uint16_t *)dz + (r + 8 * i) * dz_ld + c) = pack8(v, dy.dtype);
             }
         }
@@ -369,9 +413,14 @@ void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t 
                int32_t bias_dtype, cudaStream_t s) {
     void *dz = pl.dz ? (char *)ws + pl.dz_off : nullptr;
     float *part = dbias && pl.parts > 1 ? (float *)((char *)ws + pl.part_off) : nullptr;
+    const dim3 wide((unsigned)((n + 255) / 256), (unsigned)pl.parts);
+    auto end = [&](const MatRef &a) { return a.p ? (const uint16_t *)a.p + (m - 1) * a.rs + n : nullptr; };
     if (pl.parts > 1 && n % 8 == 0 && vector_rows(dy) && vector_rows(pre))
-        launch_behind(linear_dz_rows_kernel<kAct>, dim3((unsigned)((n + 255) / 256), (unsigned)pl.parts), 256, 0, s, dy,
-                      pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part);
+        launch_behind(linear_dz_rows_kernel<kAct, false>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
+                      pl.rows_per_part, dz, pl.dz_ld, part);
+    else if (pl.parts > 1 && dy.cs == 1 && (!pre.p || pre.cs == 1))
+        launch_behind(linear_dz_rows_kernel<kAct, true>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
+                      pl.rows_per_part, dz, pl.dz_ld, part);
     else
         launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts), pl.parts > 1 ? 256 : 1024,
                       0, s, dy, pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part, part ? nullptr : dbias, bias_dtype);

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(32 * kWarps) product_rows_kernel(const Product
             uint4 q[kRowsW], u[kM];
 #pragma unroll
             for (int r = 0; r < kRowsW; ++r)
-                q[r] = n0 + r < pr.nb ? ptx::ld_nc_v4(w + (n0 + r) * pr.b.s_mn + g * 8) : make_uint4(0, 0, 0, 0);
+                q[r] = n0 + r < pr.nb ? *reinterpret_cast<const uint4 *>(w + (n0 + r) * pr.b.s_mn + g * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int m = 0; m < kM; ++m) u[m] = *reinterpret_cast<const uint4 *>(x + m * pr.a.s_mn + g * 8);
 #pragma unroll
