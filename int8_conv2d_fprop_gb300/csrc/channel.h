@@ -66,6 +66,9 @@ struct Product {
     int32_t bias_dtype = 0;
     bool bias_along_a = false;
     int32_t act = CONV_ACT_NONE;
+    // The stream's previous kernel is a product that shares no buffer with
+    // this one but inputs: the two may run side by side.
+    bool beside_previous = false;
 };
 
 // Operand the kernel reads in place: one stride 1, the other a multiple of 8

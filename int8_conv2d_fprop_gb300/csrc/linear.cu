@@ -612,6 +612,9 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         pr.ma = n, pr.nb = k, pr.k = m;
         pr.a = {dz.p, dz.cs, dz.rs};
         pr.b = {xr.p, xr.cs, xr.rs};
+        // dw does not wait for dx (unless dx's joining kernel still reads the
+        // partial sums' workspace)
+        pr.beside_previous = want_dx && product_plan(m, k, n).parts == 1;
         pr.in_dtype = x->dtype;
         const MatRef o = mat_ref(dw, dw_dev);
         pr.d = dw_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dw->dtype;

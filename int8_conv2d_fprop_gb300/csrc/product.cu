@@ -84,6 +84,7 @@ struct ProductArgs {
     int32_t slots;               // staging slots of an epilogue warp: 2 where a residual is loaded ahead
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     int32_t split;               // CTAs of a cluster sharing one tile along k (1: none)
+    int32_t late_wait;           // waits for the stream's previous kernel at its end, not its start
     int32_t spin;                // short sums: waits poll (latency counts, and nothing else wants the issue slots)
     int32_t parts;               // runs of k, each summed to `part` (1: none),
     int32_t full;                // of the tiles from this one on
@@ -694,8 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         ptx::tc_fence_after();
         tmem = *(volatile uint32_t *)&ctl->tmem_base;
     }
-    // nothing above reads or writes global memory
-    ptx::grid_dependency_wait();
+    // Nothing above reads or writes global memory.  A product beside an
+    // independent one (the previous kernel) begins at once: that one let it
+    // start only after its own wait, so all the kernels before the two have
+    // ended; it waits before it ends, so that whoever waits for it finds both
+    // done.
+    if (!a.late_wait) ptx::grid_dependency_wait();
     ptx::launch_dependents();
 
     if ((warp == 0 || warp == 3) && lane == 0) {
@@ -906,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     ptx::tc_fence_after();
     if (warp == 2) tmem_dealloc<kPair>(tmem, 512);
+    if (a.late_wait) ptx::grid_dependency_wait();
 }
 
 // Adds the runs' partial sums, in their order, and finishes the product:
@@ -1125,6 +1131,7 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
         }
     }
     a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
+    a.late_wait = pr.beside_previous;
     a.spin = !pair && a.k_steps <= 32 * a.split;
     const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b;
     a.full = (int32_t)(pl.parts > 1 ? pl.full : tiles);
