@@ -282,7 +282,7 @@ __device__ __forceinline__ uint4 load8_shifted(const uint16_t *row, int64_t c, i
 // 1024 GELU: 60 us, 5.2 TB/s of dy, preact and dz); the slope's arithmetic
 // takes about half the issue slots.
 template <int kAct, bool kShift>
-__global__ void __launch_bounds__(256) linear_dz_rows_kernel(MatRef dy, MatRef pre, const uint16_t *dy_end,
+__global__ void __launch_bounds__(256, 3) linear_dz_rows_kernel(MatRef dy, MatRef pre, const uint16_t *dy_end,
                                                              const uint16_t *pre_end, int64_t rows, int64_t cols,
                                                              int64_t rows_per_block, void *dz, int64_t dz_ld,
                                                              float *part) {
@@ -388,9 +388,9 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
             pl.dz_off = pl.bytes;
             pl.bytes += (size_t)round_up(m * pl.dz_ld * 2, 256);
         }
-        // enough blocks for every SM to hold several, whichever kernel runs
+        // two rounds of three blocks per SM, whichever kernel runs
         // (few rows: one block to a column, without a second kernel)
-        const int64_t wanted = m <= 512 ? 1 : std::min<int64_t>(512, std::max<int64_t>(1, 2432 / ((n + 255) / 256)));
+        const int64_t wanted = m <= 512 ? 1 : std::min<int64_t>(512, std::max<int64_t>(1, 912 / ((n + 255) / 256)));
         pl.rows_per_part = round_up((m + wanted - 1) / wanted, 8);
         pl.parts = (m + pl.rows_per_part - 1) / pl.rows_per_part;
         pl.part_off = pl.bytes;

@@ -914,20 +914,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (a.late_wait) ptx::grid_dependency_wait();
 }
 
-// Adds the runs' partial sums, in their order, and finishes the product:
-// 32 rows x 8 columns per warp, lane = row.
+// Adds the runs' partial sums and finishes the product: 32 rows x 8 columns
+// per block, lane = row; warp w adds runs w, w + 8, ... and the first warp the
+// warps' sums, in order.
 template <int kAct>
 __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant__ ProductArgs a, int rows_per_tile) {
-    __shared__ __align__(16) float bias[8][32];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    __shared__ __align__(16) float bias[32];
+    __shared__ float sums[8][8][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     const int tiles = a.tiles_a * a.tiles_b - a.full;  // those cut
-    // unit: 8 columns of 32 rows, columns fastest
+    // block: 8 columns of 32 rows, columns fastest
     const int per_half = a.tile_b / 8 * 4, halves = rows_per_tile / kTileA;
-    const int u = blockIdx.x * 8 + warp;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    if (u >= tiles * halves * per_half) return;
-    const int th = u / per_half, in = u - th * per_half;
+    const int th = blockIdx.x / per_half, in = blockIdx.x - th * per_half;
     const int quad = in / (a.tile_b / 8), c = (in - quad * (a.tile_b / 8)) * 8;
     const int t = th / halves, half = th - t * halves;
     int ia, ib;
@@ -935,7 +935,7 @@ __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant
     WarpTile wt;
     wt.lane = lane;
     wt.slot = 0;  // (unused by 8-column tiles)
-    wt.bias = ptx::smem_addr(bias[warp]);
+    wt.bias = ptx::smem_addr(bias);
     wt.row0 = ia * rows_per_tile + half * kTileA + quad * 32;
     wt.rows = min(32, a.ma - wt.row0);
     wt.b0 = ib * a.tile_b + c;
@@ -944,16 +944,20 @@ __global__ void __launch_bounds__(256) product_join_kernel(const __grid_constant
     const float *p = a.part + ((int64_t)th * a.tile_b + c) * kTileA + quad * 32 + lane;
     const int64_t run = (int64_t)tiles * halves * a.tile_b * kTileA;
     float v[8] = {};
-    for (int r0 = 0; r0 < a.parts; r0 += 8) {
-        float q[8][8];  // 64 loads in flight
+#pragma unroll 4
+    for (int r = warp; r < a.parts; r += 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < 8; ++j) v[j] += p[r * run + j * kTileA];
+    }
+    if (warp > 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[i][j] = r0 + i < a.parts ? p[(r0 + i) * run + j * kTileA] : 0.0f;
+        for (int j = 0; j < 8; ++j) sums[warp][j][lane] = v[j];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < warps; ++w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += q[i][j];
+        for (int j = 0; j < 8; ++j) v[j] += sums[w][j][lane];
     }
     finish8<kAct>(a, wt, v);
 }
@@ -1203,8 +1207,8 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
         static const Join joins[5] = {product_join_kernel<CONV_ACT_NONE>, product_join_kernel<CONV_ACT_RELU>,
                                       product_join_kernel<CONV_ACT_GELU>, product_join_kernel<CONV_ACT_GELU_TANH>,
                                       product_join_kernel<CONV_ACT_SILU>};
-        const int64_t warps = (tiles - a.full) * (tile_a / 32) * (a.tile_b / 8);
-        if (!launch_behind(joins[pr.act], dim3((unsigned)cdiv(warps, 8)), 256, 0, (cudaStream_t)stream, a, tile_a))
+        const int64_t blocks = (tiles - a.full) * (tile_a / 32) * (a.tile_b / 8);
+        if (!launch_behind(joins[pr.act], dim3((unsigned)blocks), 32 * std::min(8, a.parts), 0, (cudaStream_t)stream, a, tile_a))
             return CONV_ERR_CUDA;
     }
     return CONV_OK;
