@@ -66,8 +66,9 @@ struct Product {
     int32_t bias_dtype = 0;
     bool bias_along_a = false;
     int32_t act = CONV_ACT_NONE;
-    // The stream's previous kernel is a product that shares no buffer with
-    // this one but inputs: the two may run side by side.
+    // The stream's previous kernel shares no buffer with this product but
+    // inputs, and lets its successor start only after all before it has
+    // ended: the two may run side by side.
     bool beside_previous = false;
 };
 

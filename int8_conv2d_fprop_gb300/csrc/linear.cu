@@ -602,6 +602,8 @@ conv_status conv_linear_grad(const conv_matrix_desc *dy, const void *dy_dev, con
         pr.ma = m, pr.nb = k, pr.k = n;
         pr.a = {dz.p, dz.rs, dz.cs};
         pr.b = {wr.p, wr.cs, wr.rs};
+        // dx waits for dz, not for the sum of its columns
+        pr.beside_previous = m > 0 && n > 0 && dbias_dev && pl.parts > 1 && jobs.count == 0;
         pr.in_dtype = x->dtype;
         const MatRef o = mat_ref(dx, dx_dev);
         pr.d = dx_dev, pr.d_sa = o.rs, pr.d_sb = o.cs, pr.d_dtype = dx->dtype;

@@ -696,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tmem = *(volatile uint32_t *)&ctl->tmem_base;
     }
     // Nothing above reads or writes global memory.  A product beside an
-    // independent one (the previous kernel) begins at once: that one let it
-    // start only after its own wait, so all the kernels before the two have
-    // ended; it waits before it ends, so that whoever waits for it finds both
-    // done.
+    // independent kernel (the stream's previous one) begins at once: that one
+    // let it start only after its own wait (or began the same way behind
+    // another such one), so all the kernels before them have ended; it waits
+    // before it ends, so that whoever waits for it finds them done.
     if (!a.late_wait) ptx::grid_dependency_wait();
     ptx::launch_dependents();
 
