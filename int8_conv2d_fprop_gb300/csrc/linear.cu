@@ -279,7 +279,7 @@ __device__ __forceinline__ uint4 load8_shifted(const uint16_t *row, int64_t c, i
 // The same for rows of adjacent elements: 32 x 8 threads of 8 columns each, a
 // row per warp, several rows in flight.  kShift: rows of any alignment and
 // length, else 16-byte aligned ones of a multiple of 8.  A stream (50176 x
-// 1024 GELU: 60 us, 5.2 TB/s of dy, preact and dz); the slope's arithmetic
+// 1024 GELU: 55-58 us, 5.3-5.6 TB/s of dy, preact and dz); the slope's arithmetic
 // takes about half the issue slots.
 template <int kAct, bool kShift>
 __global__ void __launch_bounds__(256, 3) linear_dz_rows_kernel(MatRef dy, MatRef pre, const uint16_t *dy_end,
