@@ -681,9 +681,19 @@ __global__ void __launch_bounds__(512) layer_norm_params_sum_kernel(const float 
     if (!out) return;
     float s = 0.0f;
     if (c < cols) {
-#pragma unroll 8
-        for (int i = ty; i < parts; i += 16)
-            s += part[((int64_t)2 * i + blockIdx.y) * part_cols + c + ((lead + i * lead_step) & 7)];
+        // All of a thread's loads in flight at once (two blocks per SM leave 304
+        // parts, 19 for each thread): 4.2 us for 1024 sums, 6.7 us in batches of 8.
+#pragma unroll 1
+        for (int i0 = ty; i0 < parts; i0 += 16 * 20) {
+            float v[20];
+#pragma unroll
+            for (int u = 0; u < 20; ++u) {
+                const int i = i0 + 16 * u;
+                v[u] = i < parts ? part[((int64_t)2 * i + blockIdx.y) * part_cols + c + ((lead + i * lead_step) & 7)] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 20; ++u) s += v[u];
+        }
     }
     red[ty][tx] = s;
     __syncthreads();
