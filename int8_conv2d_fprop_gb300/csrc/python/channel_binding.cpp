@@ -119,11 +119,20 @@ struct Vector {
     }
 };
 
-// One type for the parameter vectors that are there.
+// Whether the parameter vectors that are there hold floats.  The library is
+// told one type for them and takes their addresses on trust: a vector of a type
+// without a code has to be refused here.
+bool float_types(std::initializer_list<const Vector *> all) {
+    for (const Vector *v : all)
+        if (v->p && v->type != CONV_FLOAT32 && v->type != CONV_FLOAT16 && v->type != CONV_BFLOAT16) return false;
+    return true;
+}
+
+// One type for the parameter vectors that are there (which hold floats).
 bool one_type(std::initializer_list<const Vector *> all, int32_t *type) {
     *type = 0;
     for (const Vector *v : all) {
-        if (!v->p && !v->type) continue;
+        if (!v->p) continue;
         if (*type && *type != v->type) {
             PyErr_SetString(PyExc_ValueError, "gain, shift and their gradients must have one type");
             return false;
@@ -261,7 +270,9 @@ PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     conv_layer_norm_params p{};
     p.eps = (float)PyFloat_AsDouble(arg[3]);
     p.scale = (float)PyFloat_AsDouble(arg[4]);
-    if (PyErr_Occurred() || !one_type({&g, &h}, &p.param_dtype)) return nullptr;
+    if (PyErr_Occurred()) return nullptr;
+    if (!float_types({&g, &h})) return status(CONV_ERR_DTYPE);
+    if (!one_type({&g, &h}, &p.param_dtype)) return nullptr;
     const Call c(*x.t, arg[8]);
     at::Tensor made;
     if (!y.t) {
@@ -290,6 +301,7 @@ PyObject *layer_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     conv_layer_norm_params p{};
     p.eps = 1e-5f;
     p.scale = 1.0f;
+    if (!float_types({&g, &dg, &dh})) return status(CONV_ERR_DTYPE);
     if (!one_type({&g, &dg, &dh}, &p.param_dtype)) return nullptr;
     const Call c(*x.t, arg[10]);
     size_t need = 0;

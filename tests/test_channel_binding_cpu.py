@@ -1,0 +1,93 @@
+"""What the channel operators' compiled binding refuses before anything touches
+a device.  The tensors are CUDA tensors by their descriptors only: their
+addresses point at nothing, so a call that is not refused ends, on a machine
+without a GPU, in the error of the missing driver.  Where there is a GPU the
+tests do not run."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class _DLTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("device_type", ctypes.c_int32), ("device_id", ctypes.c_int32),
+                ("ndim", ctypes.c_int32), ("code", ctypes.c_uint8), ("bits", ctypes.c_uint8), ("lanes", ctypes.c_uint16),
+                ("shape", ctypes.c_void_p), ("strides", ctypes.c_void_p), ("byte_offset", ctypes.c_uint64)]
+
+
+class _Managed(ctypes.Structure):
+    _fields_ = [("tensor", _DLTensor), ("context", ctypes.c_void_p), ("deleter", ctypes.c_void_p)]
+
+
+_CODES = {torch.int8: (0, 8), torch.int16: (0, 16), torch.int32: (0, 32), torch.int64: (0, 64), torch.uint8: (1, 8),
+          torch.bool: (6, 8), torch.float16: (2, 16), torch.float32: (2, 32), torch.float64: (2, 64),
+          torch.bfloat16: (4, 16)}
+_kept = []
+_next = [0x10000000]
+
+
+def described(*shape, dtype=torch.bfloat16, device=0):
+    """A contiguous CUDA tensor of this shape without memory behind it."""
+    sizes = (ctypes.c_int64 * len(shape))(*shape)
+    code, bits = _CODES[dtype]
+    _next[0] += 1 << 20
+    m = _Managed(_DLTensor(_next[0], 2, device, len(shape), code, bits, 1, ctypes.addressof(sizes), None, 0), None, None)
+    _kept.append((m, sizes))
+    capsule = ctypes.pythonapi.PyCapsule_New
+    capsule.restype, capsule.argtypes = ctypes.py_object, [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
+    return torch._C._from_dlpack(capsule(ctypes.addressof(m), b"dltensor", None))
+
+
+@pytest.fixture
+def ic(monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("these addresses are not to reach a GPU")
+    monkeypatch.setattr(torch.cuda, "_lazy_init", lambda: None)
+    import __graft_entry__
+    __graft_entry__.build_library()
+    import int8_conv2d_fprop_gb300 as m
+    return m
+
+
+BF16, F32 = torch.bfloat16, torch.float32
+NOT_FLOATS = [torch.float64, torch.int64, torch.int32, torch.int16, torch.int8, torch.uint8, torch.bool]
+
+
+def refused(ic, name, call):
+    with pytest.raises(ic.ConvError) as e:
+        call()
+    assert e.value.name == name
+
+
+@pytest.mark.parametrize("dtype", NOT_FLOATS)
+@pytest.mark.parametrize("which", ["gain", "shift"])
+def test_layer_norm_takes_float_parameters_only(ic, which, dtype):
+    x = described(4, 16)
+    refused(ic, "CONV_ERR_DTYPE", lambda: ic.conv_layer_norm(x, **{which: described(16, dtype=dtype)}))
+    # ... and not with a float vector beside it
+    both = {"gain": described(16, dtype=F32), "shift": described(16, dtype=F32)}
+    both[which] = described(16, dtype=dtype)
+    refused(ic, "CONV_ERR_DTYPE", lambda: ic.conv_layer_norm(x, **both))
+
+
+@pytest.mark.parametrize("dtype", NOT_FLOATS)
+@pytest.mark.parametrize("which", ["gain", "dgain", "dshift"])
+def test_layer_norm_grad_takes_float_parameters_only(ic, which, dtype):
+    x, dy, dx = described(4, 16), described(4, 16), described(4, 16)
+    mean, rstd = described(4, dtype=F32), described(4, dtype=F32)
+
+    def call(**vectors):
+        gain = vectors.pop("gain", None)
+        return lambda: ic.conv_layer_norm_grad(dy, x, gain, mean, rstd, dx=dx, **vectors)
+
+    refused(ic, "CONV_ERR_DTYPE", call(**{which: described(16, dtype=dtype)}))
+    every = {k: described(16, dtype=F32) for k in ("gain", "dgain", "dshift")}
+    every[which] = described(16, dtype=dtype)
+    refused(ic, "CONV_ERR_DTYPE", call(**every))
+
+
+def test_parameters_of_two_float_types(ic):
+    x = described(4, 16)
+    with pytest.raises(ValueError, match="one type"):
+        ic.conv_layer_norm(x, described(16, dtype=F32), described(16))
