@@ -38,8 +38,19 @@ bool fail(const char *what, const char *why) {
     return false;
 }
 
+// What the tensors of one call have in common.
+struct Common {
+    const at::Tensor *first = nullptr;
+
+    // Kernels run on one device and take addresses on trust.
+    bool admit(const at::Tensor &t, const char *what) {
+        if (!first) first = &t;
+        return t.device() == first->device() || fail(what, "must be on the device of the call's other tensors");
+    }
+};
+
 // The tensor behind a Python argument; NULL (no error set) for None.
-const at::Tensor *tensor(PyObject *o, const char *what, bool *ok) {
+const at::Tensor *tensor(Common &all, PyObject *o, const char *what, bool *ok) {
     *ok = true;
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) {
@@ -48,7 +59,7 @@ const at::Tensor *tensor(PyObject *o, const char *what, bool *ok) {
         return nullptr;
     }
     const at::Tensor *t = &THPVariable_Unpack(o);
-    if (!t->is_cuda()) *ok = fail(what, "must be a CUDA tensor");
+    *ok = t->is_cuda() ? all.admit(*t, what) : fail(what, "must be a CUDA tensor");
     return t;
 }
 
@@ -59,9 +70,9 @@ struct Matrix {
     const at::Tensor *t = nullptr;
     const conv_matrix_desc *desc() const { return t ? &d : nullptr; }
 
-    bool read(PyObject *o, const char *what, bool required) {
+    bool read(Common &all, PyObject *o, const char *what, bool required) {
         bool ok;
-        t = tensor(o, what, &ok);
+        t = tensor(all, o, what, &ok);
         if (!ok) return false;
         if (!t) return !required || fail(what, "is required");
         return read(*t, what);
@@ -100,9 +111,9 @@ struct Matrix {
 struct Vector {
     void *p = nullptr;
     int32_t type = 0;
-    bool read(PyObject *o, const char *what, int64_t n) {
+    bool read(Common &all, PyObject *o, const char *what, int64_t n) {
         bool ok;
-        const at::Tensor *t = tensor(o, what, &ok);
+        const at::Tensor *t = tensor(all, o, what, &ok);
         if (!ok) return false;
         if (!t) return true;
         if (t->dim() != 1 || t->size(0) != n || (n > 1 && t->stride(0) != 1)) {
@@ -113,8 +124,8 @@ struct Vector {
         type = type_code(t->scalar_type());
         return true;
     }
-    bool read_float(PyObject *o, const char *what, int64_t n) {
-        if (!read(o, what, n)) return false;
+    bool read_float(Common &all, PyObject *o, const char *what, int64_t n) {
+        if (!read(all, o, what, n)) return false;
         return !p || type == CONV_FLOAT32 || fail(what, "must be float32");
     }
 };
@@ -171,10 +182,16 @@ struct Workspace {
     at::Tensor own;
     void *p = nullptr;
     size_t bytes = 0;
-    bool take(const Call &c, PyObject *given, size_t need) {
+    // (before there is a call, so that nothing has touched the device yet)
+    static bool admit(Common &all, PyObject *given) {
+        if (!THPVariable_Check(given)) return true;
+        const at::Tensor &t = THPVariable_Unpack(given);
+        return !t.is_cuda() || all.admit(t, "workspace");
+    }
+    bool take(Common &all, const Call &c, PyObject *given, size_t need) {
         if (need == 0) return true;
         bool ok;
-        const at::Tensor *t = tensor(given, "workspace", &ok);
+        const at::Tensor *t = tensor(all, given, "workspace", &ok);
         if (!ok) return false;
         if (t && t->is_contiguous() && (size_t)t->nbytes() >= need) {
             p = t->data_ptr();
@@ -200,10 +217,12 @@ PyObject *status(conv_status st) { return PyLong_FromLong(st); }
 PyObject *linear(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!count(n, 9)) return nullptr;
+    Common all;
     Matrix x, w, r, z, y;
     Vector b;
-    if (!x.read(arg[0], "x", true) || !w.read(arg[1], "w", true) || !b.read(arg[2], "bias", w.d.rows) ||
-        !r.read(arg[4], "residual", false) || !z.read(arg[5], "preact", false) || !y.read(arg[6], "out", false))
+    if (!x.read(all, arg[0], "x", true) || !w.read(all, arg[1], "w", true) || !b.read(all, arg[2], "bias", w.d.rows) ||
+        !r.read(all, arg[4], "residual", false) || !z.read(all, arg[5], "preact", false) || !y.read(all, arg[6], "out", false) ||
+        !Workspace::admit(all, arg[7]))
         return nullptr;
     conv_linear_params p{};
     p.activation = (int32_t)PyLong_AsLong(arg[3]);
@@ -221,7 +240,7 @@ PyObject *linear(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     conv_status st = conv_linear_workspace_size(&x.d, x.p, &w.d, w.p, &need);
     if (st) return status(st);
     Workspace ws;
-    if (!ws.take(c, arg[7], need)) return nullptr;
+    if (!ws.take(all, c, arg[7], need)) return nullptr;
     st = conv_linear(&x.d, x.p, &w.d, w.p, b.p, r.desc(), r.p, z.desc(), z.p, &y.d, y.p, &p, ws.p, ws.bytes, c.stream);
     if (st) return status(st);
     if (made.defined()) return THPVariable_Wrap(std::move(made));
@@ -234,11 +253,12 @@ PyObject *linear(PyObject *, PyObject *const *arg, Py_ssize_t n) {
 PyObject *linear_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!count(n, 10)) return nullptr;
+    Common all;
     Matrix dy, x, w, z, dx, dw;
     Vector db;
-    if (!dy.read(arg[0], "dy", true) || !x.read(arg[1], "x", true) || !w.read(arg[2], "w", true) ||
-        !z.read(arg[3], "preact", false) || !dx.read(arg[5], "dx", false) || !dw.read(arg[6], "dw", false) ||
-        !db.read(arg[7], "dbias", w.d.rows))
+    if (!dy.read(all, arg[0], "dy", true) || !x.read(all, arg[1], "x", true) || !w.read(all, arg[2], "w", true) ||
+        !z.read(all, arg[3], "preact", false) || !dx.read(all, arg[5], "dx", false) || !dw.read(all, arg[6], "dw", false) ||
+        !db.read(all, arg[7], "dbias", w.d.rows) || !Workspace::admit(all, arg[8]))
         return nullptr;
     conv_linear_params p{};
     p.activation = (int32_t)PyLong_AsLong(arg[4]);
@@ -249,7 +269,7 @@ PyObject *linear_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     conv_status st = conv_linear_grad_workspace_size(&dy.d, dy.p, &x.d, x.p, &w.d, w.p, &p, &need);
     if (st) return status(st);
     Workspace ws;
-    if (!ws.take(c, arg[8], need)) return nullptr;
+    if (!ws.take(all, c, arg[8], need)) return nullptr;
     st = conv_linear_grad(&dy.d, dy.p, &x.d, x.p, &w.d, w.p, z.desc(), z.p, dx.desc(), dx.p, dw.desc(), dw.p, db.p, &p,
                           ws.p, ws.bytes, c.stream);
     if (st) return status(st);
@@ -261,11 +281,12 @@ PyObject *linear_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
 PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!count(n, 9)) return nullptr;
+    Common all;
     Matrix x, y;
     Vector g, h, mean, rstd;
-    if (!x.read(arg[0], "x", true) || !g.read(arg[1], "gain", x.d.cols) || !h.read(arg[2], "shift", x.d.cols) ||
-        !y.read(arg[5], "out", false) || !mean.read_float(arg[6], "mean", x.d.rows) ||
-        !rstd.read_float(arg[7], "rstd", x.d.rows))
+    if (!x.read(all, arg[0], "x", true) || !g.read(all, arg[1], "gain", x.d.cols) || !h.read(all, arg[2], "shift", x.d.cols) ||
+        !y.read(all, arg[5], "out", false) || !mean.read_float(all, arg[6], "mean", x.d.rows) ||
+        !rstd.read_float(all, arg[7], "rstd", x.d.rows))
         return nullptr;
     conv_layer_norm_params p{};
     p.eps = (float)PyFloat_AsDouble(arg[3]);
@@ -291,12 +312,14 @@ PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
 PyObject *layer_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (!count(n, 11)) return nullptr;
+    Common all;
     Matrix dy, x, r, dx;
     Vector g, mean, rstd, dg, dh;
-    if (!dy.read(arg[0], "dy", true) || !x.read(arg[1], "x", true) || !g.read(arg[2], "gain", x.d.cols) ||
-        !mean.read_float(arg[3], "mean", x.d.rows) || !rstd.read_float(arg[4], "rstd", x.d.rows) ||
-        !r.read(arg[5], "residual_grad", false) || !dx.read(arg[6], "dx", false) ||
-        !dg.read(arg[7], "dgain", x.d.cols) || !dh.read(arg[8], "dshift", x.d.cols))
+    if (!dy.read(all, arg[0], "dy", true) || !x.read(all, arg[1], "x", true) || !g.read(all, arg[2], "gain", x.d.cols) ||
+        !mean.read_float(all, arg[3], "mean", x.d.rows) || !rstd.read_float(all, arg[4], "rstd", x.d.rows) ||
+        !r.read(all, arg[5], "residual_grad", false) || !dx.read(all, arg[6], "dx", false) ||
+        !dg.read(all, arg[7], "dgain", x.d.cols) || !dh.read(all, arg[8], "dshift", x.d.cols) ||
+        !Workspace::admit(all, arg[9]))
         return nullptr;
     conv_layer_norm_params p{};
     p.eps = 1e-5f;
@@ -308,7 +331,7 @@ PyObject *layer_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     conv_status st = conv_layer_norm_grad_workspace_size(&x.d, &need);
     if (st) return status(st);
     Workspace ws;
-    if (!ws.take(c, arg[9], need)) return nullptr;
+    if (!ws.take(all, c, arg[9], need)) return nullptr;
     st = conv_layer_norm_grad(&dy.d, dy.p, &x.d, x.p, g.p, (const float *)mean.p, (const float *)rstd.p, r.desc(), r.p,
                               dx.desc(), dx.p, dg.p, dh.p, &p, ws.p, ws.bytes, c.stream);
     if (st) return status(st);

@@ -91,3 +91,49 @@ def test_parameters_of_two_float_types(ic):
     x = described(4, 16)
     with pytest.raises(ValueError, match="one type"):
         ic.conv_layer_norm(x, described(16, dtype=F32), described(16))
+
+
+# every tensor argument of the four calls: builds it, given the device of one of them
+def _linear_arguments(at):
+    return ("conv_linear", [described(4, 16, device=at("x")), described(8, 16, device=at("w"))],
+            {"bias": described(8, device=at("bias")), "residual": described(4, 8, device=at("residual")),
+             "preact": described(4, 8, device=at("preact")), "out": described(4, 8, device=at("out")),
+             "workspace": described(1 << 16, dtype=torch.uint8, device=at("workspace"))})
+
+
+def _linear_grad_arguments(at):
+    return ("conv_linear_grad", [described(4, 8, device=at("dy")), described(4, 16, device=at("x")),
+                                 described(8, 16, device=at("w"))],
+            {"preact": described(4, 8, device=at("preact")), "activation": "gelu",
+             "dx": described(4, 16, device=at("dx")), "dw": described(8, 16, device=at("dw")),
+             "dbias": described(8, dtype=F32, device=at("dbias")),
+             "workspace": described(1 << 16, dtype=torch.uint8, device=at("workspace"))})
+
+
+def _norm_arguments(at):
+    return ("conv_layer_norm", [described(4, 16, device=at("x")), described(16, dtype=F32, device=at("gain")),
+                                described(16, dtype=F32, device=at("shift"))],
+            {"out": described(4, 16, device=at("out")), "mean": described(4, dtype=F32, device=at("mean")),
+             "rstd": described(4, dtype=F32, device=at("rstd"))})
+
+
+def _norm_grad_arguments(at):
+    return ("conv_layer_norm_grad", [described(4, 16, device=at("dy")), described(4, 16, device=at("x")),
+                                     described(16, dtype=F32, device=at("gain")),
+                                     described(4, dtype=F32, device=at("mean")), described(4, dtype=F32, device=at("rstd"))],
+            {"residual_grad": described(4, 16, device=at("residual_grad")), "dx": described(4, 16, device=at("dx")),
+             "dgain": described(16, dtype=F32, device=at("dgain")), "dshift": described(16, dtype=F32, device=at("dshift")),
+             "workspace": described(1 << 16, dtype=torch.uint8, device=at("workspace"))})
+
+
+_TENSORS = [(_linear_arguments, "x w bias residual preact out workspace"),
+            (_linear_grad_arguments, "dy x w preact dx dw dbias workspace"),
+            (_norm_arguments, "x gain shift out mean rstd"),
+            (_norm_grad_arguments, "dy x gain mean rstd residual_grad dx dgain dshift workspace")]
+
+
+@pytest.mark.parametrize("arguments,which", [(a, w) for a, names in _TENSORS for w in names.split()])
+def test_tensors_of_two_devices(ic, arguments, which):
+    name, args, kwargs = arguments(lambda n: 1 if n == which else 0)
+    with pytest.raises(ValueError, match="device"):
+        getattr(ic, name)(*args, **kwargs)
