@@ -139,6 +139,16 @@ bool float_types(std::initializer_list<const Vector *> all) {
     return true;
 }
 
+// An activation code; -1 for a number that is none (its lower 32 bits
+// may be one).
+bool activation_code(PyObject *o, int32_t *code) {
+    int overflow = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &overflow);
+    if (v == -1 && PyErr_Occurred()) return false;
+    *code = overflow || v < CONV_ACT_NONE || v > CONV_ACT_SILU ? -1 : (int32_t)v;
+    return true;
+}
+
 // One type for the parameter vectors that are there (which hold floats).
 bool one_type(std::initializer_list<const Vector *> all, int32_t *type) {
     *type = 0;
@@ -225,8 +235,8 @@ PyObject *linear(PyObject *, PyObject *const *arg, Py_ssize_t n) {
         !Workspace::admit(all, arg[7]))
         return nullptr;
     conv_linear_params p{};
-    p.activation = (int32_t)PyLong_AsLong(arg[3]);
-    if (PyErr_Occurred()) return nullptr;
+    if (!activation_code(arg[3], &p.activation)) return nullptr;
+    if (p.activation < 0) return status(CONV_ERR_BAD_PARAM);
     p.bias_dtype = b.type;
     const Call c(*x.t, arg[8]);
     at::Tensor made;
@@ -261,8 +271,8 @@ PyObject *linear_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
         !db.read(all, arg[7], "dbias", w.d.rows) || !Workspace::admit(all, arg[8]))
         return nullptr;
     conv_linear_params p{};
-    p.activation = (int32_t)PyLong_AsLong(arg[4]);
-    if (PyErr_Occurred()) return nullptr;
+    if (!activation_code(arg[4], &p.activation)) return nullptr;
+    if (p.activation < 0) return status(CONV_ERR_BAD_PARAM);
     p.bias_dtype = db.type;
     const Call c(*x.t, arg[9]);
     size_t need = 0;

@@ -137,3 +137,10 @@ def test_tensors_of_two_devices(ic, arguments, which):
     name, args, kwargs = arguments(lambda n: 1 if n == which else 0)
     with pytest.raises(ValueError, match="device"):
         getattr(ic, name)(*args, **kwargs)
+
+
+@pytest.mark.parametrize("code", [-1, 5, 1 << 32, (1 << 32) + 2, -(1 << 32), 1 << 70])
+def test_activation_codes_are_not_cut_to_32_bits(ic, code):
+    x, w, dy = described(4, 16), described(8, 16), described(4, 8)
+    refused(ic, "CONV_ERR_BAD_PARAM", lambda: ic.conv_linear(x, w, activation=code))
+    refused(ic, "CONV_ERR_BAD_PARAM", lambda: ic.conv_linear_grad(dy, x, w, preact=dy, activation=code, dx=x))
