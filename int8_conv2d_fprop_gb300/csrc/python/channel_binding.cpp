@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -42,9 +43,13 @@ bool fail(const char *what, const char *why) {
 struct Common {
     const at::Tensor *first = nullptr;
 
-    // Kernels run on one device and take addresses on trust.
+    // Kernels run on one device and take addresses on trust; autograd does
+    // not see these calls.
     bool admit(const at::Tensor &t, const char *what) {
         if (!first) first = &t;
+        if (t.requires_grad() && at::GradMode::is_enabled())
+            return fail(what, "requires a gradient, which this call would not record: detach it, or call under "
+                              "torch.no_grad() and make the gradients with the *_grad calls");
         return t.device() == first->device() || fail(what, "must be on the device of the call's other tensors");
     }
 };
@@ -111,9 +116,10 @@ struct Matrix {
 struct Vector {
     void *p = nullptr;
     int32_t type = 0;
+    const at::Tensor *t = nullptr;
     bool read(Common &all, PyObject *o, const char *what, int64_t n) {
         bool ok;
-        const at::Tensor *t = tensor(all, o, what, &ok);
+        t = tensor(all, o, what, &ok);
         if (!ok) return false;
         if (!t) return true;
         if (t->dim() != 1 || t->size(0) != n || (n > 1 && t->stride(0) != 1)) {
@@ -221,6 +227,13 @@ bool count(Py_ssize_t have, Py_ssize_t want) {
     return false;
 }
 
+// Tells autograd that a tensor's values changed, as an in-place operation
+// does: graphs that saved them refuse to go back.
+void changed(std::initializer_list<const at::Tensor *> outputs) {
+    for (const at::Tensor *t : outputs)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *status(conv_status st) { return PyLong_FromLong(st); }
 
 // linear(x, w, bias, activation, residual, preact, out, workspace, stream) -> out
@@ -253,6 +266,8 @@ PyObject *linear(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     if (!ws.take(all, c, arg[7], need)) return nullptr;
     st = conv_linear(&x.d, x.p, &w.d, w.p, b.p, r.desc(), r.p, z.desc(), z.p, &y.d, y.p, &p, ws.p, ws.bytes, c.stream);
     if (st) return status(st);
+    if (made.defined()) y.t = nullptr;
+    changed({z.t, y.t});
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     Py_INCREF(arg[6]);
     return arg[6];
@@ -283,6 +298,7 @@ PyObject *linear_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     st = conv_linear_grad(&dy.d, dy.p, &x.d, x.p, &w.d, w.p, z.desc(), z.p, dx.desc(), dx.p, dw.desc(), dw.p, db.p, &p,
                           ws.p, ws.bytes, c.stream);
     if (st) return status(st);
+    changed({dx.t, dw.t, db.t});
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -312,6 +328,8 @@ PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     }
     const conv_status st = conv_layer_norm(&x.d, x.p, g.p, h.p, &y.d, y.p, (float *)mean.p, (float *)rstd.p, &p, c.stream);
     if (st) return status(st);
+    if (made.defined()) y.t = nullptr;
+    changed({y.t, mean.t, rstd.t});
     if (made.defined()) return THPVariable_Wrap(std::move(made));
     Py_INCREF(arg[5]);
     return arg[5];
@@ -345,6 +363,7 @@ PyObject *layer_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     st = conv_layer_norm_grad(&dy.d, dy.p, &x.d, x.p, g.p, (const float *)mean.p, (const float *)rstd.p, r.desc(), r.p,
                               dx.desc(), dx.p, dg.p, dh.p, &p, ws.p, ws.bytes, c.stream);
     if (st) return status(st);
+    changed({dx.t, dg.t, dh.t});
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }

@@ -144,3 +144,18 @@ def test_activation_codes_are_not_cut_to_32_bits(ic, code):
     x, w, dy = described(4, 16), described(8, 16), described(4, 8)
     refused(ic, "CONV_ERR_BAD_PARAM", lambda: ic.conv_linear(x, w, activation=code))
     refused(ic, "CONV_ERR_BAD_PARAM", lambda: ic.conv_linear_grad(dy, x, w, preact=dy, activation=code, dx=x))
+
+
+@pytest.mark.parametrize("arguments,which", [(a, w) for a, names in _TENSORS for w in names.split() if w != "workspace"])
+def test_tensors_that_require_a_gradient(ic, arguments, which):
+    """Refused while gradients are recorded, which the call would not be; with
+    recording off such a call is like any other (here it gets as far as the
+    missing driver)."""
+    name, args, kwargs = arguments(lambda n: 0)
+    order = dict(_TENSORS)[arguments].split()
+    target = args[order.index(which)] if order.index(which) < len(args) else kwargs[which]
+    target.requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        getattr(ic, name)(*args, **kwargs)
+    with torch.no_grad(), pytest.raises(RuntimeError, match="CUDA"):
+        getattr(ic, name)(*args, **kwargs)
