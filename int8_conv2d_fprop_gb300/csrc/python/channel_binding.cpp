@@ -43,10 +43,12 @@ bool fail(const char *what, const char *why) {
 struct Common {
     const at::Tensor *first = nullptr;
 
-    // Kernels run on one device and take addresses on trust; autograd does
-    // not see these calls.
+    // Kernels run on one device and take addresses on trust, and the values
+    // as they stand there; autograd does not see these calls.
     bool admit(const at::Tensor &t, const char *what) {
         if (!first) first = &t;
+        if (t.is_neg() || t._is_zerotensor())
+            return fail(what, "is a lazy view whose memory does not hold its values; clone it");
         if (t.requires_grad() && at::GradMode::is_enabled())
             return fail(what, "requires a gradient, which this call would not record: detach it, or call under "
                               "torch.no_grad() and make the gradients with the *_grad calls");

@@ -159,3 +159,15 @@ def test_tensors_that_require_a_gradient(ic, arguments, which):
         getattr(ic, name)(*args, **kwargs)
     with torch.no_grad(), pytest.raises(RuntimeError, match="CUDA"):
         getattr(ic, name)(*args, **kwargs)
+
+
+@pytest.mark.parametrize("arguments,which", [(a, w) for a, names in _TENSORS for w in names.split() if w != "workspace"])
+def test_lazily_negated_views(ic, arguments, which):
+    """The imaginary part of a conjugate, say: its memory holds the opposite."""
+    name, args, kwargs = arguments(lambda n: 0)
+    order = dict(_TENSORS)[arguments].split()
+    i = order.index(which)
+    where, key = (args, i) if i < len(args) else (kwargs, which)
+    where[key] = torch._neg_view(where[key])
+    with pytest.raises(ValueError, match="lazy"):
+        getattr(ic, name)(*args, **kwargs)
