@@ -562,8 +562,10 @@ __global__ void __launch_bounds__(kWarp ? 256 : grad_threads(kNv), kWarp ? (kNv 
         }
         const float m = mu, rr = rs;
         if (r + step < a.rows) mu = a.mean[r + step], rs = a.rstd[r + step];
-        // n = x rstd - mean rstd
-        const Pair scale = pair(rr), offset = pair(-m * rr);
+        // n = (x - mean) rstd: the difference first, whose rounding is its own
+        // (x rstd - mean rstd in one instruction is off by the rounding of
+        // mean rstd: dgain by 2e-5 where the mean is 1000 deviations)
+        const Pair scale = pair(rr), minus_mean = pair(-m);
         Pair st2 = pair(0.0f), stn2 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : grad_threads(kNv), kWarp ? (kNv 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // (outside the row dy is 0, and so is every term)
-                const Pair d = element2(gy[i], j), n = fma2(element2(gx[i], j), scale, offset);
+                const Pair d = element2(gy[i], j), n = mul2(add2(element2(gx[i], j), minus_mean), scale);
                 const Pair u = mul2(d, gain[j]);
                 st2 = add2(st2, u);
                 stn2 = fma2(u, n, stn2);
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : grad_threads(kNv), kWarp ? (kNv 
             load_gain(i, gain);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const Pair n = fma2(element2(gx[i], j), scale, offset);
+                const Pair n = mul2(add2(element2(gx[i], j), minus_mean), scale);
                 Pair w = fma2(mul2(element2(gy[i], j), gain[j]), scale, minus_st);
                 w = fma2(n, minus_stn, w);
                 if (res) w = add2(w, element2(gr[i], j));

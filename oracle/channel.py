@@ -134,15 +134,16 @@ def layer_norm_grad(dy, x, gain, mean, rstd, residual=None):
     return (dx if residual is None else dx + residual), (dy * n).sum(0), dy.sum(0)
 
 
-def layer_norm_grad_bounds(dy, x, gain, mean, rstd, residual, outs, x_type, p_type):
+def layer_norm_grad_bounds(dy, x, gain, mean, rstd, residual, outs, x_type, p_type, centred=False):
     """Sums as in layer_norm_bounds; the normalised value n is off by 2^-22 of
-    (|x| + |mean|) rstd + |n|."""
+    (|x| + |mean|) rstd + |n|, or with `centred` of |n| alone, as the product of
+    a rounded difference x - mean is."""
     dx, dg, db = outs
     m, c = x.shape
     terms = (c / 32 + 16) * 2.0 ** -23
     r = rstd[:, None]
     n = (x - mean[:, None]) * r
-    en = 2.0 ** -22 * ((np.abs(x) + np.abs(mean)[:, None]) * r + np.abs(n))
+    en = 2.0 ** -22 * ((0 if centred else (np.abs(x) + np.abs(mean)[:, None]) * r) + np.abs(n))
     t = np.abs(dy if gain is None else dy * gain)
     s1, s2 = t.mean(1, keepdims=True), (t * np.abs(n)).mean(1, keepdims=True)
     e2 = (terms + 2.0 ** -21) * s2 + (t * en).mean(1, keepdims=True)

@@ -1,5 +1,8 @@
 """Edges of the channel operators on the GPU."""
+import numpy as np
 import pytest
+
+from oracle import channel as oc
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +60,65 @@ def test_outputs_count_as_changed_in_place(ic):
     with torch.inference_mode():
         frozen = randn(g, 6, 16)
     ic.conv_layer_norm(frozen, out=frozen)
+
+
+# ----------------------------------------------------------- norm, far from zero
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def check(got, want, bound, what):
+    got = f64(got)
+    with np.errstate(invalid="ignore"):
+        bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.size} outside the bound, first at "
+                           f"{tuple(int(i[0]) for i in np.nonzero(bad))}, worst {np.nanmax(np.abs(got - want) / bound):.3g}")
+
+
+def strided(v, dtype, lead):
+    """The values in rows that start `lead` elements past a boundary of 8 and are
+    a multiple of 8 apart; lead None: columns two elements apart."""
+    m, c = v.shape
+    if lead is None:
+        return torch.full((m, 2 * c), float("nan"), device="cuda", dtype=dtype)[:, ::2].copy_(v)
+    return torch.full((m, (c + 15) // 8 * 8), float("nan"), device="cuda", dtype=dtype)[:, lead:lead + c].copy_(v)
+
+
+# every way a row is held: by a warp (two widths), by a block (three), read again for each pass
+HELD = [(40, 200), (40, 512), (700, 1000), (700, 4097), (330, 8192), (6, 17000)]
+
+
+@pytest.mark.parametrize("m,c", HELD)
+@pytest.mark.parametrize("mean", [1000.0, -30000.0])
+# x, dy alike; x and dy at different leads; columns apart
+@pytest.mark.parametrize("leads", [(0, 0), (3, 3), (1, 2), (None, 0)])
+def test_layer_norm_grad_far_from_zero(ic, m, c, mean, leads):
+    """Rows whose mean is many deviations: n = (x - mean) rstd is only off by
+    its own rounding, whatever the mean."""
+    g = gen(m + c)
+    x, dy = strided(randn(g, m, c) + mean, F32, leads[0]), strided(randn(g, m, c) / 4, F32, leads[1])
+    gain = 1 + 0.3 * randn(g, c)
+    _, mu, rstd = oc.layer_norm(f64(x))
+    mu, rstd = (torch.from_numpy(v.astype(np.float32)).cuda() for v in (mu, rstd))
+    dx, dg, db = torch.empty(m, c, device="cuda"), torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    ic.conv_layer_norm_grad(dy, x, gain, mu, rstd, dx=dx, dgain=dg, dshift=db)
+    args = [f64(v) for v in (dy, x, gain, mu, rstd)] + [None]
+    want = oc.layer_norm_grad(*args)
+    bounds = oc.layer_norm_grad_bounds(*args, want, "float32", "float32", centred=True)
+    for got, v, b, what in zip((dx, dg, db), want, bounds, ("dx", "dgain", "dshift")):
+        check(got, v, b, what)
+
+
+@pytest.mark.parametrize("m,c", HELD)
+def test_layer_norm_grad_of_constant_rows(ic, m, c):
+    """No deviation: n is 0, and so is dgain, whatever the rows' value."""
+    g = gen(c)
+    dy = randn(g, m, c)
+    mean, rstd = torch.randn(m, generator=g, device="cuda") * 1e6, torch.full((m,), 1e-5 ** -0.5, device="cuda")
+    x = mean[:, None].expand(m, c).contiguous()
+    dx, dg = torch.empty_like(x), torch.full((c,), 5.0, device="cuda")
+    ic.conv_layer_norm_grad(dy, x, None, mean, rstd, dx=dx, dgain=dg)
+    assert not dg.any()
+    want = f64(rstd)[:, None] * (f64(dy) - f64(dy).mean(1, keepdims=True))
+    d = np.abs(f64(dy))
+    check(dx, want, f64(rstd)[:, None] * ((c / 32 + 16) * 2.0 ** -23 * d.mean(1, keepdims=True) + 2.0 ** -21 * (d + 1)), "dx")
