@@ -567,7 +567,9 @@ conv_status conv_linear(const conv_matrix_desc *x, const void *x_dev, const conv
  * dbias_dev may be NULL: not computed; at least one is wanted.  With an
  * activation dz is rounded once to x's type before the products (as a
  * stored gradient would be); dbias sums it unrounded, in 32 bits.
- * ReLU's slope at 0 is 0.  M = 0 gives dw = 0 and dbias = 0; N = 0 gives
+ * ReLU's slope at 0 is 0, and so it is at a NaN; the other slopes of a NaN are
+ * NaN.  At an infinite pre-activation (a 16-bit one may have overflowed) every
+ * slope is its limit, 1 or 0.  M = 0 gives dw = 0 and dbias = 0; N = 0 gives
  * dx = 0.
  *
  * The workspace (conv_linear_grad_workspace_size bytes, 256-byte aligned)

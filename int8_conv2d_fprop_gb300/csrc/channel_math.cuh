@@ -198,8 +198,10 @@ __device__ __forceinline__ void activation_slope(float &a, float &b) {
         const Pair q = fma2(mul2(s, pair(-1.0f)), s, s);
         split(fma2(d, q, s), &a, &b);
     } else if constexpr (kAct == CONV_ACT_SILU) {
-        const Pair z = pair(a, b);
-        const Pair s = logistic_of(mul2(z, pair(-1.442695041f)));
+        // s + z s (1 - s), s = logistic(z); z held to +-128 in the second term,
+        // where s is 0 or 1 and the term has vanished, for the same reason
+        const Pair s = logistic_of(mul2(pair(a, b), pair(-1.442695041f)));
+        const Pair z = pair(fminf(fmaxf(a, -128.0f), 128.0f), fminf(fmaxf(b, -128.0f), 128.0f));
         const Pair q = fma2(mul2(s, pair(-1.0f)), s, s);
         split(fma2(z, q, s), &a, &b);
     } else {

@@ -122,3 +122,32 @@ def test_layer_norm_grad_of_constant_rows(ic, m, c):
     want = f64(rstd)[:, None] * (f64(dy) - f64(dy).mean(1, keepdims=True))
     d = np.abs(f64(dy))
     check(dx, want, f64(rstd)[:, None] * ((c / 32 + 16) * 2.0 ** -23 * d.mean(1, keepdims=True) + 2.0 ** -21 * (d + 1)), "dx")
+
+
+# ------------------------------------------------------- non-finite pre-activations
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dt", [F16, BF16])
+# the gradient's passes over dy: few rows; rows of aligned vectors, of any alignment; columns contiguous
+@pytest.mark.parametrize("m,n,cols", [(3, 24, False), (600, 24, False), (600, 25, False), (600, 24, True)])
+def test_slopes_at_infinite_and_nan_preactivations(ic, act, dt, m, n, cols):
+    """1 at plus infinity, 0 at minus infinity (the slopes' limits; 0 where dy is
+    0), NaN at a NaN, but ReLU's 0."""
+    g = gen(n)
+    z, dy = randn(g, m, n).to(dt), torch.zeros(m, n, device="cuda", dtype=dt)
+    inf, nan = float("inf"), float("nan")
+    z[1, 0], z[m - 1, 1], z[1, 2] = inf, -inf, nan
+    z[0, 3], z[1, 4] = inf, -inf
+    dy[1, 0], dy[m - 1, 1], dy[1, 2] = 2.0, 2.0, 2.0
+    x, w = randn(g, m, 8).to(dt), randn(g, n, 8).to(dt)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(n, device="cuda")
+    if cols:
+        z, dy = z.t().contiguous().t(), dy.t().contiguous().t()
+    ic.conv_linear_grad(dy, x, w, preact=z, activation=act, dx=dx, dw=dw, dbias=db)
+    assert db[0] == 2 and db[1] == 0 and not db[3:].any()
+    assert db[2] == 0 if act == "relu" else torch.isnan(db[2])
+    assert torch.equal(dw[0], 2 * x[1]) and not dw[1].any() and not dw[3:].any()
+    assert not dx[0].any() and not dx[m - 1].any()
+    if act == "relu":
+        assert torch.equal(dx[1], 2 * w[0]) and not dw[2].any()
+    else:
+        assert torch.isnan(dx[1]).all() and torch.isnan(dw[2]).all()
