@@ -409,36 +409,37 @@ GradPlan plan_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_ma
 }
 
 template <int kAct>
-void launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, void *dbias,
+bool launch_dz(const GradPlan &pl, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n, void *ws, void *dbias,
                int32_t bias_dtype, cudaStream_t s) {
     void *dz = pl.dz ? (char *)ws + pl.dz_off : nullptr;
     float *part = dbias && pl.parts > 1 ? (float *)((char *)ws + pl.part_off) : nullptr;
     const dim3 wide((unsigned)((n + 255) / 256), (unsigned)pl.parts);
     auto end = [&](const MatRef &a) { return a.p ? (const uint16_t *)a.p + (m - 1) * a.rs + n : nullptr; };
     if (pl.parts > 1 && n % 8 == 0 && vector_rows(dy) && vector_rows(pre))
-        launch_behind(linear_dz_rows_kernel<kAct, false>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
-                      pl.rows_per_part, dz, pl.dz_ld, part);
-    else if (pl.parts > 1 && dy.cs == 1 && (!pre.p || pre.cs == 1))
-        launch_behind(linear_dz_rows_kernel<kAct, true>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
-                      pl.rows_per_part, dz, pl.dz_ld, part);
-    else
-        launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts), pl.parts > 1 ? 256 : 1024,
-                      0, s, dy, pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part, part ? nullptr : dbias, bias_dtype);
+        return launch_behind(linear_dz_rows_kernel<kAct, false>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
+                             pl.rows_per_part, dz, pl.dz_ld, part);
+    if (pl.parts > 1 && dy.cs == 1 && (!pre.p || pre.cs == 1))
+        return launch_behind(linear_dz_rows_kernel<kAct, true>, wide, 256, 0, s, dy, pre, end(dy), end(pre), m, n,
+                             pl.rows_per_part, dz, pl.dz_ld, part);
+    return launch_behind(linear_dz_kernel<kAct>, dim3((unsigned)((n + 31) / 32), (unsigned)pl.parts),
+                         pl.parts > 1 ? 256 : 1024, 0, s, dy, pre, m, n, pl.rows_per_part, dz, pl.dz_ld, part,
+                         part ? nullptr : dbias, bias_dtype);
 }
 
 conv_status make_dz(const GradPlan &pl, int32_t act, const MatRef &dy, const MatRef &pre, int64_t m, int64_t n,
                     void *ws, void *dbias, int32_t bias_dtype, cudaStream_t s) {
+    bool ok;
     switch (act) {
-        case CONV_ACT_RELU: launch_dz<CONV_ACT_RELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
-        case CONV_ACT_GELU: launch_dz<CONV_ACT_GELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
-        case CONV_ACT_GELU_TANH: launch_dz<CONV_ACT_GELU_TANH>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
-        case CONV_ACT_SILU: launch_dz<CONV_ACT_SILU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
-        default: launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_RELU: ok = launch_dz<CONV_ACT_RELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_GELU: ok = launch_dz<CONV_ACT_GELU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_GELU_TANH: ok = launch_dz<CONV_ACT_GELU_TANH>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        case CONV_ACT_SILU: ok = launch_dz<CONV_ACT_SILU>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
+        default: ok = launch_dz<CONV_ACT_NONE>(pl, dy, pre, m, n, ws, dbias, bias_dtype, s); break;
     }
-    if (dbias && pl.parts > 1)
-        launch_behind(column_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, 0, s,
-                      (const float *)((char *)ws + pl.part_off), pl.parts, n, dbias, bias_dtype);
-    return cudaGetLastError() == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    if (ok && dbias && pl.parts > 1)
+        ok = launch_behind(column_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, 0, s,
+                           (const float *)((char *)ws + pl.part_off), pl.parts, n, dbias, bias_dtype);
+    return ok ? CONV_OK : CONV_ERR_CUDA;
 }
 
 }  // namespace
