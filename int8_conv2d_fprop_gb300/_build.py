@@ -5,15 +5,18 @@ Every translation unit under ``csrc/`` is compiled in parallel into
 ``_build/`` and linked into ``libint8conv.so`` next to this file;
 ``csrc/python/channel_binding.cpp`` is compiled against torch's headers into
 ``_channel.so``, which loads the library.  Rebuilds only what is older than a
-source or header.
+source or header, and the binding where it was built for another Python or
+torch; without torch the library alone is built (its C entry points need none).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +27,7 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint8conv.so")
 BINDING_SRC = os.path.join(CSRC, "python", "channel_binding.cpp")
 BINDING = os.path.join(PKG, "_channel.so")
+BINDING_STAMP = os.path.join(OBJDIR, "channel_binding.txt")  # what the binding was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -53,18 +57,30 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def torch_root() -> str | None:
+    """Where torch is installed (without importing it), or None."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def binding_target() -> str:
+    """The Python and the torch that a binding built now would be for."""
+    with open(os.path.join(torch_root(), "version.py")) as f:
+        return f"{sys.version}\n{sysconfig.get_paths()['include']}\n{torch_root()}\n{f.read()}"
+
+
 def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_STAMP):
         return False
     t = os.path.getmtime(BINDING)
     deps = [BINDING_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return all(os.path.getmtime(d) <= t for d in deps)
+    with open(BINDING_STAMP) as f:
+        return all(os.path.getmtime(d) <= t for d in deps) and f.read() == binding_target()
 
 
 def build_binding() -> None:
     """_channel.so; needs the library next to it to link with."""
-    import torch
-    root = os.path.dirname(torch.__file__)
+    root = torch_root()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-o", tmp, BINDING_SRC, "-I", INCLUDE,
@@ -76,11 +92,16 @@ def build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(binding_target())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     build_library(force, verbose, extra_flags)
-    if force or not binding_up_to_date():
+    if torch_root() is None:
+        print("torch is not installed: the channel operators' Python binding is left out", file=sys.stderr)
+    elif force or not binding_up_to_date():
         build_binding()
     return LIB
 
@@ -115,6 +136,5 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=()) ->
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True,
                 extra_flags=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else []))
