@@ -79,8 +79,9 @@ struct Summer {
 // warp) meets the same lead on all its rows whatever the row stride, and its
 // columns stay in the same registers: odd widths cost two partial groups per
 // row.  This wants one lead for all the matrices a call reads; an output with
-// another one is turned through shared memory, a row at a time.  Otherwise thread t
-// holds elements t, t + T, ..., one per access.
+// another one is turned through shared memory, a row at a time.  The gradient of
+// matrices with several leads has thread t hold elements t, t + T, ..., one per
+// access.
 template <typename T>
 constexpr bool kIs16 = sizeof(T) == 2;
 
@@ -289,7 +290,7 @@ struct NormArgs {
     int32_t turn;  // y's rows have another lead than x's
 };
 
-template <typename X, typename Y, int kNv, bool kVec, bool kWarp>
+template <typename X, typename Y, int kNv, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 256 : norm_threads(kNv), kWarp ? (kNv == 4 ? 2 : 1) : norm_blocks(kNv))
     layer_norm_rows_kernel(const NormArgs a) {
     __shared__ __align__(16) BlockSums sums;
@@ -301,11 +302,11 @@ __global__ void __launch_bounds__(kWarp ? 256 : norm_threads(kNv), kWarp ? (kNv 
     const int64_t step = kWarp ? (int64_t)gridDim.x * 8 : gridDim.x;
     const X *x = (const X *)a.x.p;
     Y *y = (Y *)const_cast<void *>(a.y.p);
-    Place<kVec> at;
+    Place<true> at;
     at.t = kWarp ? threadIdx.x % 32 : threadIdx.x;
     at.threads = kWarp ? 32 : blockDim.x;
     at.cols = a.cols;
-    at.lead = kVec ? lead_of(x + first * a.x.rs) : 0;
+    at.lead = lead_of(x + first * a.x.rs);
     const float per = 1.0f / (float)a.cols;
     constexpr bool kKeep = kNv <= 2;  // parameters in registers over the rows
     const Turn<Y> turn{(Y *)(shared + (kKeep ? 0 : kNv * 16 * blockDim.x)) +
@@ -388,10 +389,10 @@ __global__ void __launch_bounds__(kWarp ? 256 : norm_threads(kNv), kWarp ? (kNv 
                     w[3] = w[3] * rstd * __uint_as_float(g.w) + __uint_as_float(b.w);
                 }
             }
-            if (kVec && a.turn) turn_group(turn, at, i, v[i]);
+            if (a.turn) turn_group(turn, at, i, v[i]);
             else store_group(y + r * a.y.rs, at, i, v[i]);
         }
-        if (kVec && a.turn) {
+        if (a.turn) {
             row_sync<kWarp>();
             store_turned(y + r * a.y.rs, turn, at);
             if (kWarp) __syncwarp();  // (a block's next row has barriers before it writes again)
@@ -835,7 +836,7 @@ RowShape row_shape(int64_t cols, const MatRef &x, bool vec, bool grad) {
     const Lead l = lead_of_rows(x);
     const bool aligned = l.base == 0 && l.step == 0;
     const int64_t groups = vec && !aligned ? (cols + 14) / 8 : (cols + 7) / 8;
-    if (groups <= (grad || !vec ? 64 : 128)) {
+    if (groups <= (grad ? 64 : 128)) {
         s.warp = true;
         s.threads = 256;
         s.nv = groups <= 32 ? 1 : groups <= 64 ? 2 : 4;
@@ -877,15 +878,12 @@ template <typename X, typename Y>
 bool launch_norm(const NormArgs &a, const RowShape &sh, unsigned grid, cudaStream_t s) {
     const size_t smem = (sh.nv == 4 ? (size_t)sh.threads * 256 : 0) +
                         (a.turn ? (size_t)turn_elems(a.cols) * sizeof(Y) * (sh.warp ? 8 : 1) : 0);
-#define I8C_NORM(NV, W)                                                                                       \
-    (sh.vec ? launch_behind(layer_norm_rows_kernel<X, Y, NV, true, W>, dim3(grid), sh.threads, smem, s, a)          \
-         : launch_behind(layer_norm_rows_kernel<X, Y, NV, false, W>, dim3(grid), sh.threads, smem, s, a))
     if (sh.nv == 4)
-        return sh.warp ? launch_large<layer_norm_rows_kernel<X, Y, 4, true, true>>(dim3(grid), sh.threads, smem, s, a)
-                       : launch_large<layer_norm_rows_kernel<X, Y, 4, true, false>>(dim3(grid), sh.threads, smem, s, a);
-    if (sh.warp) return sh.nv == 1 ? I8C_NORM(1, true) : I8C_NORM(2, true);
-    return I8C_NORM(2, false);
-#undef I8C_NORM
+        return sh.warp ? launch_large<layer_norm_rows_kernel<X, Y, 4, true>>(dim3(grid), sh.threads, smem, s, a)
+                       : launch_large<layer_norm_rows_kernel<X, Y, 4, false>>(dim3(grid), sh.threads, smem, s, a);
+    if (!sh.warp) return launch_behind(layer_norm_rows_kernel<X, Y, 2, false>, dim3(grid), sh.threads, smem, s, a);
+    return sh.nv == 1 ? launch_behind(layer_norm_rows_kernel<X, Y, 1, true>, dim3(grid), sh.threads, smem, s, a)
+                      : launch_behind(layer_norm_rows_kernel<X, Y, 2, true>, dim3(grid), sh.threads, smem, s, a);
 }
 
 template <typename X>
@@ -982,8 +980,9 @@ conv_status conv_layer_norm(const conv_matrix_desc *x, const void *x_dev, const 
     a.rows = rows, a.cols = (int32_t)cols;
     a.eps = p->eps, a.scale = p->scale, a.param_dtype = p->param_dtype;
     const cudaStream_t s = (cudaStream_t)stream;
-    const RowShape sh = row_shape(cols, a.x, one_lead({&a.x, &a.y}) || turnable(cols, y->dtype), false);
     a.turn = !one_lead({&a.x, &a.y});
+    // (rows too wide to be turned are too wide for an element per access too)
+    const RowShape sh = a.turn && !turnable(cols, y->dtype) ? RowShape() : row_shape(cols, a.x, true, false);
     bool ok;
     if (sh.nv == 0 || !unit_columns(a.x) || !unit_columns(a.y)) {
         ok = launch_behind(layer_norm_any_kernel, dim3((unsigned)rows), cols > 4096 ? 1024 : 256, 0, s, a);
