@@ -10,14 +10,15 @@
 
 namespace {
 struct Launch {
-    int64_t grid, block, smem, kernel;
+    int64_t grid, block, smem, kernel, cluster;
 };
 std::vector<Launch> launches;
 int fail_at = -1;                         // this launch fails
 cudaError_t last_error = cudaSuccess;
 
-cudaError_t launch(const void *kernel, dim3 grid, dim3 block, size_t smem) {
-    launches.push_back({(int64_t)grid.x * grid.y * grid.z, (int64_t)block.x * block.y * block.z, (int64_t)smem, (int64_t)kernel});
+cudaError_t launch(const void *kernel, dim3 grid, dim3 block, size_t smem, int cluster) {
+    launches.push_back({(int64_t)grid.x * grid.y * grid.z, (int64_t)block.x * block.y * block.z, (int64_t)smem,
+                        (int64_t)kernel, cluster});
     if ((int)launches.size() - 1 != fail_at) return cudaSuccess;
     return last_error = cudaErrorLaunchOutOfResources;
 }
@@ -35,17 +36,20 @@ void fake_reset(int fail, int stale) {
 }
 int fake_launches(int64_t *out, int most) {
     for (int i = 0; i < (int)launches.size() && i < most; ++i) {
-        out[4 * i] = launches[i].grid, out[4 * i + 1] = launches[i].block;
-        out[4 * i + 2] = launches[i].smem, out[4 * i + 3] = launches[i].kernel;
+        out[5 * i] = launches[i].grid, out[5 * i + 1] = launches[i].block, out[5 * i + 2] = launches[i].smem;
+        out[5 * i + 3] = launches[i].kernel, out[5 * i + 4] = launches[i].cluster;
     }
     return (int)launches.size();
 }
 
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **) {
-    return launch(f, c->gridDim, c->blockDim, c->dynamicSmemBytes);
+    int cluster = 0;
+    for (unsigned i = 0; i < c->numAttrs; ++i)
+        if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = (int)c->attrs[i].val.clusterDim.x;
+    return launch(f, c->gridDim, c->blockDim, c->dynamicSmemBytes, cluster);
 }
 cudaError_t __cudaLaunchKernel(cudaKernel_t f, dim3 grid, dim3 block, void **, size_t smem, cudaStream_t) {
-    return launch(f, grid, block, smem);
+    return launch(f, grid, block, smem, 0);
 }
 cudaError_t cudaGetLastError(void) {
     const cudaError_t e = last_error;

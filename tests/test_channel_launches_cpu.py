@@ -55,9 +55,10 @@ def address():
 
 
 def launches(fake):
-    out = (ctypes.c_int64 * 64)()
+    """(blocks, threads, shared memory, kernel, cluster size or 0) of each."""
+    out = (ctypes.c_int64 * 80)()
     n = fake.fake_launches(out, 16)
-    return [tuple(out[4 * i:4 * i + 4]) for i in range(n)]
+    return [tuple(out[5 * i:5 * i + 5]) for i in range(n)]
 
 
 def linear(fake, m, k, n, dtype=BF16, act=2, out=None, pad=0, residual=True, preact=True):
@@ -119,3 +120,35 @@ def test_an_earlier_error_is_not_this_calls(fake, call):
     fake.fake_reset(-1, 1)
     assert CALLS[call](fake) == OK
     assert fake.cudaGetLastError() != 0  # left for whose it is
+
+
+def test_sizes_reach_the_forms_they_are_tested_for(fake):
+    """The product's forms by what they launch: a cluster of 2 for each pair's
+    tile, clusters of single CTAs that share one, a joining kernel behind sums
+    cut into runs."""
+    import channel_sizes as sizes
+
+    def made(size):
+        fake.fake_reset(-1, 0)
+        assert linear(fake, *size) == OK
+        return launches(fake)
+
+    single, pairs = made((100, 64, 64))[0][3], made((50176, 512, 2048))[0][3]
+    assert single != pairs
+    for size in sizes.PAIR_TILES:
+        (_, _, _, kernel, cluster), = made(size)
+        assert kernel == pairs and cluster == 2, size
+    for size in sizes.WIDE_SINGLE_TILES:
+        (_, _, _, kernel, cluster), = made(size)
+        assert kernel == single and cluster == 1, size
+    for size in sizes.JOINED_RUNS + sizes.CUT_LAST_ROUND:
+        first, join = made(size)
+        assert first[3] == pairs and first[4] == 2 and join[3] not in (single, pairs), size
+        tiles = -(-size[0] // 256) * -(-size[2] // 256)
+        assert (tiles < 76) == (size in sizes.JOINED_RUNS), size
+    for split, size in sizes.CLUSTERS:
+        (_, _, _, kernel, cluster), = made(size)
+        assert kernel == single and cluster == split, size
+    for size in sizes.FEW_ROWS:
+        _, threads, _, kernel, cluster = made(size)[-1]  # (behind the copies of rows that are not aligned)
+        assert threads == 256 and cluster == 0, size
