@@ -145,6 +145,10 @@ __device__ __forceinline__ Pair gelu_tanh_arg(Pair z) {
 // 32-bit arithmetic, and falling below 2^-126 before x = -16.  One
 // exponential per value and half the instructions of a polynomial times
 // exp(-x^2/2).
+// That is the accuracy of 1 + erf in 32 bits, and like it absolute: of Phi
+// itself it is 0.24 % at -4, 2.1 % at -5 and 8.8 % at -6.  (Accuracy of 2^-12
+// of Phi takes degree 11 and 12 us of the 111 us of 50176 x 512 -> 2048 with a
+// pre-activation, 2^-10 degree 8 and 5.5 us.)
 __device__ __forceinline__ Pair normal_tail(Pair x) {
     Pair p = fma2(x, pair(1.917647205e-05f), pair(6.586165400e-04f));
     p = fma2(x, p, pair(7.754437625e-03f));

@@ -151,3 +151,23 @@ def test_slopes_at_infinite_and_nan_preactivations(ic, act, dt, m, n, cols):
         assert torch.equal(dx[1], 2 * w[0]) and not dw[2].any()
     else:
         assert torch.isnan(dx[1]).all() and torch.isnan(dw[2]).all()
+
+
+# --------------------------------------------------------------------- GELU
+@pytest.mark.parametrize("m", [1, 100, 3000])
+def test_gelu_is_as_exact_as_stated(ic, m):
+    """Phi off by 1.4e-7 by its fit and 2^-23 by its exponential (2^-22.5 of a
+    value of at most a half), then one rounding; the slope's second term, at
+    most a quarter, by a few 2^-22 of itself."""
+    n = 1040
+    z = torch.linspace(-16.5, 16.5, n, device="cuda").to(BF16)
+    x, w = torch.zeros(m, 8, device="cuda", dtype=BF16), torch.zeros(n, 8, device="cuda", dtype=BF16)
+    x[:, 0], w[:, 0] = 1.0, z
+    y = ic.conv_linear(x, w, activation="gelu", out=torch.empty(m, n, device="cuda"))
+    f = f64(z)
+    want = oc.activate(f, "gelu")
+    check(y, np.broadcast_to(want, (m, n)), (1.4e-7 + 2.0 ** -23) * np.abs(f) + 2.0 ** -23 * np.abs(want) + 2.0 ** -126, "y")
+    # the bias gradient of one row is dy times the slope, in 32 bits
+    one, db = torch.ones(1, n, device="cuda", dtype=BF16), torch.empty(n, device="cuda")
+    ic.conv_linear_grad(one, x[:1], w, preact=z[None], activation="gelu", dbias=db)
+    check(db, oc.activation_slope(f, "gelu"), np.full(n, 2.0 ** -21), "slope")
