@@ -27,6 +27,8 @@ CHANNEL_SYMBOLS = (
 )
 
 
+# The C ABI's structures and argument types, for callers of libint8conv.so
+# through ctypes; the entry points below go through the compiled binding.
 class MatrixDesc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("col_stride", ctypes.c_int64),

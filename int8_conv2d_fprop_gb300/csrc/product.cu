@@ -10,8 +10,9 @@
 // forward product and both gradients are one kernel.
 //
 // What bounds it: with long sums the loads' latency over the ring (32 KB per
-// k-step and SM; 4 / 5 / 6 stages take 695 / 621 / 582 us on 8192 x 4096 ->
-// 16384, 1.89 PFLOP/s) and, over seconds, the power cap; with short ones what
+// k-step and SM; 4 / 5 / 6 stages took 695 / 621 / 582 us on 8192 x 4096 ->
+// 16384 on a cool device) and the power cap (626 us alone, replayed; 675-680 us
+// among calls on other data, 1.62 PFLOP/s); with short ones what
 // an SM moves in and out (50176 x 512 -> 2048: 3.5 us for each round of 76
 // tiles, 95 GB/s per SM; 4.9 with GELU and a second output); a single small
 // tile takes 3.5 us: 0.6 of set-up, 1.0 for its first loads, 0.3 for the
@@ -313,10 +314,7 @@ __device__ __forceinline__ void rows_to_slot(const WarpTile &t, const char *p, i
     for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane / 4 + 8 * i, t.lane & 3), q[i]);
 }
 
-// The same for any strides, an element at a time, `cols` columns from column
-// b0 + c on: lanes along the rows, or along the columns (32 of 16 bits, or 16
-// of 32 bits and two rows).
-// 16-bit rows, two at a time, in 32-bit words where a row's alignment has
+// 16-bit rows, two at a time, from and to the slot in 32-bit words where a row's alignment has
 // them: lane w of a row takes columns 2w - odd and the next, and the last lane
 // the column that is left.  p: the first row's first element.
 __device__ __noinline__ void slot_to_words(uint16_t *p, int64_t row, int rows, int cols, uint32_t slot) {
@@ -360,6 +358,9 @@ __device__ __noinline__ void words_to_slot(const uint16_t *p, int64_t row, int r
     }
 }
 
+// The same for any strides, an element at a time, `cols` columns from column
+// b0 + c on: lanes along the rows, or along the columns (32 of 16 bits, or 16
+// of 32 bits and two rows).
 __device__ __noinline__ void slot_to_any(Side s, WarpTile t, int c, int cols) {
     const bool wide = s.dtype == CONV_FLOAT32;
     if (s.walk == kWalkAlongA) {
@@ -1058,7 +1059,7 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k) {
         const int64_t tiles = pl.tiles_a * pl.tiles_b;
         // Fewer tiles than pairs: all of them in runs.  A last round that
         // leaves half the pairs idle or more: its tiles in runs, where that
-        // saves more than the joining kernel takes (about 8 us, 24 k-steps).
+        // saves 40 k-steps or more (14 us; the joining kernel takes about 8).
         const int64_t last = tiles % (kSms / 2);
         int64_t parts = 1;
         if (tiles * 2 < kSms) parts = std::min(kSms / 2 / tiles, k_steps / 8);
@@ -1144,8 +1145,8 @@ conv_status product_launch(const Product &given, void *workspace, void *stream) 
     const int grid = a.split > 1 ? (int)units * a.split : (int)std::min<int64_t>(units, sms / cluster) * cluster;
     a.b_boxes = (int32_t)cdiv(a.b_rows, 64);
     a.stage_bytes = 16384 + (int32_t)round_up(a.b_mn ? a.b_boxes * 8192 : a.b_rows * 128, 1024);
-    // (long sums hide the epilogue and want the slots' stage of the ring: 4 / 5
-    // / 6 stages take 695 / 621 / 582 us at 8192 x 4096 x 16384)
+    // (long sums hide the epilogue and want the slots' stage of the ring, see
+    // the stages' times at the head of this file)
     a.slots = a.res.walk == kWalkRows && a.res.dtype != CONV_FLOAT32 && a.split == 1 && pl.parts == 1 && a.k_steps <= 24 ? 2 : 1;
     a.stages = std::min(kMaxStages, (kRingBytes - (a.slots - 1) * kEpilogueWarps * kSlotBytes) / a.stage_bytes);
     const int tile_a = pair ? 256 : 128;
