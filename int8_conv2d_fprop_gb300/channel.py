@@ -10,8 +10,9 @@ copied).  Outputs that are not given are allocated; a workspace that is not
 given (or is too small) is allocated for the call, on the stream the call
 runs on.  Autograd does not record these calls: a tensor that requires a
 gradient is refused while gradients are recorded (detach it, or call under
-``torch.no_grad()``), and outputs count as changed in place.  The marshalling itself is compiled (csrc/python): read from Python,
-the tensors' attributes take longer than the smallest kernels.
+``torch.no_grad()``), and outputs count as changed in place.  The marshalling
+itself is compiled (csrc/python): read from Python, the tensors' attributes
+take longer than the smallest kernels.
 """
 from __future__ import annotations
 

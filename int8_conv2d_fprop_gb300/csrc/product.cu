@@ -11,8 +11,8 @@
 //
 // What bounds it: with long sums the loads' latency over the ring (32 KB per
 // k-step and SM; 4 / 5 / 6 stages took 695 / 621 / 582 us on 8192 x 4096 ->
-// 16384 on a cool device) and the power cap (626 us alone, replayed; 675-680 us
-// among calls on other data, 1.62 PFLOP/s); with short ones what
+// 16384, as replayed when they were compared) and the power cap (577-626 us
+// replayed, 675-680 us among calls on other data: 1.62 PFLOP/s); with short ones what
 // an SM moves in and out (50176 x 512 -> 2048: 3.5 us for each round of 76
 // tiles, 95 GB/s per SM; 4.9 with GELU and a second output); a single small
 // tile takes 3.5 us: 0.6 of set-up, 1.0 for its first loads, 0.3 for the
