@@ -76,14 +76,17 @@ typedef enum {
 } conv_status;
 
 /* The convolution entry points take CONV_INT8 and CONV_INT32; the float types
- * belong to the channel operators (conv_linear, conv_layer_norm and their
- * gradients). */
+ * belong to the channel operators (conv_linear, conv_layer_norm and what
+ * follows them below).  The 8-bit floats are the ones with 4 exponent and 3
+ * mantissa bits (largest 448, no infinity) and with 5 and 2 (largest 57344). */
 typedef enum {
     CONV_INT8 = 1,
     CONV_INT32 = 2,
     CONV_FLOAT32 = 3,
     CONV_FLOAT16 = 4,
-    CONV_BFLOAT16 = 5
+    CONV_BFLOAT16 = 5,
+    CONV_FLOAT8_E4M3 = 6,
+    CONV_FLOAT8_E5M2 = 7
 } conv_dtype;
 
 typedef enum { CONV_CROSS_CORRELATION = 0, CONV_CONVOLUTION = 1 } conv_mode;
@@ -642,6 +645,200 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
                                  const void *residual_grad_dev, const conv_matrix_desc *dx, void *dx_dev,
                                  void *dgain_dev, void *dshift_dev, const conv_layer_norm_params *p, void *workspace,
                                  size_t workspace_bytes, void *stream);
+
+/*
+ * 8-bit operands: blocks of 128 elements with a 32-bit scale each.
+ *
+ * Quantisation of x [M,C] (CONV_FLOAT32, CONV_FLOAT16 or CONV_BFLOAT16): with
+ * v = x, or v = x * act'(preact) where an activation is given (the loss
+ * gradient before an activation, unrounded; preact [M,C] of CONV_FLOAT16 or
+ * CONV_BFLOAT16, or x's type; slopes as in conv_linear_grad),
+ *   scale = max(a / L, 2^-126),  q = v / scale rounded to nearest even
+ * where a is the largest magnitude of the block and L the largest value of
+ * q's type.  (q is made as v * (L / a), off by 2^-23 of itself before it is
+ * rounded.)  Blocks are 128 elements of a row (tile 1) or squares of 128 x
+ * 128 (tile 128), counted from the first row and column; the last ones may be
+ * short.  A block that holds an infinity or a NaN has it as its scale, and
+ * everything made of the block is NaN.
+ *   q   [M,C], scale  [ceil(M / tile), ceil(C / 128)]   (rows)
+ *   qt  [C,M], scale_t [ceil(C / tile), ceil(M / 128)]  (columns: the same of
+ *              x transposed, which is what a product over the rows wants)
+ * Either pair, or both from one reading of x; at least one is wanted.  q and
+ * qt are of one type, CONV_FLOAT8_E4M3 or CONV_FLOAT8_E5M2; the scales are
+ * CONV_FLOAT32.  Any strides.  (For tile 128 scale_t is scale transposed.)
+ * No workspace.  M = 0 or C = 0 does nothing.
+ *
+ * Errors: CONV_ERR_NULL_PTR (also a pair half given, and an activation
+ * without preact); CONV_ERR_DTYPE; CONV_ERR_BAD_PARAM (tile, activation,
+ * reserved fields); CONV_ERR_SHAPE_MISMATCH; CONV_ERR_BAD_STRIDES;
+ * CONV_ERR_BUFFER_TOO_SMALL; CONV_ERR_ALIGNMENT; CONV_ERR_TOO_LARGE;
+ * CONV_ERR_OVERLAP (an output shares bytes with anything else of the call);
+ * CONV_ERR_CUDA; CONV_ERR_UNSUPPORTED_DEVICE.
+ */
+typedef struct {
+    int32_t tile;        /* rows that share a scale: 1 or 128 */
+    int32_t activation;  /* conv_activation */
+    int32_t reserved[2]; /* must be 0 */
+} conv_quantize_params;
+
+conv_status conv_quantize(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *preact,
+                          const void *preact_dev, const conv_matrix_desc *q, void *q_dev,
+                          const conv_matrix_desc *scale, void *scale_dev, const conv_matrix_desc *qt, void *qt_dev,
+                          const conv_matrix_desc *scale_t, void *scale_t_dev, const conv_quantize_params *p,
+                          void *stream);
+
+/*
+ * conv_linear of 8-bit operands with block scales: with sx and sw the scales
+ * of row m's and row n's blocks (b counts 128 elements of K),
+ *   z[m,n] = sum_b sx[m,b] * sw[n,b] * (sum over block b of x[m,k] * w[n,k])
+ *            + bias[n]
+ *   y[m,n] = act(z[m,n]) + residual[m,n],   preact[m,n] = z[m,n]
+ * x [M,K] and w [N,K] are CONV_FLOAT8_E4M3 or CONV_FLOAT8_E5M2, each its own,
+ * with adjacent columns (any row stride).  x_scale is CONV_FLOAT32 of
+ * [M, ceil(K / 128)] (a scale for each row) or [ceil(M / 128), ceil(K / 128)]
+ * (for each square), w_scale likewise with N; any strides.  y [M,N] is
+ * CONV_FLOAT32, CONV_FLOAT16 or CONV_BFLOAT16, residual [M,N] of y's type,
+ * preact [M,N] CONV_FLOAT16 or CONV_BFLOAT16; the bias holds
+ * p->bias_dtype, CONV_FLOAT32 or y's type.
+ * Products are exact, the sums of a block and over the blocks are in 32 bits,
+ * and y and preact are each rounded once.
+ *
+ * The gradients are products of the same kind: with w quantised in columns
+ * (wt) and the loss gradient dz quantised both ways (dz, dzt),
+ *   dx = dz wt^T (M x K over N),  dw = dzt xt^T (N x K over M).
+ *
+ * M = 0 or N = 0 does nothing; K = 0 gives act(bias) + residual.  residual may
+ * be the same matrix as y.  The workspace holds packed copies of x and w
+ * unless their rows are 16-byte aligned, and partial sums of products cut
+ * into runs.  Workspace rules, asynchrony, repeatability and errors as for
+ * conv_linear (CONV_ERR_BAD_STRIDES also for columns of x or w that are not
+ * adjacent).
+ */
+conv_status conv_linear_fp8_workspace_size(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *w,
+                                           const void *w_dev, size_t *bytes);
+
+conv_status conv_linear_fp8(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *x_scale,
+                            const void *x_scale_dev, const conv_matrix_desc *w, const void *w_dev,
+                            const conv_matrix_desc *w_scale, const void *w_scale_dev, const void *bias_dev,
+                            const conv_matrix_desc *residual, const void *residual_dev,
+                            const conv_matrix_desc *preact, void *preact_dev, const conv_matrix_desc *y, void *y_dev,
+                            const conv_linear_params *p, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A residual block's end and the next one's beginning: the norm behind the
+ * block, its gate, the residual sum and the norm before the next block.  For
+ * a block's output x [M,C] and the stream skip [M,C] that went around it:
+ *   n   = x * rx * post_gain, rx = 1 / sqrt(sum x^2 / C + eps)  (post_norm;
+ *         otherwise n = x)
+ *   sum = skip_scale * skip + branch_scale * gate * n
+ *   y   = sum * rs * gain,    rs = 1 / sqrt(sum of sum^2 / C + eps)
+ * Every part may be left out: skip (with skip_dev) NULL is none; gate NULL is
+ * 1; post_gain_dev and gain_dev NULL are 1; sum NULL is not written, y NULL
+ * not computed (at least one of the two is wanted).  With x and y alone this
+ * is the root-mean-square norm of x.
+ * x is CONV_FLOAT32, CONV_FLOAT16 or CONV_BFLOAT16; skip and sum are of one
+ * type, x's or CONV_FLOAT32; y is of x's type or, with y_scale [M,
+ * ceil(C / 128)] of CONV_FLOAT32, CONV_FLOAT8_E4M3: quantised as by
+ * conv_quantize with tile 1.  gate is [G,C] of CONV_FLOAT32 or x's type, M a
+ * multiple of G: row g of it serves rows g M/G up to (g + 1) M/G.  Gains hold
+ * C values of param_dtype; post_rstd_dev (rx) and rstd_dev (rs) receive M
+ * 32-bit floats and may be NULL.
+ * Everything between reading and the rounding of sum and y (each once; y is
+ * made of the unrounded sum) is in 32 bits.  sum may be the same matrix as
+ * skip, and y or sum the same as x where the types are the same.  C is 1 to
+ * 49152.  M = 0 does nothing.  No workspace.  A row with an infinity or a NaN
+ * gives NaN in that row alone.
+ * Errors as for conv_layer_norm (CONV_ERR_SHAPE_MISMATCH also where G does
+ * not divide M, CONV_ERR_TOO_LARGE also for C).
+ */
+typedef struct {
+    float eps;           /* > 0, finite */
+    float skip_scale;    /* finite */
+    float branch_scale;  /* finite */
+    int32_t post_norm;   /* 0 or 1 */
+    int32_t param_dtype; /* type of the gains (and of their gradients): CONV_FLOAT32 or x's type */
+    int32_t reserved[3]; /* must be 0 */
+} conv_block_norm_params;
+
+conv_status conv_block_norm(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_desc *skip,
+                            const void *skip_dev, const conv_matrix_desc *gate, const void *gate_dev,
+                            const void *post_gain_dev, const void *gain_dev, const conv_matrix_desc *sum,
+                            void *sum_dev, const conv_matrix_desc *y, void *y_dev, const conv_matrix_desc *y_scale,
+                            void *y_scale_dev, float *post_rstd_dev, float *rstd_dev,
+                            const conv_block_norm_params *p, void *stream);
+
+/*
+ * Gradients of conv_block_norm for the loss gradients dy [M,C] of y (of x's
+ * type) and dsum [M,C] of sum (what reaches the stream from later blocks; of
+ * the stream's type), either of which may be NULL (0), not both; with
+ * h = sum as the forward call wrote it and the statistics rx and rs:
+ *   t  = dy * gain,  u = h * rs,  dh = dsum + rs * (t - u * sum (t u) / C)
+ *   dskip = skip_scale * dh,  db = branch_scale * gate * dh
+ *   v  = x * rx (post_norm; else x),  dn = db * post_gain
+ *   dx = rx * (dn - v * sum (dn v) / C)  (post_norm; else dx = db)
+ *   dgate[g] = branch_scale * post_gain * sum over g's rows of dh * v
+ *   dgain = sum over the rows of dy * u,  dpost_gain = sum over the rows of db * v
+ * h (sum) and rstd_dev are wanted with dy, x with a post norm or dgate, and
+ * post_rstd_dev with a post norm.  Each of dx (of x's type), dskip (of the
+ * stream's type: h's and dsum's), dgate ([G,C] of CONV_FLOAT32 or x's type;
+ * without a gate G is its number of rows), dgain_dev and dpost_gain_dev (C
+ * values of param_dtype; dpost_gain only with a post norm, dgain only with
+ * dy) may be NULL: not computed; at least one is wanted.  dskip may be the
+ * same matrix as dsum, and dx the same as dy.  Sums are in 32 bits, in an
+ * order that does not depend on timing.  M = 0 gives zero for the sums over
+ * rows.  C is 1 to 24576.
+ *
+ * The workspace (conv_block_norm_grad_workspace_size bytes, 256-byte aligned)
+ * holds partial sums; groups is G of gate and dgate (1 without them).
+ * Errors as for conv_block_norm.
+ */
+conv_status conv_block_norm_grad_workspace_size(const conv_matrix_desc *x, int64_t groups, size_t *bytes);
+
+conv_status conv_block_norm_grad(const conv_matrix_desc *dy, const void *dy_dev, const conv_matrix_desc *dsum,
+                                 const void *dsum_dev, const conv_matrix_desc *x, const void *x_dev,
+                                 const conv_matrix_desc *sum, const void *sum_dev, const conv_matrix_desc *gate,
+                                 const void *gate_dev, const void *post_gain_dev, const void *gain_dev,
+                                 const float *post_rstd_dev, const float *rstd_dev, const conv_matrix_desc *dx,
+                                 void *dx_dev, const conv_matrix_desc *dskip, void *dskip_dev,
+                                 const conv_matrix_desc *dgate, void *dgate_dev, void *dpost_gain_dev,
+                                 void *dgain_dev, const conv_block_norm_params *p, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Global norm of many gradient tensors, and clipping by it:
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + eps)), rounded once
+ * Each tensor is `count` adjacent elements of CONV_FLOAT32, CONV_FLOAT16 or
+ * CONV_BFLOAT16; out is of the same type, and NULL for clipping in place
+ * (where a factor of 1 writes nothing).  norm_dev receives one 32-bit float.
+ * max_norm infinite only takes the norm (out is not written).  The squares are
+ * summed in 32 bits over 32 elements and in 64 beyond, with 64-bit squares
+ * where 32 bits would overflow or underflow, in an order that depends on
+ * neither timing nor addresses.  As the formulas have it, an infinite norm
+ * gives a factor of 0 and a NaN one of NaN.
+ * Tensors that share bytes (also one that is given twice) are refused, as is
+ * an out that shares bytes with any tensor or out but its own.  The table of
+ * tensors is read before the call returns.
+ * Workspace: conv_clip_grads_workspace_size bytes, 256-byte aligned (partial
+ * sums).  Errors: CONV_ERR_NULL_PTR; CONV_ERR_DTYPE; CONV_ERR_BAD_PARAM
+ * (n or count negative, max_norm or eps negative or NaN, eps infinite,
+ * reserved not 0); CONV_ERR_ALIGNMENT; CONV_ERR_TOO_LARGE (2^45 elements or
+ * more in one tensor, 2^31 chunks of 16384 elements in all);
+ * CONV_ERR_OVERLAP; CONV_ERR_WORKSPACE; CONV_ERR_CUDA;
+ * CONV_ERR_UNSUPPORTED_DEVICE.
+ */
+typedef struct {
+    const void *grad;
+    void *out;
+    int64_t count;
+    int32_t dtype;
+    int32_t reserved; /* must be 0 */
+} conv_grad_tensor;
+
+conv_status conv_clip_grads_workspace_size(const conv_grad_tensor *tensors, int64_t n, size_t *bytes);
+
+conv_status conv_clip_grads(const conv_grad_tensor *tensors, int64_t n, float max_norm, float eps, float *norm_dev,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a status. */
 const char *conv_status_string(conv_status s);

@@ -15,8 +15,8 @@ element strides, exactly what a torch tensor's ``size()``/``stride()`` give
 (a channels_last tensor is NHWC in memory).
 
 The channel operators that follow a convolution (matrix product with bias,
-activation and residual, layer norm, and their gradients) are in
-``channel.py`` and re-exported here.
+activation and residual, also of 8-bit floats, layer norm, block norms, and
+their gradients) are in ``channel.py`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -26,8 +26,11 @@ from typing import Optional, Sequence, Tuple
 
 from . import channel
 from .channel import (  # noqa: F401
-    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ACTIVATIONS, CONV_BFLOAT16, CONV_FLOAT16, CONV_FLOAT32,
-    LayerNormParams, LinearParams, MatrixDesc, conv_layer_norm, conv_layer_norm_grad, conv_linear, conv_linear_grad,
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ACTIVATIONS, BlockNormParams,
+    CONV_BFLOAT16, CONV_FLOAT16, CONV_FLOAT32,
+    CONV_FLOAT8_E4M3, CONV_FLOAT8_E5M2, GradTensor, LayerNormParams, LinearParams, MatrixDesc, QuantizeParams,
+    conv_block_norm, conv_block_norm_grad, conv_clip_grads, conv_layer_norm, conv_layer_norm_grad, conv_linear,
+    conv_linear_fp8, conv_linear_grad, conv_quantize,
 )
 
 _PKG = os.path.dirname(os.path.abspath(__file__))

@@ -17,10 +17,16 @@ struct MatRef {
 MatRef mat_ref(const conv_matrix_desc *d, const void *p);
 
 inline int64_t channel_elem_size(int32_t dtype) {
-    return dtype == CONV_INT8 ? 1 : (dtype == CONV_FLOAT16 || dtype == CONV_BFLOAT16) ? 2 : 4;
+    return dtype == CONV_INT8 || dtype == CONV_FLOAT8_E4M3 || dtype == CONV_FLOAT8_E5M2 ? 1
+           : dtype == CONV_FLOAT16 || dtype == CONV_BFLOAT16                            ? 2
+                                                                                         : 4;
 }
 
 inline bool is_half_type(int32_t dtype) { return dtype == CONV_FLOAT16 || dtype == CONV_BFLOAT16; }
+inline bool is_float_type(int32_t dtype) { return dtype == CONV_FLOAT32 || is_half_type(dtype); }
+inline bool is_eight_bit_type(int32_t dtype) { return dtype == CONV_FLOAT8_E4M3 || dtype == CONV_FLOAT8_E5M2; }
+
+constexpr int64_t kScaleBlock = 128;  // elements that share a scale
 
 // Checks one matrix: extents 0..2^31-257, positive strides that alias no two
 // elements, extent inside capacity_bytes.  The type is the caller's concern.
@@ -97,5 +103,36 @@ ProductPlan product_plan(int64_t ma, int64_t nb, int64_t k);
 
 // workspace: part_bytes of the plan.
 conv_status product_launch(const Product &pr, void *workspace, void *stream);
+
+// ---------------------------------------------------------------- product of 8-bit operands
+// D[a,b] = epilogue(sum over blocks of 128 k of scale_a * scale_b * sum_k A[a,k] * B[b,k]).
+struct ScaledOperand {
+    const uint8_t *p = nullptr;  // k contiguous, rows 16-byte aligned
+    int64_t rs = 0;
+    const float *scale = nullptr;
+    int64_t s_rs = 0, s_cs = 0;
+    int32_t shift = 0;           // rows that share a scale: 1 << shift
+    int32_t e5m2 = 0;
+};
+
+struct ScaledProduct {
+    int64_t ma = 0, nb = 0, k = 0;
+    ScaledOperand a, b;
+    void *d = nullptr;
+    int64_t d_sa = 0, d_sb = 0;
+    int32_t d_dtype = 0;
+    const void *res = nullptr;   // of D's type
+    int64_t res_sa = 0, res_sb = 0;
+    void *pre = nullptr;
+    int64_t pre_sa = 0, pre_sb = 0;
+    int32_t pre_dtype = 0;
+    const void *bias = nullptr;  // along b
+    int32_t bias_dtype = 0;
+    int32_t act = CONV_ACT_NONE;
+};
+
+// A few rows of a (scaled_rows.cu).
+bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k);
+conv_status scaled_rows_launch(const ScaledProduct &pr, void *stream);
 
 }  // namespace i8c

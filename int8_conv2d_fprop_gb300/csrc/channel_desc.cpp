@@ -22,7 +22,7 @@ uint64_t matrix_extent_bytes(const conv_matrix_desc *d) {
 
 conv_status check_matrix(const conv_matrix_desc *d) {
     if (!d) return CONV_ERR_NULL_PTR;
-    if (d->dtype < CONV_INT8 || d->dtype > CONV_BFLOAT16) return CONV_ERR_DTYPE;
+    if (d->dtype < CONV_INT8 || d->dtype > CONV_FLOAT8_E5M2) return CONV_ERR_DTYPE;
     if (d->reserved != 0 || d->rows < 0 || d->cols < 0) return CONV_ERR_BAD_PARAM;
     // tile coordinates are 32-bit, a tile may reach 256 past the extent
     if (d->rows > INT32_MAX - 256 || d->cols > INT32_MAX - 256) return CONV_ERR_TOO_LARGE;

@@ -1,0 +1,346 @@
+// channel_rows.cuh -- rows of channels in registers: how a warp or a block
+// holds, loads, sums and stores them; shared by the norms.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <initializer_list>
+#include <type_traits>
+
+#include "channel.h"
+#include "channel_launch.cuh"
+#include "channel_math.cuh"
+#include "tc_ptx.cuh"
+
+namespace i8c {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums of two values over the block (at most 32 warps), the same in every
+// thread and in the same order in all of them, with one barrier: consecutive
+// sums use the two buffers in turn, and no warp can be two sums ahead.
+struct BlockSums {
+    float2 part[2][32];
+};
+
+struct Summer {
+    BlockSums *s;
+    int turn = 0;
+    __device__ __forceinline__ float2 operator()(float u, float v) {
+        u = warp_sum(u);
+        v = warp_sum(v);
+        float2 *p = s->part[turn];
+        turn ^= 1;
+        if (threadIdx.x % 32 == 0) p[threadIdx.x / 32] = make_float2(u, v);
+        __syncthreads();
+        const int warps = blockDim.x / 32;
+        float2 t = make_float2(0.0f, 0.0f);
+        const float4 *q = reinterpret_cast<const float4 *>(p);
+#pragma unroll 4
+        for (int i = 0; i < warps / 2; ++i) {
+            const float4 w = q[i];
+            t.x += w.x + w.z;
+            t.y += w.y + w.w;
+        }
+        if (warps & 1) t.x += p[warps - 1].x, t.y += p[warps - 1].y;
+        return t;
+    }
+    __device__ __forceinline__ float operator()(float u) { return (*this)(u, 0.0f).x; }
+};
+
+// ---------------------------------------------------------------- rows in registers
+// A row is held by a warp (kWarp: eight rows per block) or by the block, 8 kNv
+// elements per thread, so that it is read once and every sum runs over
+// registers.
+//
+// kVec: thread t holds the aligned groups of 8 elements t, t + T, ...: one
+// 16-byte vector of a 16-bit type, two of a 32-bit one.  A row that starts
+// `lead` elements past such a boundary starts with a partial group and ends
+// with one.  Blocks step over the rows in multiples of 8, so a block (or
+// warp) meets the same lead on all its rows whatever the row stride, and its
+// columns stay in the same registers: odd widths cost two partial groups per
+// row.  This wants one lead for all the matrices a call reads; an output with
+// another one is turned through shared memory, a row at a time.  The gradient of
+// matrices with several leads has thread t hold elements t, t + T, ..., one per
+// access.
+template <typename T>
+constexpr bool kIs16 = sizeof(T) == 2;
+
+template <typename T>
+struct Group {  // 8 elements as stored
+    uint32_t w[kIs16<T> ? 4 : 8];
+};
+
+template <typename T>
+__device__ __forceinline__ float element(const Group<T> &g, int j) {
+    if constexpr (std::is_same_v<T, float>) return __uint_as_float(g.w[j]);
+    else if constexpr (std::is_same_v<T, int32_t>) return (float)(int32_t)g.w[j];
+    else if constexpr (std::is_same_v<T, __half>)
+        return __half2float(__ushort_as_half((unsigned short)(g.w[j / 2] >> (j % 2 * 16))));
+    else return __uint_as_float(j % 2 ? g.w[j / 2] & 0xffff0000u : g.w[j / 2] << 16);
+}
+
+// Elements 2j and 2j + 1 as a pair of floats.
+template <typename T>
+__device__ __forceinline__ Pair element2(const Group<T> &g, int j) {
+    if constexpr (std::is_same_v<T, __half>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&g.w[j]));
+        return pair(f.x, f.y);
+    } else {
+        return pair(element(g, 2 * j), element(g, 2 * j + 1));
+    }
+}
+
+__device__ __forceinline__ uint32_t bits16(float v, const __half *) { return __half_as_ushort(__float2half_rn(v)); }
+__device__ __forceinline__ uint32_t bits16(float v, const __nv_bfloat16 *) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Where a thread's elements lie in its rows.
+template <bool kVec>
+struct Place {
+    int t, threads, cols, lead;
+    // column of element j of the thread's group i; outside the row if not below cols
+    __device__ __forceinline__ int column(int i, int j) const {
+        return kVec ? (i * threads + t) * 8 - lead + j : (i * 8 + j) * threads + t;
+    }
+    __device__ __forceinline__ bool inside(int c) const { return (uint32_t)c < (uint32_t)cols; }
+    __device__ __forceinline__ bool whole(int i) const {
+        return kVec ? inside(column(i, 0)) && inside(column(i, 7)) : inside(column(i, 7));
+    }
+};
+
+// Elements past the boundary of 8 at which p lies.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T *p) {
+    return (int)((uintptr_t)p / sizeof(T)) & 7;
+}
+
+// Group i of the row that starts at p; zeros outside the row.
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_group(const T *p, const Place<kVec> &at, int i, Group<T> &g) {
+    if (kVec && at.whole(i)) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p + at.column(i, 0));
+        const uint4 a = q[0];
+        g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
+        if constexpr (!kIs16<T>) {
+            const uint4 b = q[1];
+            g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if constexpr (kIs16<T>) {
+            const uint32_t v = at.inside(c) ? reinterpret_cast<const uint16_t *>(p)[c] : 0u;
+            if (j % 2) g.w[j / 2] |= v << 16;
+            else g.w[j / 2] = v;
+        } else {
+            g.w[j] = at.inside(c) ? reinterpret_cast<const uint32_t *>(p)[c] : 0u;
+        }
+    }
+}
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, const float (&v)[8]) {
+    if (kVec && at.whole(i)) {
+        const int c = at.column(i, 0);
+        if constexpr (kIs16<T>) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], std::is_same_v<T, __half> ? CONV_FLOAT16 : CONV_BFLOAT16);
+            *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            *reinterpret_cast<float4 *>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if (!at.inside(c)) continue;
+        if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)bits16(v[j], p);
+        else p[c] = v[j];
+    }
+}
+
+// The same for an output whose lead differs from the rows read: its groups
+// are put together in shared memory, element c of the row at c + lead.
+template <typename T>
+struct Turn {
+    T *buf;     // shared memory of the row's warp or block: cols + 16 elements
+    int lead;   // of the output's rows
+};
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void turn_group(const Turn<T> &u, const Place<kVec> &at, int i, const float (&v)[8]) {
+    if (at.whole(i)) {
+        T *to = u.buf + at.column(i, 0) + u.lead;
+        if constexpr (kIs16<T>) {
+            if (((u.lead ^ at.lead) & 1) == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+                    reinterpret_cast<uint32_t *>(to)[j / 2] =
+                        pack2(v[j], v[j + 1], std::is_same_v<T, __half> ? CONV_FLOAT16 : CONV_BFLOAT16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)bits16(v[j], u.buf);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) to[j] = v[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        if (!at.inside(c)) continue;
+        if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(u.buf)[c + u.lead] = (uint16_t)bits16(v[j], u.buf);
+        else u.buf[c + u.lead] = v[j];
+    }
+}
+
+template <bool kVec, typename T>
+__device__ __forceinline__ void store_turned(T *p, const Turn<T> &u, const Place<kVec> &at) {
+    for (int g = at.t; g * 8 < at.cols + u.lead; g += at.threads) {
+        const int c = g * 8 - u.lead;
+        if (c >= 0 && c + 8 <= at.cols) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(u.buf + g * 8);
+            uint4 *o = reinterpret_cast<uint4 *>(p + c);
+            o[0] = q[0];
+            if constexpr (!kIs16<T>) o[1] = q[1];
+        } else {
+            for (int j = max(0, -c); j < 8 && c + j < at.cols; ++j) p[c + j] = u.buf[g * 8 + j];
+        }
+    }
+}
+
+template <bool kWarp>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (kWarp) __syncwarp();
+    else __syncthreads();
+}
+
+// 8 values of a parameter vector (any alignment; absent or outside: `fill`).
+template <bool kVec>
+__device__ __forceinline__ void load_params(const void *p, int32_t dtype, float fill, const Place<kVec> &at, int i,
+                                            float (&v)[8]) {
+    if (kVec && p && at.whole(i)) {
+        const int c = at.column(i, 0);
+        const char *q = (const char *)p + (int64_t)c * (dtype == CONV_FLOAT32 ? 4 : 2);
+        if ((uintptr_t)q % 16 == 0) {
+            if (dtype == CONV_FLOAT32) {
+                const float4 a = reinterpret_cast<const float4 *>(q)[0], b = reinterpret_cast<const float4 *>(q)[1];
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+                unpack8(*reinterpret_cast<const uint4 *>(q), dtype, v);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int c = at.column(i, j);
+        v[j] = p && at.inside(c) ? load_as_float(p, c, dtype) : fill;
+    }
+}
+
+// Elements of a row being turned, a multiple of 16.
+__host__ __device__ constexpr int turn_elems(int cols) { return (cols + 31) / 16 * 16; }
+
+// Rows on their way: a thread's groups of the next kDepth rows come in by
+// asynchronous copies into slots that only this thread reads, so that the
+// loads in flight cost no registers and no barriers.
+template <typename X>
+constexpr int kDepth = kIs16<X> ? 3 : 2;
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <typename X>
+struct Slots {
+    uint32_t base;    // this thread's first 16 bytes
+    uint32_t stride;  // 16 bytes of every thread of the block
+    __device__ __forceinline__ uint32_t at(int stage, int matrix, int matrices, int i, int nv) const {
+        return base + ((stage * matrices + matrix) * nv + i) * (kIs16<X> ? 1 : 2) * stride;
+    }
+};
+
+template <typename X>
+__device__ __forceinline__ void fetch_group(const X *p, const Place<true> &at, int i, uint32_t slot, uint32_t stride) {
+    if (at.whole(i)) {
+        copy_async16(slot, p + at.column(i, 0));
+        if constexpr (!kIs16<X>) copy_async16(slot + stride, p + at.column(i, 4));
+        return;
+    }
+    Group<X> g;
+    load_group(p, at, i, g);
+    ptx::st_shared_v4(slot, make_uint4(g.w[0], g.w[1], g.w[2], g.w[3]));
+    if constexpr (!kIs16<X>) ptx::st_shared_v4(slot + stride, make_uint4(g.w[4], g.w[5], g.w[6], g.w[7]));
+}
+
+template <typename X>
+__device__ __forceinline__ void read_group(uint32_t slot, uint32_t stride, Group<X> &g) {
+    const uint4 a = ptx::ld_shared_v4(slot);
+    g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
+    if constexpr (!kIs16<X>) {
+        const uint4 b = ptx::ld_shared_v4(slot + stride);
+        g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
+    }
+}
+
+// ---------------------------------------------------------------- host
+inline bool unit_columns(const MatRef &m) { return !m.p || m.cs <= 1; }
+
+// Lead of a matrix's rows: 8 values for the rows modulo 8, as base and step.
+struct Lead {
+    int64_t base, step;
+};
+inline Lead lead_of_rows(const MatRef &m) {
+    const int64_t size = channel_elem_size(m.dtype);
+    return {(int64_t)((uintptr_t)m.p / (uintptr_t)size & 7), m.rs & 7};
+}
+
+// Whether the rows of all matrices (those given) have one lead.
+inline bool one_lead(std::initializer_list<const MatRef *> all) {
+    const Lead l = lead_of_rows(**all.begin());
+    for (const MatRef *m : all) {
+        if (!m->p) continue;
+        const Lead k = lead_of_rows(*m);
+        if (k.base != l.base || k.step != l.step) return false;
+    }
+    return true;
+}
+
+// A launch with more than 48 KB of shared memory.
+template <auto kKernel, typename Args>
+inline bool launch_large(dim3 grid, int threads, size_t smem, cudaStream_t s, const Args &a) {
+    static std::atomic<bool> ready[64];  // (check_device admits 64 devices)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!ready[dev].load()) {
+        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10) != cudaSuccess) return false;
+        ready[dev].store(true);
+    }
+    return launch_behind(kKernel, grid, threads, smem, s, a);
+}
+
+// A vector the call reads or writes: aligned to its element, and apart from
+// the matrix `m`.
+inline conv_status check_vector(const void *p, int64_t n, int64_t size, const conv_matrix_desc *m, const void *m_dev) {
+    if (!p || n == 0) return CONV_OK;
+    if ((uintptr_t)p % (uintptr_t)size) return CONV_ERR_ALIGNMENT;
+    if (m && overlaps(p, (uint64_t)(n * size), m_dev, matrix_extent_bytes(m))) return CONV_ERR_OVERLAP;
+    return CONV_OK;
+}
+
+}  // namespace i8c

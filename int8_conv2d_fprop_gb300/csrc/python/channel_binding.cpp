@@ -11,13 +11,16 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_strided.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
+#include <vector>
 
 #include "int8conv.h"
 
@@ -30,6 +33,8 @@ int32_t type_code(at::ScalarType t) {
         case at::kFloat: return CONV_FLOAT32;
         case at::kHalf: return CONV_FLOAT16;
         case at::kBFloat16: return CONV_BFLOAT16;
+        case at::kFloat8_e4m3fn: return CONV_FLOAT8_E4M3;
+        case at::kFloat8_e5m2: return CONV_FLOAT8_E5M2;
         default: return 0;  // refused by the library
     }
 }
@@ -157,6 +162,26 @@ bool activation_code(PyObject *o, int32_t *code) {
     return true;
 }
 
+// The tensor type of a code that an entry point allocates an output in.
+bool scalar_type(PyObject *o, at::ScalarType *type) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) return false;
+    switch (v) {
+        case CONV_FLOAT32: *type = at::kFloat; return true;
+        case CONV_FLOAT16: *type = at::kHalf; return true;
+        case CONV_BFLOAT16: *type = at::kBFloat16; return true;
+        case CONV_FLOAT8_E4M3: *type = at::kFloat8_e4m3fn; return true;
+        case CONV_FLOAT8_E5M2: *type = at::kFloat8_e5m2; return true;
+        default: PyErr_SetString(PyExc_ValueError, "dtype is not one this call makes"); return false;
+    }
+}
+
+// A Python number as a 32-bit float.
+bool number(PyObject *o, float *v) {
+    *v = (float)PyFloat_AsDouble(o);
+    return !PyErr_Occurred();
+}
+
 // One type for the parameter vectors that are there (which hold floats).
 bool one_type(std::initializer_list<const Vector *> all, int32_t *type) {
     *type = 0;
@@ -193,7 +218,46 @@ struct Call {
     at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const {
         return at::empty(sizes, at::TensorOptions().dtype(type).device(where));
     }
+    // A matrix [..., cols] of like's leading dims (or of `rows` alone), rows and columns these strides apart.
+    at::Tensor matrix(const at::Tensor *like, int64_t rows, int64_t cols, int64_t row_stride, int64_t col_stride,
+                      at::ScalarType type) const {
+        at::DimVector sizes, strides;
+        if (like) {
+            sizes.assign(like->sizes().begin(), like->sizes().end());
+            strides.resize(sizes.size());
+            int64_t step = row_stride;
+            for (int64_t i = (int64_t)sizes.size() - 2; i >= 0; --i) {
+                strides[i] = step;
+                step *= sizes[i];
+            }
+            sizes.back() = cols;
+            strides.back() = col_stride;
+        } else {
+            sizes = {rows, cols};
+            strides = {row_stride, col_stride};
+        }
+        return at::empty_strided(sizes, strides, at::TensorOptions().dtype(type).device(where));
+    }
 };
+
+int64_t blocks_of(int64_t n, int64_t of) { return (n + of - 1) / of; }
+
+// The scales of [rows, cols] in blocks of `tile` rows: neighbouring rows' next to one another.
+at::Tensor scales_for(const Call &c, const at::Tensor *like, int64_t rows, int64_t cols, int64_t tile) {
+    const int64_t lines = blocks_of(rows, tile);
+    return c.matrix(tile == 1 ? like : nullptr, lines, blocks_of(cols, 128), 1, std::max<int64_t>(lines, 1), at::kFloat);
+}
+// 8-bit values in rows of a multiple of 16 bytes, as the products read them in place.
+at::Tensor eight_bit_for(const Call &c, const at::Tensor *like, int64_t rows, int64_t cols, at::ScalarType type) {
+    return c.matrix(like, rows, cols, std::max<int64_t>(blocks_of(cols, 16), 1) * 16, 1, type);
+}
+
+// A result that was allocated here, or the caller's own (borrowed from its argument).
+PyObject *result(at::Tensor &made, PyObject *given) {
+    if (made.defined()) return THPVariable_Wrap(std::move(made));
+    Py_INCREF(given);
+    return given;
+}
 
 // The caller's workspace where it is large enough, else one of the call's.
 struct Workspace {
@@ -370,7 +434,281 @@ PyObject *layer_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// quantize(x, preact, activation, tile, dtype, rows, columns, out, scale, out_t, scale_t, stream)
+//     -> (out, scale) of rows, of columns, or of both
+PyObject *quantize(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 12)) return nullptr;
+    Common all;
+    Matrix x, z, m[4];  // q, scale, qt, scale_t
+    static const char *const names[] = {"out", "scale", "out_t", "scale_t"};
+    if (!x.read(all, arg[0], "x", true) || !z.read(all, arg[1], "preact", false)) return nullptr;
+    for (int i = 0; i < 4; ++i)
+        if (!m[i].read(all, arg[7 + i], names[i], false)) return nullptr;
+    conv_quantize_params p{};
+    if (!activation_code(arg[2], &p.activation)) return nullptr;
+    if (p.activation < 0) return status(CONV_ERR_BAD_PARAM);
+    const long tile = PyLong_AsLong(arg[3]);
+    if (tile == -1 && PyErr_Occurred()) return nullptr;
+    if (tile != 1 && tile != 128) return status(CONV_ERR_BAD_PARAM);
+    p.tile = (int32_t)tile;
+    at::ScalarType type;
+    if (!scalar_type(arg[4], &type)) return nullptr;
+    const bool want[2] = {PyObject_IsTrue(arg[5]) == 1, PyObject_IsTrue(arg[6]) == 1};
+    const int64_t rows = x.d.rows, cols = x.d.cols;
+    const Call c(*x.t, arg[11]);
+    at::Tensor made[4];
+    for (int f = 0; f < 2; ++f) {
+        if (!want[f]) {
+            if (m[2 * f].t || m[2 * f + 1].t) {
+                PyErr_Format(PyExc_ValueError, "%s is given, but not wanted", names[m[2 * f].t ? 2 * f : 2 * f + 1]);
+                return nullptr;
+            }
+            continue;
+        }
+        const int64_t a = f ? cols : rows, b = f ? rows : cols;
+        const at::Tensor *like = f ? nullptr : x.t;
+        if (!m[2 * f].t) {
+            made[2 * f] = eight_bit_for(c, like, a, b, type);
+            if (!m[2 * f].read(made[2 * f], names[2 * f])) return nullptr;
+        }
+        if (!m[2 * f + 1].t) {
+            made[2 * f + 1] = scales_for(c, like, a, b, tile);
+            if (!m[2 * f + 1].read(made[2 * f + 1], names[2 * f + 1])) return nullptr;
+        }
+    }
+    const conv_status st = conv_quantize(&x.d, x.p, z.desc(), z.p, m[0].desc(), m[0].p, m[1].desc(), m[1].p, m[2].desc(),
+                                         m[2].p, m[3].desc(), m[3].p, &p, c.stream);
+    if (st) return status(st);
+    PyObject *r = PyTuple_New(2 * (want[0] + want[1]));
+    if (!r) return nullptr;
+    for (int i = 0, k = 0; i < 4; ++i) {
+        if (!want[i / 2]) continue;
+        if (!made[i].defined()) changed({m[i].t});
+        PyTuple_SET_ITEM(r, k++, result(made[i], arg[7 + i]));
+    }
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// linear_fp8(x, x_scale, w, w_scale, bias, activation, residual, preact, out, dtype, workspace, stream) -> out
+PyObject *linear_fp8(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 12)) return nullptr;
+    Common all;
+    Matrix x, xs, w, ws, r, z, y;
+    Vector b;
+    if (!x.read(all, arg[0], "x", true) || !xs.read(all, arg[1], "x_scale", true) || !w.read(all, arg[2], "w", true) ||
+        !ws.read(all, arg[3], "w_scale", true) || !b.read(all, arg[4], "bias", w.d.rows) ||
+        !r.read(all, arg[6], "residual", false) || !z.read(all, arg[7], "preact", false) ||
+        !y.read(all, arg[8], "out", false) || !Workspace::admit(all, arg[10]))
+        return nullptr;
+    conv_linear_params p{};
+    if (!activation_code(arg[5], &p.activation)) return nullptr;
+    if (p.activation < 0) return status(CONV_ERR_BAD_PARAM);
+    p.bias_dtype = b.type;
+    at::ScalarType type;
+    if (!scalar_type(arg[9], &type)) return nullptr;
+    const Call c(*x.t, arg[11]);
+    at::Tensor made;
+    if (!y.t) {
+        at::DimVector sizes(x.t->sizes().begin(), x.t->sizes().end());
+        sizes.back() = w.d.rows;
+        made = c.empty(sizes, type);
+        if (!y.read(made, "out")) return nullptr;
+    }
+    size_t need = 0;
+    conv_status st = conv_linear_fp8_workspace_size(&x.d, x.p, &w.d, w.p, &need);
+    if (st) return status(st);
+    Workspace work;
+    if (!work.take(all, c, arg[10], need)) return nullptr;
+    st = conv_linear_fp8(&x.d, x.p, &xs.d, xs.p, &w.d, w.p, &ws.d, ws.p, b.p, r.desc(), r.p, z.desc(), z.p, &y.d, y.p, &p,
+                         work.p, work.bytes, c.stream);
+    if (st) return status(st);
+    if (made.defined()) y.t = nullptr;
+    changed({z.t, y.t});
+    return result(made, arg[8]);
+    END_HANDLE_TH_ERRORS
+}
+
+// block_norm(x, skip, post_norm, post_gain, gate, skip_scale, branch_scale, gain, norm, eps, sum, out, out_scale, dtype,
+//            post_rstd, rstd, stream) -> (sum or None, out or None[, out_scale])
+PyObject *block_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 17)) return nullptr;
+    Common all;
+    Matrix x, skip, gate, sum, y, ys;
+    Vector pg, g, prstd, rstd;
+    if (!x.read(all, arg[0], "x", true) || !skip.read(all, arg[1], "skip", false) ||
+        !pg.read(all, arg[3], "post_gain", x.d.cols) || !gate.read(all, arg[4], "gate", false) ||
+        !g.read(all, arg[7], "gain", x.d.cols) || !sum.read(all, arg[10], "sum", false) ||
+        !y.read(all, arg[11], "out", false) || !ys.read(all, arg[12], "out_scale", false) ||
+        !prstd.read_float(all, arg[14], "post_rstd", x.d.rows) || !rstd.read_float(all, arg[15], "rstd", x.d.rows))
+        return nullptr;
+    conv_block_norm_params p{};
+    p.post_norm = PyObject_IsTrue(arg[2]) == 1;
+    const bool norm = PyObject_IsTrue(arg[8]) == 1;
+    if (!number(arg[5], &p.skip_scale) || !number(arg[6], &p.branch_scale) || !number(arg[9], &p.eps)) return nullptr;
+    if (!float_types({&pg, &g})) return status(CONV_ERR_DTYPE);
+    if (!one_type({&pg, &g}, &p.param_dtype)) return nullptr;
+    at::ScalarType type = x.t->scalar_type();
+    if (arg[13] != Py_None && !scalar_type(arg[13], &type)) return nullptr;
+    if (!norm && (y.t || ys.t || rstd.t)) {
+        PyErr_SetString(PyExc_ValueError, "out, out_scale and rstd belong to the norm, which is not wanted");
+        return nullptr;
+    }
+    if (!p.post_norm && (pg.t || prstd.t)) {
+        PyErr_SetString(PyExc_ValueError, "post_gain and post_rstd belong to the post norm, which is not wanted");
+        return nullptr;
+    }
+    const Call c(*x.t, arg[16]);
+    at::Tensor made_sum, made, made_scale;
+    if (!sum.t && (skip.t || gate.t || p.post_norm || !norm)) {
+        made_sum = c.empty(x.t->sizes(), skip.t ? skip.t->scalar_type() : x.t->scalar_type());
+        if (!sum.read(made_sum, "sum")) return nullptr;
+    }
+    bool eight = false;
+    if (norm) {
+        if (!y.t) {
+            made = type == at::kFloat8_e4m3fn ? eight_bit_for(c, x.t, x.d.rows, x.d.cols, type) : c.empty(x.t->sizes(), type);
+            if (!y.read(made, "out")) return nullptr;
+        }
+        eight = y.d.dtype == CONV_FLOAT8_E4M3;
+        if (!eight && ys.t) {
+            PyErr_SetString(PyExc_ValueError, "out_scale belongs to an 8-bit out");
+            return nullptr;
+        }
+        if (eight && !ys.t) {
+            made_scale = scales_for(c, x.t, x.d.rows, x.d.cols, 1);
+            if (!ys.read(made_scale, "out_scale")) return nullptr;
+        }
+    }
+    const conv_status st = conv_block_norm(&x.d, x.p, skip.desc(), skip.p, gate.desc(), gate.p, pg.p, g.p, sum.desc(), sum.p,
+                                           y.desc(), y.p, ys.desc(), ys.p, (float *)prstd.p, (float *)rstd.p, &p, c.stream);
+    if (st) return status(st);
+    if (!made_sum.defined()) changed({sum.t});
+    if (!made.defined()) changed({y.t});
+    if (!made_scale.defined()) changed({ys.t});
+    changed({prstd.t, rstd.t});
+    PyObject *r = PyTuple_New(eight ? 3 : 2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, result(made_sum, arg[10]));
+    PyTuple_SET_ITEM(r, 1, result(made, arg[11]));
+    if (eight) PyTuple_SET_ITEM(r, 2, result(made_scale, arg[12]));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// block_norm_grad(dy, dsum, x, sum, post_norm, post_gain, gate, skip_scale, branch_scale, gain, post_rstd, rstd,
+//                 dx, dskip, dgate, dgain, dpost_gain, workspace, stream) -> None
+PyObject *block_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 19)) return nullptr;
+    Common all;
+    Matrix dy, ds, x, h, gate, dx, dskip, dgate;
+    Vector pg, g, prstd, rstd, dg, dpg;
+    if (!dy.read(all, arg[0], "dy", false) || !ds.read(all, arg[1], "dsum", false)) return nullptr;
+    if (!dy.t && !ds.t) {
+        PyErr_SetString(PyExc_ValueError, "dy or dsum is required");
+        return nullptr;
+    }
+    const Matrix &like = dy.t ? dy : ds;
+    const int64_t rows = like.d.rows, cols = like.d.cols;
+    if (!x.read(all, arg[2], "x", false) || !h.read(all, arg[3], "sum", false) || !pg.read(all, arg[5], "post_gain", cols) ||
+        !gate.read(all, arg[6], "gate", false) || !g.read(all, arg[9], "gain", cols) ||
+        !prstd.read_float(all, arg[10], "post_rstd", rows) || !rstd.read_float(all, arg[11], "rstd", rows) ||
+        !dx.read(all, arg[12], "dx", false) || !dskip.read(all, arg[13], "dskip", false) ||
+        !dgate.read(all, arg[14], "dgate", false) || !dg.read(all, arg[15], "dgain", cols) ||
+        !dpg.read(all, arg[16], "dpost_gain", cols) || !Workspace::admit(all, arg[17]))
+        return nullptr;
+    conv_block_norm_params p{};
+    p.eps = 1e-6f;  // (in the statistics already)
+    p.post_norm = PyObject_IsTrue(arg[4]) == 1;
+    if (!number(arg[7], &p.skip_scale) || !number(arg[8], &p.branch_scale)) return nullptr;
+    if (!float_types({&pg, &g, &dg, &dpg})) return status(CONV_ERR_DTYPE);
+    if (!one_type({&pg, &g, &dg, &dpg}, &p.param_dtype)) return nullptr;
+    const Call c(*like.t, arg[18]);
+    const int64_t groups = gate.t ? gate.d.rows : dgate.t ? dgate.d.rows : rows > 0 ? 1 : 0;
+    size_t need = 0;
+    conv_status st = conv_block_norm_grad_workspace_size(&like.d, groups, &need);
+    if (st) return status(st);
+    Workspace ws;
+    if (!ws.take(all, c, arg[17], need)) return nullptr;
+    st = conv_block_norm_grad(dy.desc(), dy.p, ds.desc(), ds.p, x.desc(), x.p, h.desc(), h.p, gate.desc(), gate.p, pg.p, g.p,
+                              (const float *)prstd.p, (const float *)rstd.p, dx.desc(), dx.p, dskip.desc(), dskip.p,
+                              dgate.desc(), dgate.p, dpg.p, dg.p, &p, ws.p, ws.bytes, c.stream);
+    if (st) return status(st);
+    changed({dx.t, dskip.t, dgate.t, dg.t, dpg.t});
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// clip_grads(grads, max_norm, eps, out, norm, workspace, stream) -> norm
+PyObject *clip_grads(PyObject *, PyObject *const *arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 7)) return nullptr;
+    Common all;
+    struct Items {
+        PyObject *o = nullptr;
+        ~Items() { Py_XDECREF(o); }
+    } grads, outs;
+    grads.o = PySequence_Fast(arg[0], "grads must be a sequence of tensors");
+    if (!grads.o) return nullptr;
+    if (arg[3] != Py_None && !(outs.o = PySequence_Fast(arg[3], "out must be a sequence of tensors"))) return nullptr;
+    const Py_ssize_t k = PySequence_Fast_GET_SIZE(grads.o);
+    if (outs.o && PySequence_Fast_GET_SIZE(outs.o) != k) {
+        PyErr_SetString(PyExc_ValueError, "out must have a tensor for every one of grads");
+        return nullptr;
+    }
+    std::vector<conv_grad_tensor> table((size_t)k);
+    std::vector<const at::Tensor *> written((size_t)k);
+    for (Py_ssize_t i = 0; i < k; ++i) {
+        bool ok;
+        const at::Tensor *g = tensor(all, PySequence_Fast_GET_ITEM(grads.o, i), "a gradient", &ok);
+        if (!ok) return nullptr;
+        const at::Tensor *o = g;
+        if (!g) return fail("a gradient", "is None; leave it out"), nullptr;
+        if (!g->is_non_overlapping_and_dense()) return fail("a gradient", "has gaps between its elements; make it contiguous"), nullptr;
+        if (outs.o) {
+            o = tensor(all, PySequence_Fast_GET_ITEM(outs.o, i), "an out", &ok);
+            if (!ok) return nullptr;
+            if (!o) return fail("an out", "is None"), nullptr;
+            if (o->scalar_type() != g->scalar_type() || o->sizes() != g->sizes() || o->strides() != g->strides())
+                return fail("an out", "must have its gradient's type, shape and strides"), nullptr;
+        }
+        table[i] = {g->numel() ? g->data_ptr() : nullptr, o->numel() ? o->data_ptr() : nullptr, g->numel(), type_code(g->scalar_type()), 0};
+        written[i] = o;
+    }
+    float max_norm, eps;
+    if (!number(arg[1], &max_norm) || !number(arg[2], &eps)) return nullptr;
+    bool ok;
+    const at::Tensor *norm = tensor(all, arg[4], "norm", &ok);
+    if (!ok || !Workspace::admit(all, arg[5])) return nullptr;
+    if (norm && (norm->numel() != 1 || norm->scalar_type() != at::kFloat)) return fail("norm", "must be one float32"), nullptr;
+    if (!all.first) return fail("grads", "has no tensors; without them norm is required"), nullptr;
+    const Call c(*all.first, arg[6]);
+    at::Tensor made;
+    if (!norm) made = c.empty({}, at::kFloat);
+    size_t need = 0;
+    conv_status st = conv_clip_grads_workspace_size(table.data(), k, &need);
+    if (st) return status(st);
+    Workspace ws;
+    if (!ws.take(all, c, arg[5], need)) return nullptr;
+    st = conv_clip_grads(table.data(), k, max_norm, eps, (float *)(norm ? norm->data_ptr() : made.data_ptr()), ws.p, ws.bytes, c.stream);
+    if (st) return status(st);
+    if (!std::isinf(max_norm))
+        for (const at::Tensor *t : written) changed({t});
+    changed({norm});
+    return result(made, arg[4]);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
+    {"quantize", (PyCFunction)(void (*)())quantize, METH_FASTCALL, nullptr},
+    {"linear_fp8", (PyCFunction)(void (*)())linear_fp8, METH_FASTCALL, nullptr},
+    {"block_norm", (PyCFunction)(void (*)())block_norm, METH_FASTCALL, nullptr},
+    {"block_norm_grad", (PyCFunction)(void (*)())block_norm_grad, METH_FASTCALL, nullptr},
+    {"clip_grads", (PyCFunction)(void (*)())clip_grads, METH_FASTCALL, nullptr},
     {"linear", (PyCFunction)(void (*)())linear, METH_FASTCALL, nullptr},
     {"linear_grad", (PyCFunction)(void (*)())linear_grad, METH_FASTCALL, nullptr},
     {"layer_norm", (PyCFunction)(void (*)())layer_norm, METH_FASTCALL, nullptr},
