@@ -131,6 +131,20 @@ struct ScaledProduct {
     int32_t act = CONV_ACT_NONE;
 };
 
+// Tile shape and runs of the tensor-core product (scaled_product.cu);
+// part_bytes of workspace hold its partial sums.
+struct ScaledPlan {
+    bool swap = false;     // a and b exchanged
+    bool pair = false;     // tiles of CTA pairs (256 rows), else of one CTA (128)
+    int32_t tile_b = 0;
+    int64_t tiles_a = 0, tiles_b = 0;
+    int32_t parts = 1;     // runs of k, summed apart and joined by a second kernel, ...
+    int64_t full = 0;      // ... of the tiles from this one on
+    size_t part_bytes = 0;
+};
+ScaledPlan scaled_plan(int64_t ma, int64_t nb, int64_t k);
+conv_status scaled_launch(const ScaledProduct &pr, void *workspace, void *stream);
+
 // A few rows of a (scaled_rows.cu).
 bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k);
 conv_status scaled_rows_launch(const ScaledProduct &pr, void *stream);

@@ -59,6 +59,7 @@ Plan plan_of(const conv_matrix_desc *x, const void *x_dev, const conv_matrix_des
     if (pl.pack_x) pl.x_off = pl.bytes, pl.bytes += (size_t)round_up(x->rows * round_up(x->cols, 16), 256);
     if (pl.pack_w) pl.w_off = pl.bytes, pl.bytes += (size_t)round_up(w->rows * round_up(w->cols, 16), 256);
     pl.part_off = pl.bytes;
+    if (!scaled_rows_applies(x->rows, w->rows, x->cols)) pl.bytes += scaled_plan(x->rows, w->rows, x->cols).part_bytes;
     return pl;
 }
 
@@ -181,7 +182,8 @@ conv_status conv_linear_fp8(const conv_matrix_desc *x, const void *x_dev, const 
     pr.pre = preact ? preact_dev : nullptr, pr.pre_sa = zr.rs, pr.pre_sb = zr.cs, pr.pre_dtype = zr.dtype;
     pr.bias = bias_dev, pr.bias_dtype = p->bias_dtype;
     pr.act = p->activation;
-    return scaled_rows_launch(pr, stream);
+    if (scaled_rows_applies(m, n, pr.k)) return scaled_rows_launch(pr, stream);
+    return scaled_launch(pr, (char *)workspace + pl.part_off, stream);
 }
 
 }  // extern "C"

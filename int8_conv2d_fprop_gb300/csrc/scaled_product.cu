@@ -1,0 +1,522 @@
+// scaled_product.cu -- D[a,b] = epilogue(sum over blocks of 128 k of
+// scale_a * scale_b * sum_k A[a,k] * B[b,k]) for 8-bit float operands, on the
+// 5th-generation tensor cores.
+//
+// The tensor cores sum one block of 128 k at a time (four MMAs of 32 k) into
+// one of two accumulators in tensor memory; eight warps take the other one,
+// multiply it by the block's scales and add it to 32-bit sums that they keep
+// in registers over all of k.  So every block costs a pass over the
+// accumulator: 128 x 256 values per CTA and block, read from tensor memory and
+// multiplied in packed pairs, against the 512 cycles that the MMAs take.  Two
+// accumulators let the MMAs run a block ahead, and through the epilogue, two.
+// Warps: 0 and 3 load the operands by TMA (128 bytes of k are one swizzled
+// row), 1 issues the MMAs, 2 copies the scales, 4 to 11 sum and finish.  The
+// control warps give registers to the summing ones, whose 128 columns of sums
+// do not fit otherwise.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "channel.h"
+#include "channel_launch.cuh"
+#include "channel_math.cuh"
+#include "product_tiles.cuh"
+#include "tc_ptx.cuh"
+
+namespace i8c {
+namespace {
+
+constexpr int kBlockK = 128;       // k elements of a block, bytes of a swizzled row
+constexpr int kMaxTileB = 256;
+constexpr int kMaxStages = 8;
+constexpr int kSumWarps = 8;       // two to a quarter of the lanes, each half the columns
+constexpr int kThreads = 128 + 32 * kSumWarps;
+constexpr int kScaleSlots = 8;     // blocks whose scales are on their way
+constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;
+constexpr int kBiasBytes = kSumWarps * 128;
+constexpr int kRingBytes = 196608;
+// registers: 384 threads start with 168 each; the summing warps' 128 sums, 64
+// values on their way and the rest of their state take up to 224
+constexpr int kControlRegs = 48, kSumRegs = 224, kLaunchRegs = 168;
+static_assert(128 * kControlRegs + 32 * kSumWarps * kSumRegs <= kThreads * kLaunchRegs);
+
+struct ScaleArgs {
+    const float *p;
+    int64_t rs, cs;
+    int32_t shift;               // rows that share a scale: 1 << shift
+    int32_t rows;                // of the operand
+};
+
+struct ScaledArgs : TileArgs {
+    CUtensorMap map_a, map_b;
+    ScaleArgs sa, sb;
+    int32_t blocks;              // of k
+    int32_t b_rows;              // rows of B per CTA
+    int32_t stages, stage_bytes; // A is the first 16 KB of a stage
+    uint32_t idesc;
+    uint64_t wait_limit_ns;
+    int *status;
+};
+
+struct SharedCtl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+
+template <bool kPair>
+__device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kPair) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    }
+}
+
+// Four bytes to shared memory, zeros where there is nothing to read.
+__device__ __forceinline__ void copy_async4(uint32_t dst, const float *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// Arrives (once, of the expected count) when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// wait_phase without a call: the summing warps have no registers to put away.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag, uint64_t limit_ns,
+                                            int *status) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (ptx::global_timer_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicExch(status, (int)CONV_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// kPair: two CTAs of a cluster work on one tile of 256 x 2 kCols
+// (cta_group::2: each holds its 128 rows of A and half the rows of B, the
+// first one issues the MMAs for both), else one CTA on 128 x 2 kCols.
+// kPerColumn: B has a scale for each row, else one for the 128 that a summing
+// warp's columns lie in.
+template <bool kPair, int kCols, bool kPerColumn>
+__global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __grid_constant__ ScaledArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int kTileB = 2 * kCols;
+    const uint32_t ring = ptx::smem_addr(smem);
+    const uint32_t staging = ring + a.stages * a.stage_bytes;
+    const uint32_t scales = staging + kSumWarps * kSlotBytes;
+    const uint32_t bias_smem = scales + kScaleSlots * kScaleBytes;
+    SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + (bias_smem - ring) + kBiasBytes);
+    if (ring & 1023) {  // the swizzles count on it (true of every launch without static shared memory)
+        if (threadIdx.x == 0) atomicExch(a.status, (int)CONV_ERR_ALIGNMENT);
+        return;
+    }
+    volatile int32_t *abort_flag = &ctl->abort_flag;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = kPair ? cluster_rank() : 0;
+    constexpr int kCluster = kPair ? 2 : 1, kRowsA = kPair ? 256 : 128;
+    const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
+    const int tiles = a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
+
+    // unit u: a whole tile, then the runs of the cut tiles; sets the blocks of k, returns the tile
+    int k_lo = 0, k_hi = a.blocks;
+    auto run_of = [&](int u) {
+        if (a.parts > 1) {
+            k_lo = 0, k_hi = a.blocks;
+            if (u >= a.full) {
+                const int cut = tiles - a.full, p = (u - a.full) / cut;
+                k_lo = (int)((int64_t)a.blocks * p / a.parts);
+                k_hi = (int)((int64_t)a.blocks * (p + 1) / a.parts);
+                u -= p * cut;
+            }
+        }
+        return u;
+    };
+
+    if (threadIdx.x == 0) {
+        ptx::prefetch_tensormap(&a.map_a);
+        for (int i = 0; i < a.stages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
+            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->acc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->acc_empty[i]), kCluster * kSumWarps);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&ctl->scale_full[i]), 32);
+            ptx::mbar_init(ptx::smem_addr(&ctl->scale_empty[i]), kSumWarps);
+        }
+        ctl->abort_flag = 0;
+        ptx::fence_mbar_init();
+    } else if (threadIdx.x == 96) {
+        ptx::prefetch_tensormap(&a.map_b);
+    }
+    __syncthreads();
+    if (warp == 2) tmem_alloc<kPair>(ptx::smem_addr(&ctl->tmem_base), 512);
+    ptx::tc_fence_before();
+    if (kPair) cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)&ctl->tmem_base;
+    // Nothing above reads or writes global memory.
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+
+    if (warp < 4) {
+        ptx::setmaxnreg_dec<kControlRegs>();
+        if ((warp == 0 || warp == 3) && lane == 0) {
+            // ------------------------------------------------ loads: operand A by warp 0, operand B by warp 3
+            const bool is_b = warp == 3;
+            const CUtensorMap *map = is_b ? &a.map_b : &a.map_a;
+            const uint32_t bytes = (uint32_t)kCluster * (is_b ? a.b_rows : kTileA) * kBlockK;
+            Ring rg;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int t = first; t < units && ok; t += step) {
+                int ia, ib;
+                tile_at(a, run_of(t), &ia, &ib);
+                const int own = is_b ? ib * kTileB + (kPair ? rank * a.b_rows : 0) : ia * kRowsA + (kPair ? rank * kTileA : 0);
+                for (int kb = k_lo; kb < k_hi; ++kb) {
+                    if (!wait_phase(ptx::smem_addr(&ctl->empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]);
+                    if (!kPair || rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+                    if (kPair) bar = map_to_rank(bar, 0);
+                    const uint32_t dst = ring + rg.idx * a.stage_bytes + (is_b ? 16384 : 0);
+                    if constexpr (kPair) tma_load_2d_pair(dst, map, kb * kBlockK, own, bar);
+                    else ptx::tma_load_2d(dst, map, kb * kBlockK, own, bar);
+                    ++issued;
+                    rg.next(a.stages);
+                }
+            }
+            // Every stage is released by the MMAs that read it; the releases
+            // reach both CTAs of a pair, so they have to be in before either
+            // leaves.  After a time-out the copies have to land first, and no
+            // release may come.
+            const bool drain_copies = *abort_flag && (!kPair || rank == 0);
+            for (int s = 0; s < a.stages && (kPair || drain_copies); ++s) {
+                const int64_t n = issued / a.stages + (s < issued % a.stages ? 1 : 0);
+                if (n == 0) continue;
+                const uint32_t bar = ptx::smem_addr(drain_copies ? &ctl->full[s] : &ctl->empty[s]);
+                const uint64_t t0 = ptx::global_timer_ns();
+                while (!ptx::mbar_try_wait(bar, (uint32_t)((n - 1) & 1)))
+                    if (ptx::global_timer_ns() - t0 > 10000000) break;
+            }
+        } else if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
+            // ------------------------------------------------ MMA: a block of k to an accumulator
+            Ring rg;
+            uint32_t n = 0;
+            bool ok = true;
+            for (int t = first; t < units && ok; t += step) {
+                run_of(t);
+                for (int kb = k_lo; kb < k_hi; ++kb, ++n) {
+                    const uint32_t slot = n & 1;
+                    if (!wait_phase(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status) ||
+                        !wait_phase(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t at = ring + rg.idx * a.stage_bytes, d = tmem + slot * kMaxTileB;
+                    const uint64_t da = ptx::smem_desc_sw128(at), db = ptx::smem_desc_sw128(at + 16384);
+#pragma unroll
+                    for (int i = 0; i < kBlockK / 32; ++i) mma8<kPair>(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
+                    mma_commit<kPair>(ptx::smem_addr(&ctl->empty[rg.idx]));
+                    mma_commit<kPair>(ptx::smem_addr(&ctl->acc_full[slot]));
+                    rg.next(a.stages);
+                }
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------ scales: of this CTA's rows, and of the tile's columns
+            Ring rg;
+            bool ok = true;
+            for (int t = first; t < units && ok; t += step) {
+                int ia, ib;
+                tile_at(a, run_of(t), &ia, &ib);
+                const int row0 = ia * kRowsA + (kPair ? (int)rank * kTileA : 0), col0 = ib * kTileB;
+                const float *pa[kTileA / 32], *pb[kPerColumn ? kTileB / 32 : 1];
+                bool in_a[kTileA / 32], in_b[kPerColumn ? kTileB / 32 : 1];
+#pragma unroll
+                for (int i = 0; i < kTileA / 32; ++i) {
+                    const int r = row0 + i * 32 + lane;
+                    in_a[i] = r < a.sa.rows;
+                    pa[i] = a.sa.p + (in_a[i] ? (int64_t)(r >> a.sa.shift) * a.sa.rs : 0);
+                }
+#pragma unroll
+                for (int i = 0; i < (kPerColumn ? kTileB / 32 : 1); ++i) {
+                    const int r = kPerColumn ? col0 + i * 32 + lane : col0 + (lane & 1) * kCols;
+                    in_b[i] = r < a.sb.rows && (kPerColumn || lane < 2);
+                    pb[i] = a.sb.p + (in_b[i] ? (int64_t)(r >> a.sb.shift) * a.sb.rs : 0);
+                }
+                for (int kb = k_lo; kb < k_hi; ++kb) {
+                    if (!wait_phase(ptx::smem_addr(&ctl->scale_empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t to = scales + rg.idx * kScaleBytes + lane * 4;
+#pragma unroll
+                    for (int i = 0; i < kTileA / 32; ++i) copy_async4(to + i * 128, pa[i] + kb * a.sa.cs, in_a[i]);
+#pragma unroll
+                    for (int i = 0; i < (kPerColumn ? kTileB / 32 : 1); ++i)
+                        if (kPerColumn || lane < 2) copy_async4(to + kTileA * 4 + i * 128, pb[i] + kb * a.sb.cs, in_b[i]);
+                    arrive_behind_copies(ptx::smem_addr(&ctl->scale_full[rg.idx]));
+                    rg.next(kScaleSlots);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else {
+        // ------------------------------------------------ sums
+        ptx::setmaxnreg_inc<kSumRegs>();
+        const int e = warp - 4, quad = warp & 3, part = e >> 2;
+        WarpTile wt;
+        wt.lane = lane;
+        wt.slot = staging + e * kSlotBytes;
+        wt.bias = bias_smem + e * 128;
+        Ring sr;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int t = first; t < units && ok; t += step) {
+            int ia, ib;
+            tile_at(a, run_of(t), &ia, &ib);
+            Pair sum[kCols / 2];
+#pragma unroll
+            for (int j = 0; j < kCols / 2; ++j) sum[j] = pair(0.0f);
+            for (int kb = k_lo; kb < k_hi; ++kb, ++n) {
+                const uint32_t slot = n & 1, at = scales + sr.idx * kScaleBytes;
+                if (!wait_inline(ptx::smem_addr(&ctl->scale_full[sr.idx]), sr.phase, abort_flag, a.wait_limit_ns, a.status)) {
+                    ok = false;
+                    break;
+                }
+                float s = __uint_as_float(ptx::ld_shared_b32(at + (quad * 32 + lane) * 4));
+                if constexpr (!kPerColumn) s *= __uint_as_float(ptx::ld_shared_b32(at + (kTileA + part) * 4));
+                if (!wait_inline(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t acc = tmem + slot * kMaxTileB + part * kCols + ((uint32_t)(quad * 32) << 16);
+                const Pair s2 = pair(s);
+                uint32_t u[2][32];
+                ptx::tmem_ld_32x32b_x32(acc, u[0]);
+#pragma unroll
+                for (int c = 0; c < kCols / 32; ++c) {
+                    ptx::tmem_ld_wait();
+                    if (c + 1 < kCols / 32) {
+                        ptx::tmem_ld_32x32b_x32(acc + (c + 1) * 32, u[(c + 1) & 1]);
+                    } else {
+                        // everything of this accumulator is in registers
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
+                            mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        Pair p = pair(__uint_as_float(u[c & 1][j]), __uint_as_float(u[c & 1][j + 1]));
+                        Pair q = pair(__uint_as_float(u[c & 1][j + 2]), __uint_as_float(u[c & 1][j + 3]));
+                        if constexpr (kPerColumn) {
+                            // (the row's scale times the column's first, as with one scale for the columns)
+                            const uint4 b = ptx::ld_shared_v4(at + (kTileA + part * kCols + c * 32 + j) * 4);
+                            sum[(c * 32 + j) / 2] = fma2(p, mul2(s2, pair(__uint_as_float(b.x), __uint_as_float(b.y))), sum[(c * 32 + j) / 2]);
+                            sum[(c * 32 + j) / 2 + 1] =
+                                fma2(q, mul2(s2, pair(__uint_as_float(b.z), __uint_as_float(b.w))), sum[(c * 32 + j) / 2 + 1]);
+                        } else {
+                            sum[(c * 32 + j) / 2] = fma2(p, s2, sum[(c * 32 + j) / 2]);
+                            sum[(c * 32 + j) / 2 + 1] = fma2(q, s2, sum[(c * 32 + j) / 2 + 1]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->scale_empty[sr.idx]));
+                sr.next(kScaleSlots);
+            }
+            if (!ok) break;
+            wt.row0 = ia * kRowsA + (kPair ? rank * kTileA : 0) + quad * 32;
+            wt.rows = min(32, a.ma - wt.row0);
+            // (the sums move down 32 columns at a time, so that the finishing code is there once)
+#pragma unroll 1
+            for (int c = part * kCols; c < (part + 1) * kCols; c += 32) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) split(sum[j], &v[2 * j], &v[2 * j + 1]);
+                if constexpr (kCols > 32) {
+#pragma unroll
+                    for (int j = 0; j + 16 < kCols / 2; ++j) sum[j] = sum[j + 16];
+                }
+                wt.b0 = ib * kTileB + c;
+                wt.cols = min(32, a.nb - wt.b0);
+                if (wt.rows <= 0 || wt.cols <= 0) continue;
+                if (t >= a.full) {
+                    float *p = a.part + (((int64_t)(t - a.full) * kCluster + rank) * kTileB + c) * kTileA + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
+                    continue;
+                }
+                finish_values<kAnyAct>(a, wt, v, lane_bias(a, wt.row0, wt.b0, lane), 0);
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group_read<0>();
+    }
+
+    __syncwarp();
+    if (kPair) cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 2) tmem_dealloc<kPair>(tmem, 512);
+}
+
+__global__ void __launch_bounds__(256) scaled_join_kernel(const __grid_constant__ ScaledArgs a, int rows_per_tile) {
+    join_runs<kAnyAct>(a, rows_per_tile);
+}
+
+}  // namespace
+
+ScaledPlan scaled_plan(int64_t ma, int64_t nb, int64_t k) {
+    ScaledPlan pl;
+    // Few rows: the long dim becomes the tile's 128 lanes, so that no lanes
+    // idle and every CTA streams its own weights.
+    if (ma < nb && ma <= 128) {
+        pl.swap = true;
+        std::swap(ma, nb);
+    }
+    const int64_t blocks = cdiv(k, kBlockK);
+    const int64_t wide = nb > 128 ? 256 : 128;
+    const int64_t pair_tiles = cdiv(ma, 256) * cdiv(nb, wide);
+    if (nb > 64 && ma > 128 && (pair_tiles * 2 >= kSms || pair_tiles * blocks >= kSms / 2 * 8)) {
+        pl.pair = true;
+        pl.tile_b = (int32_t)wide;
+        pl.tiles_a = cdiv(ma, 256), pl.tiles_b = cdiv(nb, wide);
+    } else {
+        pl.tile_b = nb <= 64 ? 64 : nb <= 128 ? 128 : 256;
+        while (pl.tile_b > 64 && cdiv(ma, kTileA) * cdiv(nb, pl.tile_b) * 2 <= kSms) pl.tile_b /= 2;
+        pl.tiles_a = cdiv(ma, kTileA), pl.tiles_b = cdiv(nb, pl.tile_b);
+    }
+    // Fewer tiles than run at once: all of them in runs.  A last round that
+    // leaves half the GPU idle or more: its tiles in runs.
+    const int64_t tiles = pl.tiles_a * pl.tiles_b, at_once = pl.pair ? kSms / 2 : kSms, last = tiles % at_once;
+    int64_t parts = 1;
+    if (tiles * 2 <= at_once) parts = std::min(at_once / tiles, blocks / 4);
+    else if (tiles > at_once && last > 0) parts = std::min<int64_t>(at_once / last, 8);
+    if (parts > 1 && tiles > at_once && blocks - blocks / parts < 20) parts = 1;
+    pl.full = tiles;
+    if (parts > 1) {
+        pl.parts = (int32_t)parts;
+        pl.full = tiles <= at_once ? 0 : tiles - last;
+        pl.part_bytes = (size_t)(parts * (tiles - pl.full) * (pl.pair ? 256 : 128) * pl.tile_b * 4);
+    }
+    return pl;
+}
+
+conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *stream) {
+    ScaledProduct pr = given;
+    const ScaledPlan pl = scaled_plan(pr.ma, pr.nb, pr.k);
+    if (pl.tiles_a * pl.tiles_b > INT32_MAX / 16) return CONV_ERR_TOO_LARGE;
+    ScaledArgs a;
+    a.bias_along_a = pl.swap;
+    if (pl.swap) {
+        std::swap(pr.ma, pr.nb);
+        std::swap(pr.a, pr.b);
+        std::swap(pr.d_sa, pr.d_sb);
+        std::swap(pr.res_sa, pr.res_sb);
+        std::swap(pr.pre_sa, pr.pre_sb);
+    }
+    a.ma = (int32_t)pr.ma, a.nb = (int32_t)pr.nb;
+    a.blocks = (int32_t)cdiv(pr.k, kBlockK);
+    a.d = make_side(pr.d, pr.d_sa, pr.d_sb, pr.d_dtype, pr.ma, pr.nb);
+    a.res = make_side(pr.res, pr.res_sa, pr.res_sb, pr.d_dtype, pr.ma, pr.nb);
+    a.pre = make_side(pr.pre, pr.pre_sa, pr.pre_sb, pr.pre_dtype, pr.ma, pr.nb);
+    a.bias = pr.bias, a.bias_dtype = pr.bias_dtype, a.act = pr.act, a.slots = 1;
+    a.sa = {pr.a.scale, pr.a.s_rs, pr.a.s_cs, pr.a.shift, (int32_t)pr.ma};
+    a.sb = {pr.b.scale, pr.b.s_rs, pr.b.s_cs, pr.b.shift, (int32_t)pr.nb};
+    a.wait_limit_ns = wait_limit_ns();
+    a.status = device_status_word();
+    if (!a.status) return CONV_ERR_CUDA;
+    const bool pair = pl.pair;
+    a.tile_b = pl.tile_b, a.tiles_a = (int32_t)pl.tiles_a, a.tiles_b = (int32_t)pl.tiles_b;
+    a.parts = pl.parts, a.full = (int32_t)pl.full, a.part = (float *)workspace;
+    a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
+    a.stage_bytes = 16384 + a.b_rows * kBlockK;
+    a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
+    const int tile_a = pair ? 256 : 128;
+    a.idesc = (1u << 4) | ((pr.a.e5m2 ? 1u : 0u) << 7) | ((pr.b.e5m2 ? 1u : 0u) << 10) | ((uint32_t)(a.tile_b >> 3) << 17) |
+              ((uint32_t)(tile_a >> 4) << 24);
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode(&a.map_a, CONV_FLOAT8_E4M3, pr.a.p, pr.k, pr.ma, pr.a.rs, kBlockK, kTileA, sw) ||
+        !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.b_rows, sw))
+        return CONV_ERR_CUDA;
+    for (auto [s, m] : {std::pair<Side *, CUtensorMap *>{&a.d, &a.map_d}, {&a.pre, &a.map_pre}})
+        if (s->walk == kWalkRows &&
+            !encode(m, s->dtype, s->p, pr.nb, pr.ma, s->sa, s->dtype == CONV_FLOAT32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+            return CONV_ERR_CUDA;
+    typedef void (*Kernel)(ScaledArgs);
+    // [single 64, 128, 256, pair 128, 256][a scale per row of B]
+    static const Kernel kernels[5][2] = {{scaled_product_kernel<false, 32, false>, scaled_product_kernel<false, 32, true>},
+                                         {scaled_product_kernel<false, 64, false>, scaled_product_kernel<false, 64, true>},
+                                         {scaled_product_kernel<false, 128, false>, scaled_product_kernel<false, 128, true>},
+                                         {scaled_product_kernel<true, 64, false>, scaled_product_kernel<true, 64, true>},
+                                         {scaled_product_kernel<true, 128, false>, scaled_product_kernel<true, 128, true>}};
+    const int which = pair ? (a.tile_b == 128 ? 3 : 4) : a.tile_b == 64 ? 0 : a.tile_b == 128 ? 1 : 2, per = pr.b.shift == 0;
+    const Kernel kernel = kernels[which][per];
+    static std::atomic<bool> ready[64][5][2];  // (check_device admits 64 devices)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CONV_ERR_CUDA;
+    if (!ready[dev][which][per].load()) {
+        // (the summing warps wait for registers that the block has to have been launched with)
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+            attr.numRegs * kThreads < 128 * kControlRegs + 32 * kSumWarps * kSumRegs ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess)
+            return CONV_ERR_CUDA;
+        ready[dev][which][per].store(true);
+    }
+    const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
+    const int cluster = pair ? 2 : 1;
+    const size_t smem = (size_t)a.stages * a.stage_bytes + kSumWarps * kSlotBytes + kScaleSlots * kScaleBytes + kBiasBytes + sizeof(SharedCtl);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, device_sm_count() / cluster) * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return CONV_ERR_CUDA;
+    if (a.parts > 1) {
+        const int64_t blocks = (tiles - a.full) * (tile_a / 32) * (a.tile_b / 8);
+        if (blocks > INT32_MAX) return CONV_ERR_TOO_LARGE;
+        if (!launch_behind(scaled_join_kernel, dim3((unsigned)blocks), 32 * std::min(8, a.parts), 0, (cudaStream_t)stream, a, tile_a))
+            return CONV_ERR_CUDA;
+    }
+    return CONV_OK;
+}
+
+}  // namespace i8c

@@ -146,7 +146,7 @@ bool launch(const ScaledProduct &pr, dim3 grid, cudaStream_t s) {
 
 }  // namespace
 
-bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k) { return true; }
+bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k) { return ma <= 32 || k == 0; }
 
 conv_status scaled_rows_launch(const ScaledProduct &pr, void *stream) {
     const int64_t groups = std::min<int64_t>((pr.ma + 7) / 8, 4);
