@@ -147,9 +147,10 @@ __device__ __forceinline__ void load_group(const T *p, const Place<kVec> &at, in
     }
 }
 
-template <bool kVec, typename T>
+// kEven: rows of whole groups.
+template <bool kVec, typename T, bool kEven = false>
 __device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, const float (&v)[8]) {
-    if (kVec && at.whole(i)) {
+    if (kEven ? at.inside(at.column(i, 0)) : kVec && at.whole(i)) {
         const int c = at.column(i, 0);
         if constexpr (kIs16<T>) {
             uint32_t w[4];
@@ -162,12 +163,14 @@ __device__ __forceinline__ void store_group(T *p, const Place<kVec> &at, int i, 
         }
         return;
     }
+    if constexpr (!kEven) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int c = at.column(i, j);
-        if (!at.inside(c)) continue;
-        if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)bits16(v[j], p);
-        else p[c] = v[j];
+        for (int j = 0; j < 8; ++j) {
+            const int c = at.column(i, j);
+            if (!at.inside(c)) continue;
+            if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)bits16(v[j], p);
+            else p[c] = v[j];
+        }
     }
 }
 
@@ -295,6 +298,115 @@ __device__ __forceinline__ void read_group(uint32_t slot, uint32_t stride, Group
     if constexpr (!kIs16<X>) {
         const uint4 b = ptx::ld_shared_v4(slot + stride);
         g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
+    }
+}
+
+// ---------------------------------------------------------------- rows by bulk copies
+// Rows of several matrices on their way to shared memory, one bulk copy per
+// row and matrix: lane m of a worker's first warp feeds matrix m.  A copy
+// takes whole 16-byte pieces, so a row that begins or ends inside one brings
+// bytes of its neighbours along, which the readers mask; where that would
+// reach past the matrix (its first or last row) the ends are copied by
+// elements.  A row lies in its slot as it does past a boundary of 8 elements.
+struct RowFeed {
+    const char *p, *end;   // the matrix's memory
+    int64_t row_bytes;     // from one row to the next
+    uint32_t bytes;        // of a row
+    uint32_t off;          // of the matrix's slot in a stage
+    uint32_t half;         // 16 where a boundary of 16 bytes may not be one of 8 elements
+    bool on;
+
+    __device__ __forceinline__ void set(const MatRef &m, int64_t rows, int32_t cols, uint32_t size, uint32_t at) {
+        p = (const char *)m.p;
+        row_bytes = m.rs * size;
+        bytes = (uint32_t)cols * size;
+        end = p + (rows - 1) * row_bytes + bytes;
+        off = at;
+        half = size == 4 ? 16 : 0;
+        on = true;
+    }
+    // One arrival on `bar` and the row's bytes.
+    __device__ __forceinline__ void fill(int64_t r, uint32_t stage, uint32_t bar) const {
+        if (!on) return;
+        const char *s = p + r * row_bytes, *e = s + bytes;
+        stage += (uint32_t)(uintptr_t)s & half;
+        const char *s0 = s - ((uintptr_t)s & 15), *e0 = e + (-(uintptr_t)e & 15);
+        if (s0 >= p && e0 <= end) {
+            ptx::mbar_arrive_expect_tx(bar, (uint32_t)(e0 - s0));
+            ptx::bulk_copy_g2s(stage + off, s0, (uint32_t)(e0 - s0), bar);
+            return;
+        }
+        const char *s1 = s + (-(uintptr_t)s & 15), *e1 = e - ((uintptr_t)e & 15);
+        const char *const lead_end = s1 < e ? s1 : e;
+        auto copy = [&](const char *from, const char *to) {
+            for (; from < to; from += 2)
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage + off + (uint32_t)(from - s0)), "h"(*(const uint16_t *)from) : "memory");
+        };
+        copy(s, lead_end);
+        if (e1 >= s1) copy(e1, e);
+        if (e1 > s1) {
+            ptx::mbar_arrive_expect_tx(bar, (uint32_t)(e1 - s1));
+            ptx::bulk_copy_g2s(stage + off + (uint32_t)(s1 - s0), s1, (uint32_t)(e1 - s1), bar);
+        } else {
+            ptx::mbar_arrive(bar);
+        }
+    }
+};
+
+// Bytes of a row's slot: the row, and the groups of 8 that its ends lie in.
+__host__ __device__ constexpr uint32_t row_slot_bytes(int32_t cols, uint32_t size) {
+    return ((uint32_t)cols + 7) / 8 * 8 * size + 8 * size;
+}
+
+// Waits for a row, not for ever: a thread that has given up once (the status
+// word then says so) does not wait again.
+struct RowWait {
+    uint64_t limit_ns;
+    int *status;
+    bool gave_up = false;
+    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
+        if (gave_up || ptx::mbar_try_wait(bar, parity)) return;
+        const uint64_t t0 = ptx::global_timer_ns();
+        while (!ptx::mbar_try_wait(bar, parity)) {
+            if (ptx::global_timer_ns() - t0 > limit_ns) {
+                gave_up = true;
+                atomicExch(status, (int)CONV_ERR_DEVICE_TIMEOUT);
+                return;
+            }
+        }
+    }
+};
+
+// Group i of a row in its slot; zeros outside the row.  kEven: rows of whole
+// groups.
+template <bool kEven, typename X>
+__device__ __forceinline__ void slot_group(uint32_t slot, const Place<true> &at, int i, Group<X> &g) {
+    const uint32_t from = slot + (uint32_t)(i * at.threads + at.t) * (uint32_t)(8 * sizeof(X));
+    if (kEven ? at.inside(at.column(i, 0)) : at.whole(i)) {
+        const uint4 a = ptx::ld_shared_v4(from);
+        g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
+        if constexpr (!kIs16<X>) {
+            const uint4 b = ptx::ld_shared_v4(from + 16);
+            g.w[4] = b.x, g.w[5] = b.y, g.w[6] = b.z, g.w[7] = b.w;
+        }
+        return;
+    }
+    if constexpr (kEven) {
+#pragma unroll
+        for (int j = 0; j < (int)(sizeof(g.w) / 4); ++j) g.w[j] = 0;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = at.inside(at.column(i, j));
+            if constexpr (kIs16<X>) {
+                uint16_t v = 0;
+                if (in) asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from + j * 2));
+                if (j % 2) g.w[j / 2] |= (uint32_t)v << 16;
+                else g.w[j / 2] = v;
+            } else {
+                g.w[j] = in ? ptx::ld_shared_b32(from + j * 4) : 0u;
+            }
+        }
     }
 }
 
