@@ -27,8 +27,9 @@ struct BlockNormArgs {
     float eps, skip_scale, branch_scale;
     int32_t param_dtype;
     int32_t post;
-    int32_t turn_sum, turn_y;  // rows of another lead than x's
+    int32_t shift_sum, shift_y;  // rows of another lead than x's
     int64_t per_worker;        // rows of a worker's stretch; 0: rows that begin anywhere, in steps
+    int32_t stages;
     uint64_t wait_limit_ns;
     int *status;
 };
@@ -38,18 +39,18 @@ struct BlockNormArgs {
 template <typename T, typename S, int kNv, bool kWarp, bool kEven>
 __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 1)
     block_norm_rows_kernel(const BlockNormArgs a) {
-    __shared__ __align__(16) BlockSums sums;
-    Summer block_sum{&sums};
+    __shared__ __align__(16) float sums[2][32];
+    RowSummer block_sum{sums};
     extern __shared__ __align__(128) uint8_t smem[];
     const int local = kWarp ? threadIdx.x / 32 : 0, workers = kWarp ? 8 : 1;
     const int64_t worker = (int64_t)blockIdx.x * workers + local;
-    const S *skip = (const S *)a.skip.p;
-    S *sum = (S *)const_cast<void *>(a.sum.p);
-    T *y = (T *)const_cast<void *>(a.y.p);
+    const bool skip = a.skip.p;
     Stretch rows;
     rows.first = a.per_worker ? worker * a.per_worker : worker;
     rows.end = a.per_worker ? min(a.rows, rows.first + a.per_worker) : a.rows;
     rows.step = a.per_worker ? 1 : (int64_t)gridDim.x * workers;
+    S *sum = (S *)const_cast<void *>(a.sum.p) + (a.sum.p ? rows.first * a.sum.rs : 0);
+    T *y = (T *)const_cast<void *>(a.y.p) + (a.y.p && !a.y_scale.p ? rows.first * a.y.rs : 0);
     Place<true> at;
     at.t = kWarp ? threadIdx.x % 32 : threadIdx.x;
     at.threads = kWarp ? 32 : blockDim.x;
@@ -58,37 +59,29 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
     const float per = 1.0f / (float)a.cols;
     const uint32_t x_slot = row_slot_bytes(a.cols, sizeof(T)), stage_bytes = x_slot + (skip ? row_slot_bytes(a.cols, sizeof(S)) : 0);
     // (the gains are every worker's own where rows begin anywhere, the gate always)
-    const int own = a.per_worker ? 0 : local;
-    const RowSpace space = row_space(workers, stage_bytes, (a.per_worker ? 2 : 2 * workers) + workers, at.threads, kNv,
-                                     (a.turn_sum ? turn_elems(a.cols) * sizeof(S) : 0) + (a.turn_y ? turn_elems(a.cols) * sizeof(T) : 0));
-    const uint32_t base = ptx::smem_addr(smem), bars = base + local * 8 * kStages, ring = base + space.rows + local * kStages * stage_bytes;
-    const uint32_t set = kNv * 32 * at.threads;
-    const uint32_t stride = at.threads * 16;
-    const Kept post_gain{base + space.kept + (2 * own) * set + at.t * 16, stride}, gain{post_gain.base + set, stride};
-    const Kept gate{base + space.kept + ((a.per_worker ? 2 : 2 * workers) + local) * set + at.t * 16, stride};
-    uint8_t *turned = smem + space.turned + local * (space.total - space.turned) / workers;
-    Turn<S> turn_sum{(S *)turned, 0};  // (the lead a row at a time: the output's may change where the rows read have one)
-    if (a.turn_sum) turned += turn_elems(a.cols) * sizeof(S);
-    Turn<T> turn_y{(T *)turned, 0};
-
+    const int own = a.per_worker ? 0 : local, first_gate = a.per_worker ? 2 : 2 * workers;
+    const RowSpace space = row_space(workers, a.stages, stage_bytes, first_gate + workers, at.threads, kNv);
+    const uint32_t base = ptx::smem_addr(smem), bars = base + local * 8 * kMostStages, ring = base + space.rows + local * a.stages * stage_bytes;
+    const uint32_t set = kNv * 32 * at.threads, stride = at.threads * 16, kept = base + space.kept + at.t * 16;
+    const Kept post_gain{kept + 2 * own * set, stride}, gain{kept + (2 * own + 1) * set, stride}, gate{kept + (first_gate + local) * set, stride};
     RowFeed feed;
     feed.on = false;
-    if (at.t == 0) feed.set(a.x, a.rows, a.cols, sizeof(T), 0);
-    if (at.t == 1 && skip) feed.set(a.skip, a.rows, a.cols, sizeof(S), x_slot);
+    if (at.t == 0) feed.set(a.x, a.rows, a.cols, sizeof(T), 0, rows.first, rows.step);
+    if (at.t == 1 && skip) feed.set(a.skip, a.rows, a.cols, sizeof(S), x_slot, rows.first, rows.step);
     if (at.t == 0) {
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) ptx::mbar_init(bars + 8 * i, skip ? 2 : 1);
+        for (int i = 0; i < a.stages; ++i) ptx::mbar_init(bars + 8 * i, skip ? 2 : 1);
         ptx::fence_mbar_init();
     }
     row_sync<kWarp>();
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     RowWait wait{a.wait_limit_ns, a.status};
-    auto fill = [&](int64_t r, int stage) {
-        if (at.t < 2 && r < rows.end) feed.fill(r, ring + stage * stage_bytes, bars + 8 * stage);
+    int64_t to_fill = rows.first;  // the row that is fetched next
+    auto fill = [&](int stage) {
+        if (feed.on && to_fill < rows.end) feed.fill<kEven>(ring + stage * stage_bytes, bars + 8 * stage);
+        to_fill += rows.step;
     };
-#pragma unroll
-    for (int d = 0; d < kStages; ++d) fill(rows.first + d * rows.step, d);
+    for (int d = 0; d < a.stages; ++d) fill(d);
     if (!a.per_worker || local == 0) {
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
@@ -106,30 +99,19 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
     uint32_t phase = 0;
     for (int64_t r = rows.first; r < rows.end; r += rows.step) {
         if (r >= gate_end) {
-            // (with the branch's scale)
             const int64_t which = r / a.rows_per_gate;
             gate_end = (which + 1) * a.rows_per_gate;
 #pragma unroll
-            for (int i = 0; i < kNv; ++i) {
-                float g[8];
-                load_params(gate_row(a.gate, which), a.gate.dtype, 1.0f, at, i, g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] *= a.branch_scale;
-                gate.keep(i, g);
-            }
+            for (int i = 0; i < kNv; ++i) keep_gate(gate, a.gate, which, post_gain, a.post, a.branch_scale, at, i);
         }
-        if (!kEven && a.turn_sum) turn_sum.lead = lead_of(sum + r * a.sum.rs);
-        if (!kEven && a.turn_y) turn_y.lead = lead_of(y + r * a.y.rs);
         const uint32_t slot = ring + stage * stage_bytes;
         wait(bars + 8 * stage, phase);
-        Group<S> gs[kNv];
         Pair v[kNv][4];
         Pair s2 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
             Group<T> gx;
             slot_group<kEven>(slot, at, i, gx);
-            if (skip) slot_group<kEven>(slot + x_slot, at, i, gs[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 v[i][j] = element2(gx, j);
@@ -142,39 +124,41 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
             rx = inverse_root(kWarp ? warp_sum(s) : block_sum(s), per, a.eps);
             if (at.t == 0 && a.post_rstd) a.post_rstd[r] = rx;
         }
-        // the slots just read take the row kStages steps on
-        if (kWarp || !a.post) row_sync<kWarp>();
-        fill(r + kStages * rows.step, stage);
-        if (++stage == kStages) stage = 0, phase ^= 1;
         s2 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < kNv; ++i) {
-            Pair g[4], p[4];
+            Pair g[4];
             gate.get(i, g);
-            if (a.post) post_gain.get(i, p);
+            Group<S> gs;
+            slot_group<kEven>(slot + x_slot, at, i, gs, skip);
+            // (without a post norm rx is 1, without a skip its values 0: no branch costs less)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                Pair h = v[i][j];
-                if (a.post) h = mul2(mul2(h, pair(rx)), p[j]);
-                h = mul2(h, g[j]);
-                if (skip) h = fma2(skip_scale, element2(gs[i], j), h);
-                v[i][j] = h;
-                s2 = fma2(h, h, s2);
+                v[i][j] = fma2(skip_scale, element2(gs, j), mul2(mul2(v[i][j], pair(rx)), g[j]));
+                s2 = fma2(v[i][j], v[i][j], s2);
             }
         }
-        if (sum) {
+        if (a.sum.p) {
 #pragma unroll
             for (int i = 0; i < kNv; ++i) {
                 float o[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) split(v[i][j], &o[2 * j], &o[2 * j + 1]);
-                if (!kEven && a.turn_sum) turn_group(turn_sum, at, i, o);
-                else store_group<true, S, kEven>(sum + r * a.sum.rs, at, i, o);
+                if (!kEven && a.shift_sum) store_shifted(sum, at, i, o);
+                else store_group<true, S, kEven>(sum, at, i, o);
             }
         }
-        if (y) {
-            const float s = sum_of(s2), rs = inverse_root(kWarp ? warp_sum(s) : block_sum(s), per, a.eps);
+        float rs = 1.0f;
+        if (a.y.p) {
+            const float s = sum_of(s2);
+            rs = inverse_root(kWarp ? warp_sum(s) : block_sum(s), per, a.eps);
             if (at.t == 0 && a.rstd) a.rstd[r] = rs;
+        }
+        // everything of the slots has been read: they take the row `stages` steps on
+        if (kWarp || !a.y.p) row_sync<kWarp>();
+        fill(stage);
+        if (++stage == a.stages) stage = 0, phase ^= 1;
+        if (a.y.p) {
 #pragma unroll
             for (int i = 0; i < kNv; ++i) {
                 Pair g[4];
@@ -205,19 +189,15 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
                         for (int j = 0; j < 8; ++j)
                             if (c + j < a.cols) p[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (j % 4 * 8));
                     }
-                } else if (!kEven && a.turn_y) {
-                    turn_group(turn_y, at, i, o);
+                } else if (!kEven && a.shift_y) {
+                    store_shifted(y, at, i, o);
                 } else {
-                    store_group<true, T, kEven>(y + r * a.y.rs, at, i, o);
+                    store_group<true, T, kEven>(y, at, i, o);
                 }
             }
         }
-        if (!kEven && (a.turn_sum || a.turn_y)) {
-            row_sync<kWarp>();
-            if (a.turn_sum) store_turned(sum + r * a.sum.rs, turn_sum, at);
-            if (a.turn_y) store_turned(y + r * a.y.rs, turn_y, at);
-            row_sync<kWarp>();
-        }
+        if (a.sum.p) sum += rows.step * a.sum.rs;
+        if (a.y.p && !a.y_scale.p) y += rows.step * a.y.rs;
     }
 }
 
@@ -287,17 +267,25 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(const Block
     }
 }
 
-size_t forward_smem(const BlockNormArgs &a, const Held &h, bool aligned, int64_t ts, int64_t ss) {
+// Threads of an SM that the kernel's launch bounds leave registers for.
+int forward_threads(const Held &h) { return h.warp ? 768 : h.nv == 1 ? 1024 : 512; }
+
+// Rows on their way, and the shared memory with them.
+size_t forward_smem(const BlockNormArgs &a, const Held &h, bool aligned, int64_t ts, int64_t ss, int *stages) {
     const uint32_t stage = row_slot_bytes(a.cols, (uint32_t)ts) + (a.skip.p ? row_slot_bytes(a.cols, (uint32_t)ss) : 0);
-    return row_space(h.warp ? 8 : 1, stage, kept_sets(aligned, h.warp), h.warp ? 32 : h.threads, h.nv,
-                     (uint32_t)((a.turn_sum ? turn_elems(a.cols) * ss : 0) + (a.turn_y ? turn_elems(a.cols) * ts : 0))).total;
+    const int workers = h.warp ? 8 : 1;
+    auto space = [&](int n) {
+        return row_space(workers, n, stage, kept_sets(aligned, h.warp, 1), h.warp ? 32 : h.threads, h.nv).total;
+    };
+    *stages = stages_for(space(0), workers * stage, std::min(16, forward_threads(h) / h.threads));
+    return space(*stages);
 }
 
 template <typename T, typename S, int kNv, bool kWarp, bool kEven>
 bool launch_rows(BlockNormArgs a, const Held &h, bool aligned, cudaStream_t s) {
     const int workers = kWarp ? 8 : 1;
-    const size_t smem = forward_smem(a, h, aligned, sizeof(T), sizeof(S));
-    const int64_t most = workers_at_once(h, kWarp ? 768 : kNv == 1 ? 1024 : 512, smem);
+    const size_t smem = forward_smem(a, h, aligned, sizeof(T), sizeof(S), &a.stages);
+    const int64_t most = workers_at_once(h, forward_threads(h), smem);
     int64_t grid;
     if (aligned) {
         a.per_worker = stretch_of(a.rows, most);
@@ -390,16 +378,16 @@ conv_status conv_block_norm(const conv_matrix_desc *x, const void *x_dev, const 
     if (!a.status) return CONV_ERR_CUDA;
     const bool eight = y_scale != nullptr;
     // (8-bit rows are written in pieces of 8 bytes, their blocks counted from an aligned row's start)
-    a.turn_sum = sum && !one_lead({&a.x, &a.sum});
-    a.turn_y = y && !eight && !one_lead({&a.x, &a.y});
+    a.shift_sum = sum && !one_lead({&a.x, &a.sum});
+    a.shift_y = y && !eight && !one_lead({&a.x, &a.y});
     const bool unit = unit_columns(a.x) && unit_columns(a.skip) && unit_columns(a.sum) && unit_columns(a.y) && unit_columns(a.gate);
-    const bool fits = (!a.turn_sum && !a.turn_y) || cols <= 4096;
-    Held h = unit && fits && one_lead({&a.x, &a.skip}) && (!eight || (aligned_rows(a.x) && aligned_rows(a.y)))
+    Held h = unit && one_lead({&a.x, &a.skip}) && (!eight || (aligned_rows(a.x) && aligned_rows(a.y)))
                        ? held(cols, aligned_rows(a.x),
-                              cols % 8 == 0 && aligned_rows(a.x) && aligned_rows(a.sum) && (eight || aligned_rows(a.y)), false)
+                              cols % 8 == 0 && aligned_rows(a.x) && aligned_rows(a.sum) && (eight || aligned_rows(a.y)))
                        : Held();
     const int32_t s_type = skip ? skip->dtype : sum ? sum->dtype : x->dtype;
-    if (h.nv && forward_smem(a, h, aligned_rows(a.x), channel_elem_size(x->dtype), channel_elem_size(s_type)) > 216 << 10) h = Held();
+    int stages;
+    if (h.nv && forward_smem(a, h, aligned_rows(a.x), channel_elem_size(x->dtype), channel_elem_size(s_type), &stages) > 216 << 10) h = Held();
     const cudaStream_t s = (cudaStream_t)stream;
     bool ok;
     if (h.nv == 0) {

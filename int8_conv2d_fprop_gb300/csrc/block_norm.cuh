@@ -59,44 +59,58 @@ __device__ __forceinline__ const void *gate_row(const MatRef &gate, int64_t row)
     return gate.p ? (const char *)gate.p + row * gate.rs * (gate.dtype == CONV_FLOAT32 ? 4 : 2) : nullptr;
 }
 
+// The gate (with the branch's scale) and the post gain, in one: what a row of
+// gate `which` is multiplied by.
+__device__ __forceinline__ void keep_gate(const Kept &kept, const MatRef &gate, int64_t which, const Kept &post_gain, bool post,
+                                          float branch_scale, const Place<true> &at, int i) {
+    float g[8];
+    load_params(gate_row(gate, which), gate.dtype, 1.0f, at, i, g);
+    Pair p[4];
+    if (post) post_gain.get(i, p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        Pair w = mul2(pair(g[2 * j], g[2 * j + 1]), pair(branch_scale));
+        if (post) w = mul2(w, p[j]);
+        split(w, &g[2 * j], &g[2 * j + 1]);
+    }
+    kept.keep(i, g);
+}
+
 // The rows of a worker: a stretch, or (rows that begin anywhere) every
 // step-th, the steps being a multiple of 8 so that all begin alike.
 struct Stretch {
     int64_t first, end, step;
 };
 
-constexpr int kStages = 2;  // rows on their way, the one being read among them
-
-// Shared memory of the row kernels: barriers, rows, kept parameters, rows
-// being turned (offsets; the same on both sides of a launch).
+// Shared memory of the row kernels: barriers, rows, kept parameters (offsets;
+// the same on both sides of a launch).
 struct RowSpace {
-    uint32_t rows, stage_bytes, kept, turned, total;
+    uint32_t rows, kept, total;
 };
-__host__ __device__ inline RowSpace row_space(int workers, uint32_t stage_bytes, int kept_sets, int worker_threads, int nv,
-                                              uint32_t turned_bytes) {
+constexpr int kMostStages = 4;  // rows on their way, the one being read among them
+__host__ __device__ inline RowSpace row_space(int workers, int stages, uint32_t stage_bytes, int kept_sets, int worker_threads,
+                                              int nv) {
     RowSpace s;
-    s.stage_bytes = stage_bytes;
-    s.rows = 128;  // (barriers of 8 workers, two stages each)
-    s.kept = s.rows + workers * kStages * stage_bytes;
-    s.turned = s.kept + kept_sets * nv * 32 * worker_threads;
-    s.total = s.turned + workers * turned_bytes;
+    s.rows = 8 * 8 * kMostStages;  // (behind the barriers of 8 workers)
+    s.kept = s.rows + workers * stages * stage_bytes;
+    s.total = s.kept + kept_sets * nv * 32 * worker_threads;
     return s;
 }
 
 // ---------------------------------------------------------------- launches
-// How rows are held: by a warp of one group of 8 per lane (in the forward pass
-// and even rows, two), else by a block of one group per thread up to 512 of
-// them, two up to 1024.  (Two groups of the gradient, or of rows with ends, do
-// not fit a warp's registers.)
+// How rows are held: by a warp of one group of 8 per lane (of even rows, two),
+// else by a block of one group per thread up to 512 of them, two up to 1024.
+// (The code for the ends of rows would not fit the registers beside two
+// groups of a warp.)
 struct Held {
     int nv = 0, threads = 0;  // nv == 0: in shared memory
     bool warp = false, even = false;
 };
-inline Held held(int64_t cols, bool aligned, bool even, bool grad) {
+inline Held held(int64_t cols, bool aligned, bool even) {
     Held h;
     h.even = even;
     const int64_t groups = aligned ? (cols + 7) / 8 : (cols + 14) / 8;
-    if (groups <= (even && !grad ? 64 : 32)) {
+    if (groups <= (even ? 64 : 32)) {
         h.warp = true, h.threads = 256;
         h.nv = groups <= 32 ? 1 : 2;
     } else if (groups <= 1024) {
@@ -166,7 +180,15 @@ inline int64_t workers_at_once(const Held &h, int threads_bound, size_t smem) {
 // workers' alike but the last one's.
 inline int64_t stretch_of(int64_t rows, int64_t most) { return (rows + most - 1) / most; }
 
-inline uint32_t kept_sets(bool stretches, bool warp) { return (stretches ? 2 : warp ? 16 : 2) + (warp ? 8 : 1); }
+// Sets of kept parameters: two gains for all workers, or (rows that begin
+// anywhere) for each, and `more` for each.
+inline int kept_sets(bool stretches, bool warp, int more) { return (stretches ? 2 : warp ? 16 : 2) + more * (warp ? 8 : 1); }
+
+// As many rows on their way as leave room for `blocks` blocks on an SM, two at least.
+inline int stages_for(uint32_t fixed, uint32_t per_stage, int blocks) {
+    const int64_t room = ((224 << 10) / blocks - 2048 - (int64_t)fixed) / (int64_t)per_stage;
+    return (int)std::max<int64_t>(2, std::min<int64_t>(kMostStages, room));
+}
 
 // The types of x and of the stream, as a call of f.
 template <typename F>

@@ -27,8 +27,8 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_grad_any_kernel(const 
     ptx::launch_dependents();
     if (first >= end) return;
     float *const dg = a.part_gain ? a.part_gain + worker * a.part_cols : nullptr;
-    float *const dp = a.part_gate && a.whole ? a.part_gate + worker * a.part_cols : nullptr;
-    float *const sv = a.part_gate || a.dgate.p ? a.scratch + worker * a.part_cols : nullptr;  // S of the gate
+    float *const dp = a.part_post ? a.part_post + worker * a.part_cols : nullptr;
+    float *const sv = a.part_post || a.dgate.p ? a.scratch + worker * a.part_cols : nullptr;  // S of the gate
     for (int c = threadIdx.x; c < a.cols; c += kAnyThreads) {
         if (dg) dg[c] = 0.0f;
         if (dp) dp[c] = 0.0f;
@@ -77,34 +77,32 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_grad_any_kernel(const 
         for (int c = threadIdx.x; c < a.cols; c += kAnyThreads) {
             const float t = sv[c];
             sv[c] = 0.0f;
-            if (!a.whole) {
-                if (a.part_gate) a.part_gate[(worker + which) * a.part_cols + c] = t;
-                continue;
-            }
             const float b = a.branch_scale * t;
             if (dp) dp[c] += b * (a.gate.p ? load_as_float(a.gate.p, gate + c * a.gate.cs, a.gate.dtype) : 1.0f);
-            if (a.dgate.p)
+            if (a.part_gate) a.part_gate[(worker + which) * a.part_cols + c] = t;
+            else if (a.dgate.p)
                 store_from_float(const_cast<void *>(a.dgate.p), which * a.dgate.rs + c * a.dgate.cs, a.dgate.dtype,
                                  b * (a.post && a.post_gain ? load_as_float(a.post_gain, c, a.param_dtype) : 1.0f));
         }
     }
 }
 
-// Adds the workers' shares.  blockIdx.y 0: dgain, 1: dpost_gain (8 columns and
-// 64 lines of shares at a time: one or two loads of a thread's in flight cover
-// the workers), 2 + i: dgate of gates 16 i to 16 i + 15, a warp each on 32
-// columns.  Worker w's shares start at (lead + w lead_step) mod 8.
+// Adds the shares.  blockIdx.y 0: dgain, 1: dpost_gain, of the blocks (8
+// columns and 64 lines at a time, 20 loads of a thread in flight: one round
+// covers them), 2 + i: dgate of gates 16 i to 16 i + 15 of the workers, a warp
+// each on 32 columns.  The shares of worker w (of a block, where it is one)
+// start at (lead + w lead_step) mod 8.
 struct BlockNormJoin {
-    const float *part_gain, *part_gate;
-    MatRef gate, dgate;
+    const float *part_gain, *part_post, *part_gate;
+    MatRef dgate;
     const void *post_gain;
     void *dgain, *dpost_gain;
     int64_t gates, rows_per_gate, per_worker;
-    int32_t workers, cols, part_cols, whole, lead, lead_step, param_dtype, post;
+    int32_t blocks, warps, workers, cols, part_cols, lead, lead_step, param_dtype, post;
     float branch_scale;
 };
 __global__ void __launch_bounds__(512) block_norm_join_kernel(const BlockNormJoin a) {
-    __shared__ float red[64][8];
+    __shared__ float red[16][8];
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     if (blockIdx.y >= 2) {
@@ -112,67 +110,53 @@ __global__ void __launch_bounds__(512) block_norm_join_kernel(const BlockNormJoi
         const int c = blockIdx.x * 32 + threadIdx.x % 32;
         if (g >= a.gates || c >= a.cols) return;
         // the workers whose stretches meet the gate's rows
-        const int64_t lo = a.per_worker ? g * a.rows_per_gate / a.per_worker : 0;
-        const int64_t hi = a.per_worker ? ((g + 1) * a.rows_per_gate - 1) / a.per_worker : a.workers - 1;
+        const int lo = a.per_worker ? (int)(g * a.rows_per_gate / a.per_worker) : 0;
+        const int hi = a.per_worker ? (int)(((g + 1) * a.rows_per_gate - 1) / a.per_worker) : a.workers - 1;
+        const float *p = a.part_gate + g * a.part_cols + c;
         float s = 0.0f;
 #pragma unroll 1
-        for (int64_t w0 = lo; w0 <= hi; w0 += 16) {
-            float v[16];
+        for (int w0 = lo; w0 <= hi; w0 += 20) {
+            float v[20];
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-                v[u] = w0 + u <= hi ? a.part_gate[(w0 + u + g) * a.part_cols + c + ((a.lead + (w0 + u) * a.lead_step) & 7)] : 0.0f;
+            for (int u = 0; u < 20; ++u)
+                v[u] = w0 + u <= hi ? p[(int64_t)(w0 + u) * a.part_cols + ((a.lead + (w0 + u) * a.lead_step) & 7)] : 0.0f;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) s += v[u];
+            for (int u = 0; u < 20; ++u) s += v[u];
         }
         s *= a.branch_scale;
         if (a.post && a.post_gain) s *= load_as_float(a.post_gain, c, a.param_dtype);
         store_from_float(const_cast<void *>(a.dgate.p), g * a.dgate.rs + c * a.dgate.cs, a.dgate.dtype, s);
         return;
     }
-    const bool post = blockIdx.y == 1;
-    if (post ? !a.dpost_gain : !a.dgain) return;
+    void *out = blockIdx.y ? a.dpost_gain : a.dgain;
+    if (!out) return;
     const int tx = threadIdx.x % 8, ty = threadIdx.x / 8;
     const int c = blockIdx.x * 8 + tx;
-    const float *part = post ? a.part_gate : a.part_gain;
-    const bool slots = post && !a.whole;  // shares of S, in slots w + g
-    const int64_t lines = slots ? a.workers + a.gates - 1 : a.workers;
+    const float *p = (blockIdx.y ? a.part_post : a.part_gain) + c;
+    const int lead = a.warps ? 0 : a.lead, lead_step = a.warps ? 0 : a.lead_step;
     float s = 0.0f;
     if (c < a.cols) {
 #pragma unroll 1
-        for (int64_t i0 = ty; i0 < lines; i0 += 64 * 8) {
-            float v[8], g[8];
+        for (int w0 = ty; w0 < a.blocks; w0 += 64 * 20) {
+            float v[20];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int64_t i = i0 + 64 * u;
-                int64_t w = i;
-                bool there = i < lines;
-                g[u] = 1.0f;
-                if (slots && a.gates > 1 && there) {
-                    // slot i is of the last gate whose first slot is not behind it (or of none)
-                    int64_t lo = 0, hi = a.gates - 1;
-                    while (lo < hi) {
-                        const int64_t mid = (lo + hi + 1) / 2;
-                        if (mid * a.rows_per_gate / a.per_worker + mid <= i) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    w = i - lo;
-                    there = w <= ((lo + 1) * a.rows_per_gate - 1) / a.per_worker;
-                    if (a.gate.p && there) g[u] = load_as_float(a.gate.p, lo * a.gate.rs + c * a.gate.cs, a.gate.dtype);
-                } else if (slots && there && a.gate.p) {
-                    g[u] = load_as_float(a.gate.p, c * a.gate.cs, a.gate.dtype);
-                }
-                v[u] = there ? part[i * a.part_cols + c + ((a.lead + w * a.lead_step) & 7)] : 0.0f;
+            for (int u = 0; u < 20; ++u) {
+                const int w = w0 + 64 * u;
+                v[u] = w < a.blocks ? p[(int64_t)w * a.part_cols + ((lead + w * lead_step) & 7)] : 0.0f;
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s = fmaf(v[u], g[u], s);
+            for (int u = 0; u < 20; ++u) s += v[u];
         }
     }
-    red[ty][tx] = s;
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (threadIdx.x % 32 < 8) red[threadIdx.x / 32][tx] = s;
     __syncthreads();
     if (ty || c >= a.cols) return;
-    for (int i = 1; i < 64; ++i) s += red[i][tx];
-    if (post) store_from_float(a.dpost_gain, c, a.param_dtype, slots ? s * a.branch_scale : s);
-    else store_from_float(a.dgain, c, a.param_dtype, s);
+    s = red[0][tx];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += red[i][tx];
+    store_from_float(out, c, a.param_dtype, s);
 }
 
 __global__ void __launch_bounds__(256) zero_matrix_kernel(MatRef m, int64_t rows, int64_t cols) {
@@ -182,11 +166,18 @@ __global__ void __launch_bounds__(256) zero_matrix_kernel(MatRef m, int64_t rows
         for (int64_t c = threadIdx.x; c < cols; c += 256) store_from_float(const_cast<void *>(m.p), r * m.rs + c * m.cs, m.dtype, 0.0f);
 }
 
-size_t grad_smem(const BlockNormGradArgs &a, const Held &h, bool aligned, int64_t ts, int64_t ss) {
+// Rows on their way, and the shared memory with them (two blocks to an SM where
+// a warp holds a row).
+size_t grad_smem(const BlockNormGradArgs &a, const Held &h, bool aligned, int64_t ts, int64_t ss, int *stages) {
     const uint32_t t_slot = row_slot_bytes(a.cols, (uint32_t)ts), s_slot = row_slot_bytes(a.cols, (uint32_t)ss);
     const uint32_t stage = (a.dy.p ? t_slot + s_slot : 0) + (a.dsum.p ? s_slot : 0) + (a.x.p ? t_slot : 0);
-    return row_space(h.warp ? 8 : 1, stage, kept_sets(aligned, h.warp), h.warp ? 32 : h.threads, h.nv,
-                     (uint32_t)((a.turn_dskip ? turn_elems(a.cols) * ss : 0) + (a.turn_dx ? turn_elems(a.cols) * ts : 0))).total;
+    const int workers = h.warp ? 8 : 1;
+    auto space = [&](int n) {
+        return row_space(workers, n, stage, kept_sets(aligned, h.warp, 2), h.warp ? 32 : h.threads, h.nv).total;
+    };
+    *stages = stages_for(space(0), workers * stage, std::min(16, 512 / h.threads));
+    // (at the end the warps' shares lie over all of it)
+    return std::max<size_t>(space(*stages), h.warp ? (size_t)a.cols * 64 : 0);
 }
 
 // (room for a lead and for whole groups)
@@ -198,11 +189,12 @@ int64_t most_workers(int64_t rows, int64_t cols) {
     return std::min<int64_t>(rows, cols <= 512 ? 16 * 152 : 4 * 152);
 }
 
-// Lines of shares: each worker's of dgain, S's slots (the gates of stretches
-// are at most as many as the workers), and a scratch line for each block.
+// Lines of shares: each worker's of dgain and of dpost_gain, S's slots (the
+// gates of stretches are at most as many as the workers), and a scratch line
+// for each block.
 size_t block_norm_grad_bytes(int64_t rows, int64_t cols) {
     if (rows == 0) return 0;
-    return (size_t)round_up(4 * most_workers(rows, cols) * part_columns(cols) * 4, 256);
+    return (size_t)round_up(5 * most_workers(rows, cols) * part_columns(cols) * 4, 256);
 }
 
 }  // namespace
@@ -312,8 +304,8 @@ conv_status conv_block_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     a.param_dtype = p->param_dtype, a.post = p->post_norm && x;
     const MatRef &ref = dy ? a.dy : a.dsum;
     const bool one = one_lead({&ref, &a.dsum, &a.x, &a.h});
-    a.turn_dx = dx && !one_lead({&ref, &a.dx});
-    a.turn_dskip = dskip && !one_lead({&ref, &a.dskip});
+    a.shift_dx = dx && !one_lead({&ref, &a.dx});
+    a.shift_dskip = dskip && !one_lead({&ref, &a.dskip});
     const bool unit = unit_columns(a.dy) && unit_columns(a.dsum) && unit_columns(a.x) && unit_columns(a.h) &&
                       unit_columns(a.dx) && unit_columns(a.dskip) && unit_columns(a.gate) && unit_columns(a.dgate);
     const bool aligned = aligned_rows(ref);
@@ -321,14 +313,13 @@ conv_status conv_block_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     if (!a.status) return CONV_ERR_CUDA;
     // (gates' gradients leave in aligned groups, whole gates' in even rows)
     Held h = unit && one && ((aligned && aligned_rows(a.dgate)) || a.gates == 1)
-                 ? held(cols, aligned, cols % 8 == 0 && aligned && aligned_rows(a.dx) && aligned_rows(a.dskip) && aligned_rows(a.dgate), true)
+                 ? held(cols, aligned, cols % 8 == 0 && aligned && aligned_rows(a.dx) && aligned_rows(a.dskip) && aligned_rows(a.dgate))
                  : Held();
-    if ((a.turn_dx || a.turn_dskip) && cols > 5120) h = Held();
     const int64_t ts = channel_elem_size(x_type), ss = channel_elem_size(s_type);
     size_t smem = 0;
     int64_t most = 0;
     if (h.nv) {
-        smem = grad_smem(a, h, aligned, ts, ss);
+        smem = grad_smem(a, h, aligned, ts, ss, &a.stages);
         most = std::min(workers_at_once(h, 512, smem), most_workers(rows, cols));
         if (smem > 216 << 10 || (!h.even && a.gates > most)) h = Held();
     }
@@ -352,8 +343,9 @@ conv_status conv_block_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     const int64_t grid = (workers + per_block - 1) / per_block;
     const int64_t lines = most_workers(rows, cols);
     a.part_gain = dgain_dev ? (float *)workspace : nullptr;
-    a.part_gate = dpost_gain_dev || (dgate && !a.whole) ? (float *)workspace + lines * a.part_cols : nullptr;
-    a.scratch = (float *)workspace + 3 * lines * a.part_cols;
+    a.part_post = dpost_gain_dev ? (float *)workspace + lines * a.part_cols : nullptr;
+    a.part_gate = dgate && !a.whole ? (float *)workspace + 2 * lines * a.part_cols : nullptr;
+    a.scratch = (float *)workspace + 4 * lines * a.part_cols;
     bool ok;
     if (h.nv)
         ok = x_type == CONV_FLOAT32   ? launch_block_norm_grad_f32(a, h, grid, smem, s)
@@ -364,10 +356,11 @@ conv_status conv_block_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
     const bool gates_left = dgate && !a.whole;
     if (ok && (dgain_dev || dpost_gain_dev || gates_left)) {
         BlockNormJoin j;
-        j.part_gain = a.part_gain, j.part_gate = a.part_gate, j.gate = a.gate, j.dgate = a.dgate, j.post_gain = post_gain_dev;
+        j.part_gain = a.part_gain, j.part_post = a.part_post, j.part_gate = a.part_gate;
+        j.dgate = a.dgate, j.post_gain = post_gain_dev;
         j.dgain = dgain_dev, j.dpost_gain = dpost_gain_dev;
         j.gates = a.gates, j.rows_per_gate = a.rows_per_gate, j.per_worker = a.per_worker;
-        j.workers = (int32_t)workers, j.cols = a.cols, j.part_cols = a.part_cols, j.whole = a.whole;
+        j.blocks = (int32_t)grid, j.warps = h.warp, j.workers = (int32_t)workers, j.cols = a.cols, j.part_cols = a.part_cols;
         const Lead lead = h.nv && !aligned ? lead_of_rows(ref) : Lead{0, 0};
         j.lead = (int32_t)lead.base, j.lead_step = (int32_t)lead.step;
         j.param_dtype = p->param_dtype, j.post = a.post, j.branch_scale = p->branch_scale;

@@ -226,6 +226,60 @@ __device__ __forceinline__ void store_turned(T *p, const Turn<T> &u, const Place
     }
 }
 
+// Stores group i of a row whose groups begin elsewhere than the thread's
+// (another lead): the thread's last elements and the next one's first make up
+// an aligned group, except at a warp's ends and the row's, whose elements go
+// one by one.  The whole warp takes part.
+template <typename T>
+__device__ __forceinline__ void store_shifted(T *p, const Place<true> &at, int i, const float (&v)[8]) {
+    const int b = (at.lead - lead_of(p)) & 7;  // the thread's first element on the output's boundary
+    constexpr int kWords = kIs16<T> ? 4 : 8;
+    uint32_t w[2 * kWords];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+        if constexpr (kIs16<T>) w[j] = pack2(v[2 * j], v[2 * j + 1], std::is_same_v<T, __half> ? CONV_FLOAT16 : CONV_BFLOAT16);
+        else w[j] = __float_as_uint(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[kWords + j] = __shfl_down_sync(0xffffffffu, w[j], 1);
+    const int c = at.column(i, 0), lane = threadIdx.x % 32;
+    const bool whole = (lane < 31 || b == 0) && c + b >= 0 && c + b + 8 <= at.cols;
+    // elements that no aligned group has: before the boundary where the previous lane cannot take them, behind it
+    // where this one cannot
+    const bool first = lane == 0 || c + b - 8 < 0 || c + b > at.cols;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (at.inside(c + j) && (j < b ? first : !whole)) {
+            if constexpr (kIs16<T>) reinterpret_cast<uint16_t *>(p)[c + j] = (uint16_t)(w[j / 2] >> (j % 2 * 16));
+            else p[c + j] = __uint_as_float(w[j]);
+        }
+    if constexpr (kIs16<T>) {
+        if (b & 4) {
+#pragma unroll
+            for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+        }
+        if (b & 2) {
+#pragma unroll
+            for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], (b & 1) * 16);
+    } else {
+#pragma unroll
+        for (int s = 4; s > 0; s >>= 1)
+            if (b & s) {
+#pragma unroll
+                for (int j = 0; j < 7 + s; ++j)
+                    if (j + s < 16) w[j] = w[j + s];
+            }
+    }
+    if (whole) {
+        uint4 *o = reinterpret_cast<uint4 *>(p + c + b);
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (!kIs16<T>) o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 template <bool kWarp>
 __device__ __forceinline__ void row_sync() {
     if constexpr (kWarp) __syncwarp();
@@ -310,26 +364,36 @@ __device__ __forceinline__ void read_group(uint32_t slot, uint32_t stride, Group
 // elements.  A row lies in its slot as it does past a boundary of 8 elements.
 struct RowFeed {
     const char *p, *end;   // the matrix's memory
-    int64_t row_bytes;     // from one row to the next
+    const char *next;      // the row to come
+    int64_t step;          // bytes from it to the one after
     uint32_t bytes;        // of a row
     uint32_t off;          // of the matrix's slot in a stage
     uint32_t half;         // 16 where a boundary of 16 bytes may not be one of 8 elements
     bool on;
 
-    __device__ __forceinline__ void set(const MatRef &m, int64_t rows, int32_t cols, uint32_t size, uint32_t at) {
+    __device__ __forceinline__ void set(const MatRef &m, int64_t rows, int32_t cols, uint32_t size, uint32_t at, int64_t first, int64_t row_step) {
         p = (const char *)m.p;
-        row_bytes = m.rs * size;
         bytes = (uint32_t)cols * size;
-        end = p + (rows - 1) * row_bytes + bytes;
+        end = p + (rows - 1) * m.rs * size + bytes;
+        next = p + first * m.rs * size;
+        step = row_step * m.rs * size;
         off = at;
         half = size == 4 ? 16 : 0;
         on = true;
     }
-    // One arrival on `bar` and the row's bytes.
-    __device__ __forceinline__ void fill(int64_t r, uint32_t stage, uint32_t bar) const {
-        if (!on) return;
-        const char *s = p + r * row_bytes, *e = s + bytes;
-        stage += (uint32_t)(uintptr_t)s & half;
+    // One arrival on `bar` and the next row's bytes.  kEven: rows of whole, aligned groups.
+    template <bool kEven>
+    __device__ __forceinline__ void fill(uint32_t stage, uint32_t bar) {
+        const char *s = next, *e = s + bytes;
+        next += step;
+        if constexpr (kEven) {
+            ptx::mbar_arrive_expect_tx(bar, bytes);
+            ptx::bulk_copy_g2s(stage + off, s, bytes, bar);
+        } else {
+            fill_any(s, e, stage + ((uint32_t)(uintptr_t)s & half), bar);
+        }
+    }
+    __device__ __forceinline__ void fill_any(const char *s, const char *e, uint32_t stage, uint32_t bar) const {
         const char *s0 = s - ((uintptr_t)s & 15), *e0 = e + (-(uintptr_t)e & 15);
         if (s0 >= p && e0 <= end) {
             ptx::mbar_arrive_expect_tx(bar, (uint32_t)(e0 - s0));
@@ -358,6 +422,26 @@ __host__ __device__ constexpr uint32_t row_slot_bytes(int32_t cols, uint32_t siz
     return ((uint32_t)cols + 7) / 8 * 8 * size + 8 * size;
 }
 
+// Sum of one value over the block (at most 32 warps), the same in every thread
+// and in the same order in all of them, with one barrier: consecutive sums use
+// the two buffers in turn, and no warp can be two sums ahead.
+struct RowSummer {
+    float (*part)[32];
+    int turn = 0;
+    __device__ __forceinline__ float operator()(float u) {
+        u = warp_sum(u);
+        float *p = part[turn];
+        turn ^= 1;
+        if (threadIdx.x % 32 == 0) p[threadIdx.x / 32] = u;
+        __syncthreads();
+        const int warps = blockDim.x / 32;
+        float t = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < warps; ++i) t += p[i];
+        return t;
+    }
+};
+
 // Waits for a row, not for ever: a thread that has given up once (the status
 // word then says so) does not wait again.
 struct RowWait {
@@ -377,12 +461,12 @@ struct RowWait {
     }
 };
 
-// Group i of a row in its slot; zeros outside the row.  kEven: rows of whole
+// Group i of a row in its slot; zeros outside the row, and where there is no matrix.  kEven: rows of whole
 // groups.
 template <bool kEven, typename X>
-__device__ __forceinline__ void slot_group(uint32_t slot, const Place<true> &at, int i, Group<X> &g) {
+__device__ __forceinline__ void slot_group(uint32_t slot, const Place<true> &at, int i, Group<X> &g, bool there = true) {
     const uint32_t from = slot + (uint32_t)(i * at.threads + at.t) * (uint32_t)(8 * sizeof(X));
-    if (kEven ? at.inside(at.column(i, 0)) : at.whole(i)) {
+    if (there && (kEven ? at.inside(at.column(i, 0)) : at.whole(i))) {
         const uint4 a = ptx::ld_shared_v4(from);
         g.w[0] = a.x, g.w[1] = a.y, g.w[2] = a.z, g.w[3] = a.w;
         if constexpr (!kIs16<X>) {
@@ -397,7 +481,7 @@ __device__ __forceinline__ void slot_group(uint32_t slot, const Place<true> &at,
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const bool in = at.inside(at.column(i, j));
+            const bool in = there && at.inside(at.column(i, j));
             if constexpr (kIs16<X>) {
                 uint16_t v = 0;
                 if (in) asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(from + j * 2));
