@@ -33,8 +33,9 @@ constexpr int kMaxTileB = 256;
 constexpr int kMaxStages = 8;
 constexpr int kSumWarps = 8;       // two to a quarter of the lanes, each half the columns
 constexpr int kThreads = 128 + 32 * kSumWarps;
-constexpr int kScaleSlots = 8;     // blocks whose scales are on their way
-constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;
+constexpr int kBatch = 4;          // blocks whose scales come together
+constexpr int kScaleSlots = 2;     // batches on their way
+constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;  // of a block
 constexpr int kBiasBytes = kSumWarps * 128;
 constexpr int kRingBytes = 196608;
 // registers: 384 threads start with 168 each; the summing warps' 128 sums, 64
@@ -96,12 +97,17 @@ __device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// wait_phase without a call: the summing warps have no registers to put away.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag, uint64_t limit_ns,
-                                            int *status) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+// A bounded wait without a call (the summing warps have no registers to put
+// away) that polls: a suspended thread resumes some time after its phase is
+// complete, and here every block of k waits for the one before.
+__device__ __forceinline__ bool wait_polling(uint32_t bar, uint32_t parity, volatile int32_t *abort_flag, uint64_t limit_ns,
+                                             int *status) {
+    if (ptx::mbar_test_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::global_timer_ns();
-    while (!ptx::mbar_try_wait(bar, parity)) {
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (ptx::mbar_test_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (ptx::global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
@@ -109,7 +115,11 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volat
             return false;
         }
     }
-    return true;
+}
+
+// sum += {lo, hi} * s
+__device__ __forceinline__ void add_scaled(Pair &sum, uint32_t lo, uint32_t hi, Pair s) {
+    asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(sum.v) : "r"(lo), "r"(hi), "l"(s.v));
 }
 
 // kPair: two CTAs of a cluster work on one tile of 256 x 2 kCols
@@ -124,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
     const uint32_t ring = ptx::smem_addr(smem);
     const uint32_t staging = ring + a.stages * a.stage_bytes;
     const uint32_t scales = staging + kSumWarps * kSlotBytes;
-    const uint32_t bias_smem = scales + kScaleSlots * kScaleBytes;
+    const uint32_t bias_smem = scales + kScaleSlots * kBatch * kScaleBytes;
     SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + (bias_smem - ring) + kBiasBytes);
     if (ring & 1023) {  // the swizzles count on it (true of every launch without static shared memory)
         if (threadIdx.x == 0) atomicExch(a.status, (int)CONV_ERR_ALIGNMENT);
@@ -233,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                 run_of(t);
                 for (int kb = k_lo; kb < k_hi; ++kb, ++n) {
                     const uint32_t slot = n & 1;
-                    if (!wait_phase(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status) ||
-                        !wait_phase(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
+                    if (!wait_polling(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status) ||
+                        !wait_polling(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
                         ok = false;
                         break;
                     }
@@ -270,17 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     in_b[i] = r < a.sb.rows && (kPerColumn || lane < 2);
                     pb[i] = a.sb.p + (in_b[i] ? (int64_t)(r >> a.sb.shift) * a.sb.rs : 0);
                 }
-                for (int kb = k_lo; kb < k_hi; ++kb) {
+                for (int kb = k_lo; kb < k_hi; kb += kBatch) {
                     if (!wait_phase(ptx::smem_addr(&ctl->scale_empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t to = scales + rg.idx * kScaleBytes + lane * 4;
+                    const uint32_t to = scales + rg.idx * kBatch * kScaleBytes + lane * 4;
 #pragma unroll
-                    for (int i = 0; i < kTileA / 32; ++i) copy_async4(to + i * 128, pa[i] + kb * a.sa.cs, in_a[i]);
+                    for (int q = 0; q < kBatch; ++q) {
+                        if (kb + q >= k_hi) break;
 #pragma unroll
-                    for (int i = 0; i < (kPerColumn ? kTileB / 32 : 1); ++i)
-                        if (kPerColumn || lane < 2) copy_async4(to + kTileA * 4 + i * 128, pb[i] + kb * a.sb.cs, in_b[i]);
+                        for (int i = 0; i < kTileA / 32; ++i) copy_async4(to + q * kScaleBytes + i * 128, pa[i] + (kb + q) * a.sa.cs, in_a[i]);
+#pragma unroll
+                        for (int i = 0; i < (kPerColumn ? kTileB / 32 : 1); ++i)
+                            if (kPerColumn || lane < 2)
+                                copy_async4(to + q * kScaleBytes + kTileA * 4 + i * 128, pb[i] + (kb + q) * a.sb.cs, in_b[i]);
+                    }
                     arrive_behind_copies(ptx::smem_addr(&ctl->scale_full[rg.idx]));
                     rg.next(kScaleSlots);
                 }
@@ -304,50 +319,55 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             Pair sum[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) sum[j] = pair(0.0f);
-            for (int kb = k_lo; kb < k_hi; ++kb, ++n) {
-                const uint32_t slot = n & 1, at = scales + sr.idx * kScaleBytes;
-                if (!wait_inline(ptx::smem_addr(&ctl->scale_full[sr.idx]), sr.phase, abort_flag, a.wait_limit_ns, a.status)) {
+            for (int k0 = k_lo; k0 < k_hi && ok; k0 += kBatch) {
+                // a batch's scales: of the row, and with it the columns' where they have one
+                const uint32_t at = scales + sr.idx * kBatch * kScaleBytes;
+                if (!wait_polling(ptx::smem_addr(&ctl->scale_full[sr.idx]), sr.phase, abort_flag, a.wait_limit_ns, a.status)) {
                     ok = false;
                     break;
                 }
-                float s = __uint_as_float(ptx::ld_shared_b32(at + (quad * 32 + lane) * 4));
-                if constexpr (!kPerColumn) s *= __uint_as_float(ptx::ld_shared_b32(at + (kTileA + part) * 4));
-                if (!wait_inline(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t acc = tmem + slot * kMaxTileB + part * kCols + ((uint32_t)(quad * 32) << 16);
-                const Pair s2 = pair(s);
-                uint32_t u[2][32];
-                ptx::tmem_ld_32x32b_x32(acc, u[0]);
-#pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    ptx::tmem_ld_wait();
-                    if (c + 1 < kCols / 32) {
-                        ptx::tmem_ld_32x32b_x32(acc + (c + 1) * 32, u[(c + 1) & 1]);
-                    } else {
-                        // everything of this accumulator is in registers
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
-                            mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
-                        }
+                const int k1 = min(k_hi, k0 + kBatch);
+#pragma unroll 1
+                for (int kb = k0; kb < k1; ++kb, ++n) {
+                    const uint32_t slot = n & 1, mine = at + (kb - k0) * kScaleBytes;
+                    float s = __uint_as_float(ptx::ld_shared_b32(mine + (quad * 32 + lane) * 4));
+                    if constexpr (!kPerColumn) s *= __uint_as_float(ptx::ld_shared_b32(mine + (kTileA + part) * 4));
+                    if (!wait_polling(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) {
+                        ok = false;
+                        break;
                     }
+                    ptx::tc_fence_after();
+                    const uint32_t acc = tmem + slot * kMaxTileB + part * kCols + ((uint32_t)(quad * 32) << 16);
+                    const Pair s2 = pair(s);
+                    uint32_t u[2][16];
+                    ptx::tmem_ld_32x32b_x16(acc, u[0]);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        Pair p = pair(__uint_as_float(u[c & 1][j]), __uint_as_float(u[c & 1][j + 1]));
-                        Pair q = pair(__uint_as_float(u[c & 1][j + 2]), __uint_as_float(u[c & 1][j + 3]));
-                        if constexpr (kPerColumn) {
-                            // (the row's scale times the column's first, as with one scale for the columns)
-                            const uint4 b = ptx::ld_shared_v4(at + (kTileA + part * kCols + c * 32 + j) * 4);
-                            sum[(c * 32 + j) / 2] = fma2(p, mul2(s2, pair(__uint_as_float(b.x), __uint_as_float(b.y))), sum[(c * 32 + j) / 2]);
-                            sum[(c * 32 + j) / 2 + 1] =
-                                fma2(q, mul2(s2, pair(__uint_as_float(b.z), __uint_as_float(b.w))), sum[(c * 32 + j) / 2 + 1]);
+                    for (int c = 0; c < kCols / 16; ++c) {
+                        ptx::tmem_ld_wait();
+                        if (c + 1 < kCols / 16) {
+                            ptx::tmem_ld_32x32b_x16(acc + (c + 1) * 16, u[(c + 1) & 1]);
                         } else {
-                            sum[(c * 32 + j) / 2] = fma2(p, s2, sum[(c * 32 + j) / 2]);
-                            sum[(c * 32 + j) / 2 + 1] = fma2(q, s2, sum[(c * 32 + j) / 2 + 1]);
+                            // everything of this accumulator is in registers
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
+                                mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            Pair &lo = sum[(c * 16 + j) / 2], &hi = sum[(c * 16 + j) / 2 + 1];
+                            const uint32_t *const from = u[c & 1] + j;
+                            if constexpr (kPerColumn) {
+                                // (the row's scale times the column's first, as with one scale for the columns)
+                                const uint4 b = ptx::ld_shared_v4(mine + (kTileA + part * kCols + c * 16 + j) * 4);
+                                add_scaled(lo, from[0], from[1], mul2(s2, pair(__uint_as_float(b.x), __uint_as_float(b.y))));
+                                add_scaled(hi, from[2], from[3], mul2(s2, pair(__uint_as_float(b.z), __uint_as_float(b.w))));
+                            } else {
+                                add_scaled(lo, from[0], from[1], s2);
+                                add_scaled(hi, from[2], from[3], s2);
+                            }
                         }
                     }
                 }
@@ -496,7 +516,7 @@ conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *str
     }
     const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
     const int cluster = pair ? 2 : 1;
-    const size_t smem = (size_t)a.stages * a.stage_bytes + kSumWarps * kSlotBytes + kScaleSlots * kScaleBytes + kBiasBytes + sizeof(SharedCtl);
+    const size_t smem = (size_t)a.stages * a.stage_bytes + kSumWarps * kSlotBytes + kScaleSlots * kBatch * kScaleBytes + kBiasBytes + sizeof(SharedCtl);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, device_sm_count() / cluster) * cluster));
     cfg.blockDim = dim3(kThreads);
