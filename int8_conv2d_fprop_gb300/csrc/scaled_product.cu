@@ -69,6 +69,13 @@ struct SharedCtl {
     int32_t abort_flag;
 };
 
+// True in one thread of the warp, whose threads are all here.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 template <bool kPair>
 __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     if constexpr (kPair) {
@@ -234,8 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                 while (!ptx::mbar_try_wait(bar, (uint32_t)((n - 1) & 1)))
                     if (ptx::global_timer_ns() - t0 > 10000000) break;
             }
-        } else if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
+        } else if (warp == 1 && (!kPair || rank == 0)) {
             // ------------------------------------------------ MMA: a block of k to an accumulator
+            // (The whole warp walks, one thread issues: descriptors that are
+            // uniform over a warp stay in uniform registers.  In a branch of one
+            // thread, four MMAs with their commit took 770 cycles to issue
+            // instead of the 513 that the tensor cores need for them.)
+            const bool issues = elect_one();
             Ring rg;
             uint32_t n = 0;
             bool ok = true;
@@ -251,10 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     ptx::tc_fence_after();
                     const uint32_t at = ring + rg.idx * a.stage_bytes, d = tmem + slot * kMaxTileB;
                     const uint64_t da = ptx::smem_desc_sw128(at), db = ptx::smem_desc_sw128(at + 16384);
+                    if (issues) {
 #pragma unroll
-                    for (int i = 0; i < kBlockK / 32; ++i) mma8<kPair>(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
-                    mma_commit<kPair>(ptx::smem_addr(&ctl->empty[rg.idx]));
-                    mma_commit<kPair>(ptx::smem_addr(&ctl->acc_full[slot]));
+                        for (int i = 0; i < kBlockK / 32; ++i) mma8<kPair>(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
+                        mma_commit<kPair>(ptx::smem_addr(&ctl->acc_full[slot]));
+                        mma_commit<kPair>(ptx::smem_addr(&ctl->empty[rg.idx]));
+                    }
+                    __syncwarp();
                     rg.next(a.stages);
                 }
             }
