@@ -54,7 +54,7 @@ struct ScaledArgs : TileArgs {
     CUtensorMap map_a, map_b;
     ScaleArgs sa, sb;
     int32_t blocks;              // of k
-    int32_t b_rows;              // rows of B per CTA
+    int32_t b_rows;              // rows of B that a CTA loads
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     uint32_t idesc;
     uint64_t wait_limit_ns;
@@ -76,23 +76,29 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-template <bool kPair>
 __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (kPair) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` of both CTAs of the cluster when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_to_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// 2-D load to the same place of both CTAs of the cluster, counted on the same barrier of each.
+__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+        : "memory");
 }
 
 // Four bytes to shared memory, zeros where there is nothing to read.
@@ -129,9 +135,10 @@ __device__ __forceinline__ void add_scaled(Pair &sum, uint32_t lo, uint32_t hi, 
     asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(sum.v) : "r"(lo), "r"(hi), "l"(s.v));
 }
 
-// kPair: two CTAs of a cluster work on one tile of 256 x 2 kCols
-// (cta_group::2: each holds its 128 rows of A and half the rows of B, the
-// first one issues the MMAs for both), else one CTA on 128 x 2 kCols.
+// kPair: two CTAs of a cluster work on one tile of 256 x 2 kCols, each on its
+// own 128 rows; each loads half the rows of B for both.  (As one MMA of both
+// CTAs, cta_group::2, every block's accumulator went back and forth between
+// them: 1080 cycles per block instead of 800.)  Else one CTA on 128 x 2 kCols.
 // kPerColumn: B has a scale for each row, else one for the 128 that a summing
 // warp's columns lie in.
 template <bool kPair, int kCols, bool kPerColumn>
@@ -173,11 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
         ptx::prefetch_tensormap(&a.map_a);
         for (int i = 0; i < a.stages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
-            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), kCluster);  // the MMAs of every CTA that the stage's loads reach
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->acc_full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&ctl->acc_empty[i]), kCluster * kSumWarps);
+            ptx::mbar_init(ptx::smem_addr(&ctl->acc_empty[i]), kSumWarps);
         }
         for (int i = 0; i < kScaleSlots; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->scale_full[i]), 32);
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
         ptx::prefetch_tensormap(&a.map_b);
     }
     __syncthreads();
-    if (warp == 2) tmem_alloc<kPair>(ptx::smem_addr(&ctl->tmem_base), 512);
+    if (warp == 2) tmem_alloc<false>(ptx::smem_addr(&ctl->tmem_base), 512);
     ptx::tc_fence_before();
     if (kPair) cluster_sync();
     else __syncthreads();
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             // ------------------------------------------------ loads: operand A by warp 0, operand B by warp 3
             const bool is_b = warp == 3;
             const CUtensorMap *map = is_b ? &a.map_b : &a.map_a;
-            const uint32_t bytes = (uint32_t)kCluster * (is_b ? a.b_rows : kTileA) * kBlockK;
+            const uint32_t bytes = (is_b ? kTileB : kTileA) * kBlockK;
             Ring rg;
             int64_t issued = 0;
             bool ok = true;
@@ -218,21 +225,20 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                         ok = false;
                         break;
                     }
-                    uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]);
-                    if (!kPair || rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
-                    if (kPair) bar = map_to_rank(bar, 0);
-                    const uint32_t dst = ring + rg.idx * a.stage_bytes + (is_b ? 16384 : 0);
-                    if constexpr (kPair) tma_load_2d_pair(dst, map, kb * kBlockK, own, bar);
-                    else ptx::tma_load_2d(dst, map, kb * kBlockK, own, bar);
+                    const uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]), dst = ring + rg.idx * a.stage_bytes;
+                    ptx::mbar_arrive_expect_tx(bar, bytes);
+                    if (!is_b) ptx::tma_load_2d(dst, map, kb * kBlockK, own, bar);
+                    else if constexpr (kPair) tma_load_2d_both(dst + 16384 + rank * a.b_rows * kBlockK, map, kb * kBlockK, own, bar);
+                    else ptx::tma_load_2d(dst + 16384, map, kb * kBlockK, own, bar);
                     ++issued;
                     rg.next(a.stages);
                 }
             }
             // Every stage is released by the MMAs that read it; the releases
             // reach both CTAs of a pair, so they have to be in before either
-            // leaves.  After a time-out the copies have to land first, and no
-            // release may come.
-            const bool drain_copies = *abort_flag && (!kPair || rank == 0);
+            // leaves.  After a time-out the copies have to land first (the
+            // other CTA's too), and no release may come.
+            const bool drain_copies = *abort_flag;
             for (int s = 0; s < a.stages && (kPair || drain_copies); ++s) {
                 const int64_t n = issued / a.stages + (s < issued % a.stages ? 1 : 0);
                 if (n == 0) continue;
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                 while (!ptx::mbar_try_wait(bar, (uint32_t)((n - 1) & 1)))
                     if (ptx::global_timer_ns() - t0 > 10000000) break;
             }
-        } else if (warp == 1 && (!kPair || rank == 0)) {
+        } else if (warp == 1) {
             // ------------------------------------------------ MMA: a block of k to an accumulator
             // (The whole warp walks, one thread issues: descriptors that are
             // uniform over a warp stay in uniform registers.  In a branch of one
@@ -265,9 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     const uint64_t da = ptx::smem_desc_sw128(at), db = ptx::smem_desc_sw128(at + 16384);
                     if (issues) {
 #pragma unroll
-                        for (int i = 0; i < kBlockK / 32; ++i) mma8<kPair>(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
-                        mma_commit<kPair>(ptx::smem_addr(&ctl->acc_full[slot]));
-                        mma_commit<kPair>(ptx::smem_addr(&ctl->empty[rg.idx]));
+                        for (int i = 0; i < kBlockK / 32; ++i) mma8(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
+                        ptx::mma_commit(ptx::smem_addr(&ctl->acc_full[slot]));
+                        if constexpr (kPair) commit_to_both(ptx::smem_addr(&ctl->empty[rg.idx]));
+                        else ptx::mma_commit(ptx::smem_addr(&ctl->empty[rg.idx]));
                     }
                     __syncwarp();
                     rg.next(a.stages);
@@ -365,10 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                             // everything of this accumulator is in registers
                             ptx::tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) {
-                                const uint32_t bar = ptx::smem_addr(&ctl->acc_empty[slot]);
-                                mbar_arrive_relaxed(kPair ? map_to_rank(bar, 0) : bar);
-                            }
+                            if (lane == 0) mbar_arrive_relaxed(ptx::smem_addr(&ctl->acc_empty[slot]));
                         }
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
     if (kPair) cluster_sync();
     else __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 2) tmem_dealloc<kPair>(tmem, 512);
+    if (warp == 2) tmem_dealloc<false>(tmem, 512);
 }
 
 __global__ void __launch_bounds__(256) scaled_join_kernel(const __grid_constant__ ScaledArgs a, int rows_per_tile) {
@@ -495,11 +499,11 @@ conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *str
     a.tile_b = pl.tile_b, a.tiles_a = (int32_t)pl.tiles_a, a.tiles_b = (int32_t)pl.tiles_b;
     a.parts = pl.parts, a.full = (int32_t)pl.full, a.part = (float *)workspace;
     a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
-    a.stage_bytes = 16384 + a.b_rows * kBlockK;
+    a.stage_bytes = 16384 + a.tile_b * kBlockK;
     a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
     const int tile_a = pair ? 256 : 128;
     a.idesc = (1u << 4) | ((pr.a.e5m2 ? 1u : 0u) << 7) | ((pr.b.e5m2 ? 1u : 0u) << 10) | ((uint32_t)(a.tile_b >> 3) << 17) |
-              ((uint32_t)(tile_a >> 4) << 24);
+              ((uint32_t)(kTileA >> 4) << 24);
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     if (!encode(&a.map_a, CONV_FLOAT8_E4M3, pr.a.p, pr.k, pr.ma, pr.a.rs, kBlockK, kTileA, sw) ||
         !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.b_rows, sw))
