@@ -135,7 +135,6 @@ struct ScaledProduct {
 // part_bytes of workspace hold its partial sums.
 struct ScaledPlan {
     bool swap = false;     // a and b exchanged
-    bool pair = false;     // tiles of CTA pairs (256 rows), else of one CTA (128)
     int32_t tile_b = 0;
     int64_t tiles_a = 0, tiles_b = 0;
     int32_t parts = 1;     // runs of k, summed apart and joined by a second kernel, ...

@@ -244,8 +244,11 @@ __device__ __forceinline__ void activate_all(const EpilogueArgs &a, float (&v)[W
 // and pre-activation is turned: rows of 64 bytes (32 columns of a 16-bit
 // matrix, 16 of a 32-bit one), each lane writing or reading its own row, and
 // runs of a row going to or from global memory.
+//
+// kSlots slots in turn: as many stores may be under way.
 struct WarpTile {
     int32_t row0, b0, rows, cols;  // rows, cols: how many are inside the matrix and the tile
+    mutable int32_t turn = 0;      // of the slots
     uint32_t slot, bias;           // bias: 128 bytes of shared memory
     int lane;
 };
@@ -398,11 +401,23 @@ __device__ __forceinline__ void free_slot(const WarpTile &t) {
     if (t.lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
 }
+// ... of the next slot in turn, which t then has.
+template <int kSlots>
+__device__ __forceinline__ void next_slot(WarpTile &t, const WarpTile &given) {
+    if (t.lane == 0) ptx::bulk_wait_group_read<kSlots - 1>();
+    __syncwarp();
+    if constexpr (kSlots > 1) {
+        t.slot = given.slot + given.turn * kSlotBytes;
+        given.turn = given.turn + 1 == kSlots ? 0 : given.turn + 1;
+    }
+}
 
-__device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *map, const WarpTile &t, const float (&v)[32]) {
+template <int kSlots = 1>
+__device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *map, const WarpTile &given, const float (&v)[32]) {
+    WarpTile t = given;
     const bool rows = s.walk == kWalkRows && t.cols == 32;
     if (s.dtype != CONV_FLOAT32) {
-        free_slot(t);
+        next_slot<kSlots>(t, given);
         if (s.dtype == CONV_FLOAT16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) ptx::st_shared_v4(piece(t.slot, t.lane, i), pack8<true>(v + 8 * i));
@@ -423,7 +438,7 @@ __device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *ma
     }
 #pragma unroll
     for (int c = 0; c < 32; c += 16) {
-        free_slot(t);
+        next_slot<kSlots>(t, given);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             ptx::st_shared_v4(piece(t.slot, t.lane, i),
@@ -525,10 +540,10 @@ __device__ __forceinline__ void fetch_residual(const EpilogueArgs &a, const Warp
 
 // 32 rows x 32 columns of sums; next: the columns from this chunk to the warp's
 // next one in the tile, 0 at the last.
-template <int kAct>
+template <int kAct, int kSlots = 1>
 __device__ __forceinline__ void finish_values(const EpilogueArgs &a, const WarpTile &t, float (&v)[32], float bias, int next) {
     add_bias(a, t, bias, v);
-    if (a.pre.walk) store_chunk(a.pre, &a.map_pre, t, v);
+    if (a.pre.walk) store_chunk<kSlots>(a.pre, &a.map_pre, t, v);
     activate_all<kAct>(a, v);
     if (a.slots == 2 && t.cols == 32) {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -545,7 +560,7 @@ __device__ __forceinline__ void finish_values(const EpilogueArgs &a, const WarpT
     } else if (a.res.walk) {
         add_chunk(a.res, t, v);
     }
-    store_chunk(a.d, &a.map_d, t, v);
+    store_chunk<kSlots>(a.d, &a.map_d, t, v);
 }
 
 // ... of those at `acc` in tensor memory.

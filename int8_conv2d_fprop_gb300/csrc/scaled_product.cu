@@ -37,7 +37,8 @@ constexpr int kBatch = 4;          // blocks whose scales come together
 constexpr int kScaleSlots = 2;     // batches on their way
 constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;  // of a block
 constexpr int kBiasBytes = kSumWarps * 128;
-constexpr int kRingBytes = 196608;
+constexpr int kSlots = 4;          // staging slots of a summing warp: its columns of a tile, all on their way at once
+constexpr int kRingBytes = 147456;
 // registers: 384 threads start with 168 each; the summing warps' 128 sums, 64
 // values on their way and the rest of their state take up to 224
 constexpr int kControlRegs = 48, kSumRegs = 224, kLaunchRegs = 168;
@@ -54,7 +55,6 @@ struct ScaledArgs : TileArgs {
     CUtensorMap map_a, map_b;
     ScaleArgs sa, sb;
     int32_t blocks;              // of k
-    int32_t b_rows;              // rows of B that a CTA loads
     int32_t stages, stage_bytes; // A is the first 16 KB of a stage
     uint32_t idesc;
     uint64_t wait_limit_ns;
@@ -82,22 +82,6 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Arrives on `bar` of both CTAs of the cluster when the MMAs issued so far are done.
-__device__ __forceinline__ void commit_to_both(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
-// 2-D load to the same place of both CTAs of the cluster, counted on the same barrier of each.
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
         : "memory");
 }
 
@@ -135,19 +119,16 @@ __device__ __forceinline__ void add_scaled(Pair &sum, uint32_t lo, uint32_t hi, 
     asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(sum.v) : "r"(lo), "r"(hi), "l"(s.v));
 }
 
-// kPair: two CTAs of a cluster work on one tile of 256 x 2 kCols, each on its
-// own 128 rows; each loads half the rows of B for both.  (As one MMA of both
-// CTAs, cta_group::2, every block's accumulator went back and forth between
-// them: 1080 cycles per block instead of 800.)  Else one CTA on 128 x 2 kCols.
+// One CTA works on a tile of 128 x 2 kCols.
 // kPerColumn: B has a scale for each row, else one for the 128 that a summing
 // warp's columns lie in.
-template <bool kPair, int kCols, bool kPerColumn>
+template <int kCols, bool kPerColumn>
 __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __grid_constant__ ScaledArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int kTileB = 2 * kCols;
     const uint32_t ring = ptx::smem_addr(smem);
     const uint32_t staging = ring + a.stages * a.stage_bytes;
-    const uint32_t scales = staging + kSumWarps * kSlotBytes;
+    const uint32_t scales = staging + kSumWarps * kSlots * kSlotBytes;
     const uint32_t bias_smem = scales + kScaleSlots * kBatch * kScaleBytes;
     SharedCtl *ctl = reinterpret_cast<SharedCtl *>(smem + (bias_smem - ring) + kBiasBytes);
     if (ring & 1023) {  // the swizzles count on it (true of every launch without static shared memory)
@@ -156,9 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
     }
     volatile int32_t *abort_flag = &ctl->abort_flag;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = kPair ? cluster_rank() : 0;
-    constexpr int kCluster = kPair ? 2 : 1, kRowsA = kPair ? 256 : 128;
-    const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
+    const int first = blockIdx.x, step = gridDim.x;
     const int tiles = a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
 
     // unit u: a whole tile, then the runs of the cut tiles; sets the blocks of k, returns the tile
@@ -180,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
         ptx::prefetch_tensormap(&a.map_a);
         for (int i = 0; i < a.stages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
-            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), kCluster);  // the MMAs of every CTA that the stage's loads reach
+            ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->acc_full[i]), 1);
@@ -198,8 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
     __syncthreads();
     if (warp == 2) tmem_alloc<false>(ptx::smem_addr(&ctl->tmem_base), 512);
     ptx::tc_fence_before();
-    if (kPair) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)&ctl->tmem_base;
     // Nothing above reads or writes global memory.
@@ -219,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             for (int t = first; t < units && ok; t += step) {
                 int ia, ib;
                 tile_at(a, run_of(t), &ia, &ib);
-                const int own = is_b ? ib * kTileB + (kPair ? rank * a.b_rows : 0) : ia * kRowsA + (kPair ? rank * kTileA : 0);
+                const int own = is_b ? ib * kTileB : ia * kTileA;
                 for (int kb = k_lo; kb < k_hi; ++kb) {
                     if (!wait_phase(ptx::smem_addr(&ctl->empty[rg.idx]), rg.phase ^ 1u, abort_flag, a.wait_limit_ns, a.status)) {
                         ok = false;
@@ -227,22 +205,17 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     }
                     const uint32_t bar = ptx::smem_addr(&ctl->full[rg.idx]), dst = ring + rg.idx * a.stage_bytes;
                     ptx::mbar_arrive_expect_tx(bar, bytes);
-                    if (!is_b) ptx::tma_load_2d(dst, map, kb * kBlockK, own, bar);
-                    else if constexpr (kPair) tma_load_2d_both(dst + 16384 + rank * a.b_rows * kBlockK, map, kb * kBlockK, own, bar);
-                    else ptx::tma_load_2d(dst + 16384, map, kb * kBlockK, own, bar);
+                    ptx::tma_load_2d(dst + (is_b ? 16384 : 0), map, kb * kBlockK, own, bar);
                     ++issued;
                     rg.next(a.stages);
                 }
             }
-            // Every stage is released by the MMAs that read it; the releases
-            // reach both CTAs of a pair, so they have to be in before either
-            // leaves.  After a time-out the copies have to land first (the
-            // other CTA's too), and no release may come.
-            const bool drain_copies = *abort_flag;
-            for (int s = 0; s < a.stages && (kPair || drain_copies); ++s) {
+            // (every stage's release is in before the last accumulator is)
+            // After a time-out the copies have to land first.
+            for (int s = 0; s < a.stages && *abort_flag; ++s) {
                 const int64_t n = issued / a.stages + (s < issued % a.stages ? 1 : 0);
                 if (n == 0) continue;
-                const uint32_t bar = ptx::smem_addr(drain_copies ? &ctl->full[s] : &ctl->empty[s]);
+                const uint32_t bar = ptx::smem_addr(&ctl->full[s]);
                 const uint64_t t0 = ptx::global_timer_ns();
                 while (!ptx::mbar_try_wait(bar, (uint32_t)((n - 1) & 1)))
                     if (ptx::global_timer_ns() - t0 > 10000000) break;
@@ -273,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
 #pragma unroll
                         for (int i = 0; i < kBlockK / 32; ++i) mma8(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
                         ptx::mma_commit(ptx::smem_addr(&ctl->acc_full[slot]));
-                        if constexpr (kPair) commit_to_both(ptx::smem_addr(&ctl->empty[rg.idx]));
-                        else ptx::mma_commit(ptx::smem_addr(&ctl->empty[rg.idx]));
+                        ptx::mma_commit(ptx::smem_addr(&ctl->empty[rg.idx]));
                     }
                     __syncwarp();
                     rg.next(a.stages);
@@ -287,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             for (int t = first; t < units && ok; t += step) {
                 int ia, ib;
                 tile_at(a, run_of(t), &ia, &ib);
-                const int row0 = ia * kRowsA + (kPair ? (int)rank * kTileA : 0), col0 = ib * kTileB;
+                const int row0 = ia * kTileA, col0 = ib * kTileB;
                 const float *pa[kTileA / 32], *pb[kPerColumn ? kTileB / 32 : 1];
                 bool in_a[kTileA / 32], in_b[kPerColumn ? kTileB / 32 : 1];
 #pragma unroll
@@ -330,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
         const int e = warp - 4, quad = warp & 3, part = e >> 2;
         WarpTile wt;
         wt.lane = lane;
-        wt.slot = staging + e * kSlotBytes;
+        wt.slot = staging + e * kSlots * kSlotBytes;
         wt.bias = bias_smem + e * 128;
         Ring sr;
         uint32_t n = 0;
@@ -370,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                             ptx::tmem_ld_32x32b_x16(acc + (c + 1) * 16, u[(c + 1) & 1]);
                         } else {
                             // everything of this accumulator is in registers
+                            // (of all lanes: the wait is the warp's)
                             ptx::tc_fence_before();
-                            __syncwarp();
                             if (lane == 0) mbar_arrive_relaxed(ptx::smem_addr(&ctl->acc_empty[slot]));
                         }
 #pragma unroll
@@ -391,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     }
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl->scale_empty[sr.idx]));
+                if (lane == 0) mbar_arrive_relaxed(ptx::smem_addr(&ctl->scale_empty[sr.idx]));  // (read, and nothing written)
                 sr.next(kScaleSlots);
             }
             if (!ok) break;
-            wt.row0 = ia * kRowsA + (kPair ? rank * kTileA : 0) + quad * 32;
+            wt.row0 = ia * kTileA + quad * 32;
             wt.rows = min(32, a.ma - wt.row0);
             // (the sums move down 32 columns at a time, so that the finishing code is there once)
 #pragma unroll 1
@@ -411,20 +383,19 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                 wt.cols = min(32, a.nb - wt.b0);
                 if (wt.rows <= 0 || wt.cols <= 0) continue;
                 if (t >= a.full) {
-                    float *p = a.part + (((int64_t)(t - a.full) * kCluster + rank) * kTileB + c) * kTileA + quad * 32 + lane;
+                    float *p = a.part + ((int64_t)(t - a.full) * kTileB + c) * kTileA + quad * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) p[j * kTileA] = v[j];
                     continue;
                 }
-                finish_values<kAnyAct>(a, wt, v, lane_bias(a, wt.row0, wt.b0, lane), 0);
+                finish_values<kAnyAct, kSlots>(a, wt, v, lane_bias(a, wt.row0, wt.b0, lane), 0);
             }
         }
         if (lane == 0) ptx::bulk_wait_group_read<0>();
     }
 
     __syncwarp();
-    if (kPair) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after();
     if (warp == 2) tmem_dealloc<false>(tmem, 512);
 }
@@ -444,20 +415,12 @@ ScaledPlan scaled_plan(int64_t ma, int64_t nb, int64_t k) {
         std::swap(ma, nb);
     }
     const int64_t blocks = cdiv(k, kBlockK);
-    const int64_t wide = nb > 128 ? 256 : 128;
-    const int64_t pair_tiles = cdiv(ma, 256) * cdiv(nb, wide);
-    if (nb > 64 && ma > 128 && (pair_tiles * 2 >= kSms || pair_tiles * blocks >= kSms / 2 * 8)) {
-        pl.pair = true;
-        pl.tile_b = (int32_t)wide;
-        pl.tiles_a = cdiv(ma, 256), pl.tiles_b = cdiv(nb, wide);
-    } else {
-        pl.tile_b = nb <= 64 ? 64 : nb <= 128 ? 128 : 256;
-        while (pl.tile_b > 64 && cdiv(ma, kTileA) * cdiv(nb, pl.tile_b) * 2 <= kSms) pl.tile_b /= 2;
-        pl.tiles_a = cdiv(ma, kTileA), pl.tiles_b = cdiv(nb, pl.tile_b);
-    }
+    pl.tile_b = nb <= 64 ? 64 : nb <= 128 ? 128 : 256;
+    while (pl.tile_b > 64 && cdiv(ma, kTileA) * cdiv(nb, pl.tile_b) * 2 <= kSms) pl.tile_b /= 2;
+    pl.tiles_a = cdiv(ma, kTileA), pl.tiles_b = cdiv(nb, pl.tile_b);
     // Fewer tiles than run at once: all of them in runs.  A last round that
     // leaves half the GPU idle or more: its tiles in runs.
-    const int64_t tiles = pl.tiles_a * pl.tiles_b, at_once = pl.pair ? kSms / 2 : kSms, last = tiles % at_once;
+    const int64_t tiles = pl.tiles_a * pl.tiles_b, at_once = kSms, last = tiles % at_once;
     int64_t parts = 1;
     if (tiles * 2 <= at_once) parts = std::min(at_once / tiles, blocks / 4);
     else if (tiles > at_once && last > 0) parts = std::min<int64_t>(at_once / last, 8);
@@ -466,7 +429,7 @@ ScaledPlan scaled_plan(int64_t ma, int64_t nb, int64_t k) {
     if (parts > 1) {
         pl.parts = (int32_t)parts;
         pl.full = tiles <= at_once ? 0 : tiles - last;
-        pl.part_bytes = (size_t)(parts * (tiles - pl.full) * (pl.pair ? 256 : 128) * pl.tile_b * 4);
+        pl.part_bytes = (size_t)(parts * (tiles - pl.full) * kTileA * pl.tile_b * 4);
     }
     return pl;
 }
@@ -495,33 +458,28 @@ conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *str
     a.wait_limit_ns = wait_limit_ns();
     a.status = device_status_word();
     if (!a.status) return CONV_ERR_CUDA;
-    const bool pair = pl.pair;
     a.tile_b = pl.tile_b, a.tiles_a = (int32_t)pl.tiles_a, a.tiles_b = (int32_t)pl.tiles_b;
     a.parts = pl.parts, a.full = (int32_t)pl.full, a.part = (float *)workspace;
-    a.b_rows = pair ? a.tile_b / 2 : a.tile_b;
     a.stage_bytes = 16384 + a.tile_b * kBlockK;
     a.stages = std::min(kMaxStages, kRingBytes / a.stage_bytes);
-    const int tile_a = pair ? 256 : 128;
     a.idesc = (1u << 4) | ((pr.a.e5m2 ? 1u : 0u) << 7) | ((pr.b.e5m2 ? 1u : 0u) << 10) | ((uint32_t)(a.tile_b >> 3) << 17) |
               ((uint32_t)(kTileA >> 4) << 24);
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     if (!encode(&a.map_a, CONV_FLOAT8_E4M3, pr.a.p, pr.k, pr.ma, pr.a.rs, kBlockK, kTileA, sw) ||
-        !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.b_rows, sw))
+        !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.tile_b, sw))
         return CONV_ERR_CUDA;
     for (auto [s, m] : {std::pair<Side *, CUtensorMap *>{&a.d, &a.map_d}, {&a.pre, &a.map_pre}})
         if (s->walk == kWalkRows &&
             !encode(m, s->dtype, s->p, pr.nb, pr.ma, s->sa, s->dtype == CONV_FLOAT32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
             return CONV_ERR_CUDA;
     typedef void (*Kernel)(ScaledArgs);
-    // [single 64, 128, 256, pair 128, 256][a scale per row of B]
-    static const Kernel kernels[5][2] = {{scaled_product_kernel<false, 32, false>, scaled_product_kernel<false, 32, true>},
-                                         {scaled_product_kernel<false, 64, false>, scaled_product_kernel<false, 64, true>},
-                                         {scaled_product_kernel<false, 128, false>, scaled_product_kernel<false, 128, true>},
-                                         {scaled_product_kernel<true, 64, false>, scaled_product_kernel<true, 64, true>},
-                                         {scaled_product_kernel<true, 128, false>, scaled_product_kernel<true, 128, true>}};
-    const int which = pair ? (a.tile_b == 128 ? 3 : 4) : a.tile_b == 64 ? 0 : a.tile_b == 128 ? 1 : 2, per = pr.b.shift == 0;
+    // [tiles of 64, 128, 256 columns][a scale per row of B]
+    static const Kernel kernels[3][2] = {{scaled_product_kernel<32, false>, scaled_product_kernel<32, true>},
+                                         {scaled_product_kernel<64, false>, scaled_product_kernel<64, true>},
+                                         {scaled_product_kernel<128, false>, scaled_product_kernel<128, true>}};
+    const int which = a.tile_b == 64 ? 0 : a.tile_b == 128 ? 1 : 2, per = pr.b.shift == 0;
     const Kernel kernel = kernels[which][per];
-    static std::atomic<bool> ready[64][5][2];  // (check_device admits 64 devices)
+    static std::atomic<bool> ready[64][3][2];  // (check_device admits 64 devices)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CONV_ERR_CUDA;
     if (!ready[dev][which][per].load()) {
@@ -534,25 +492,13 @@ conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *str
         ready[dev][which][per].store(true);
     }
     const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b, units = a.full + (tiles - a.full) * a.parts;
-    const int cluster = pair ? 2 : 1;
-    const size_t smem = (size_t)a.stages * a.stage_bytes + kSumWarps * kSlotBytes + kScaleSlots * kBatch * kScaleBytes + kBiasBytes + sizeof(SharedCtl);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(units, device_sm_count() / cluster) * cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)cluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return CONV_ERR_CUDA;
+    const size_t smem = (size_t)a.stages * a.stage_bytes + kSumWarps * kSlots * kSlotBytes + kScaleSlots * kBatch * kScaleBytes + kBiasBytes + sizeof(SharedCtl);
+    if (!launch_behind(kernel, dim3((unsigned)std::min<int64_t>(units, device_sm_count())), kThreads, smem, (cudaStream_t)stream, a))
+        return CONV_ERR_CUDA;
     if (a.parts > 1) {
-        const int64_t blocks = (tiles - a.full) * (tile_a / 32) * (a.tile_b / 8);
+        const int64_t blocks = (tiles - a.full) * (kTileA / 32) * (a.tile_b / 8);
         if (blocks > INT32_MAX) return CONV_ERR_TOO_LARGE;
-        if (!launch_behind(scaled_join_kernel, dim3((unsigned)blocks), 32 * std::min(8, a.parts), 0, (cudaStream_t)stream, a, tile_a))
+        if (!launch_behind(scaled_join_kernel, dim3((unsigned)blocks), 32 * std::min(8, a.parts), 0, (cudaStream_t)stream, a, kTileA))
             return CONV_ERR_CUDA;
     }
     return CONV_OK;
