@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
     };
 
     if (threadIdx.x == 0) {
-        ptx::prefetch_tensormap(&a.map_a);
+        if (a.blocks > 0) ptx::prefetch_tensormap(&a.map_a);
         for (int i = 0; i < a.stages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&ctl->full[i]), 2);  // the two loading threads
             ptx::mbar_init(ptx::smem_addr(&ctl->empty[i]), 1);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
         }
         ctl->abort_flag = 0;
         ptx::fence_mbar_init();
-    } else if (threadIdx.x == 96) {
+    } else if (threadIdx.x == 96 && a.blocks > 0) {
         ptx::prefetch_tensormap(&a.map_b);
     }
     __syncthreads();
@@ -465,8 +465,9 @@ conv_status scaled_launch(const ScaledProduct &given, void *workspace, void *str
     a.idesc = (1u << 4) | ((pr.a.e5m2 ? 1u : 0u) << 7) | ((pr.b.e5m2 ? 1u : 0u) << 10) | ((uint32_t)(a.tile_b >> 3) << 17) |
               ((uint32_t)(kTileA >> 4) << 24);
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!encode(&a.map_a, CONV_FLOAT8_E4M3, pr.a.p, pr.k, pr.ma, pr.a.rs, kBlockK, kTileA, sw) ||
-        !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.tile_b, sw))
+    // (without products nothing is loaded: there are no maps)
+    if (a.blocks > 0 && (!encode(&a.map_a, CONV_FLOAT8_E4M3, pr.a.p, pr.k, pr.ma, pr.a.rs, kBlockK, kTileA, sw) ||
+        !encode(&a.map_b, CONV_FLOAT8_E4M3, pr.b.p, pr.k, pr.nb, pr.b.rs, kBlockK, a.tile_b, sw)))
         return CONV_ERR_CUDA;
     for (auto [s, m] : {std::pair<Side *, CUtensorMap *>{&a.d, &a.map_d}, {&a.pre, &a.map_pre}})
         if (s->walk == kWalkRows &&

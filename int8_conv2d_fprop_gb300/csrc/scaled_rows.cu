@@ -1,14 +1,15 @@
 // scaled_rows.cu -- the product of 8-bit operands for a few rows of
 // activations: the stream of weights is all there is.
 //
-// A block takes 16 rows of w, its eight warps the blocks of 128 k in turn; a
-// lane reads 32 bytes of two rows of w and of a row of x in each.  The
-// multiplications run on the tensor cores' warp-level form (16 rows of w by 8
-// of x, f16 operands, which hold the 8-bit values exactly, 32-bit sums): a
-// lane's bytes go to the instruction in the order in which they lie in
-// memory, for both operands alike, so that nothing is rearranged.  Each block's
-// sums are scaled and added in 32 bits; the warps' sums meet in shared memory
-// in a fixed order.
+// A warp takes 16 rows of w and every split-th block of 128 k, as many warps to
+// the same rows as fill the GPU (16 per SM, which all run at once); a lane
+// reads 32 bytes of two rows of w and of a row of x, a block ahead of the one
+// it multiplies.  The multiplications run on the tensor cores' warp-level form
+// (16 rows of w by 8 of x, f16 operands, which hold the 8-bit values exactly,
+// 32-bit sums): a lane's bytes go to the instruction in the order in which
+// they lie in memory, for both operands alike, so that nothing is rearranged.
+// Each block's sums are scaled and added in 32 bits; the warps' sums meet in
+// shared memory in a fixed order.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,12 +23,12 @@
 namespace i8c {
 namespace {
 
-constexpr int kRowsW = 16;  // rows of w per block
+constexpr int kRowsW = 16;  // rows of w per warp
 constexpr int kWarps = 8;
 
 // Bytes k0 .. k0 + 31 of a row, zeros from k on.
-__device__ __forceinline__ void load32(const uint8_t *row, int64_t k0, int64_t k, bool valid, uint32_t (&v)[8]) {
-    if (valid && k0 + 32 <= k) {
+__device__ __forceinline__ void load32(const uint8_t *row, int64_t k0, int64_t k, uint32_t (&v)[8]) {
+    if (k0 + 32 <= k) {
         const uint4 a = reinterpret_cast<const uint4 *>(row + k0)[0], b = reinterpret_cast<const uint4 *>(row + k0)[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         return;
@@ -35,11 +36,9 @@ __device__ __forceinline__ void load32(const uint8_t *row, int64_t k0, int64_t k
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         v[i] = 0;
-        if (valid && k0 + 4 * i < k) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (k0 + 4 * i + j < k) v[i] |= (uint32_t)row[k0 + 4 * i + j] << (8 * j);
-        }
+        for (int j = 0; j < 4; ++j)
+            if (k0 + 4 * i + j < k) v[i] |= (uint32_t)row[k0 + 4 * i + j] << (8 * j);
     }
 }
 
@@ -63,104 +62,129 @@ __device__ __forceinline__ float activate_value(float z, int32_t act) {
     return z;
 }
 
-// kG: groups of 8 rows of x.
+// What a lane has of one block of k.
+template <int kG>
+struct Loaded {
+    uint32_t w[2][8], x[kG][8];
+    float sw[2], sx[kG][2];
+};
+
+// kG: groups of 8 rows of x.  split: warps to the same rows of w.
 template <int kG, bool kXE5m2, bool kWE5m2>
-__global__ void __launch_bounds__(32 * kWarps) scaled_rows_kernel(const ScaledProduct pr) {
+__global__ void __launch_bounds__(32 * kWarps, 2) scaled_rows_kernel(const ScaledProduct pr, int split) {
     __shared__ float part[kWarps][8 * kG][kRowsW + 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane >> 2, t = lane & 3;
-    const int64_t n0 = (int64_t)blockIdx.x * kRowsW;
+    const int tiles = kWarps / split;  // of 16 rows of w, in this block
+    const int64_t n0 = ((int64_t)blockIdx.x * tiles + warp / split) * kRowsW;
     const int blocks = (int)((pr.k + kScaleBlock - 1) / kScaleBlock);
-    const bool w_in[2] = {n0 + g < pr.nb, n0 + g + 8 < pr.nb};
-    const uint8_t *w = pr.b.p + (n0 + g) * pr.b.rs;
-    const float *ws[2] = {pr.b.scale + ((n0 + g) >> pr.b.shift) * pr.b.s_rs, pr.b.scale + ((n0 + g + 8) >> pr.b.shift) * pr.b.s_rs};
+    // (rows past the last are read as the first: nothing of theirs is stored, and rows do not meet)
+    const uint8_t *w[2], *x[kG];
+    const float *ws[2], *xs[kG][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t n = n0 + g + 8 * h < pr.nb ? n0 + g + 8 * h : 0;
+        w[h] = pr.b.p + n * pr.b.rs;
+        ws[h] = pr.b.scale + (n >> pr.b.shift) * pr.b.s_rs;
+    }
+#pragma unroll
+    for (int j = 0; j < kG; ++j) {
+        x[j] = pr.a.p + (8 * j + g < pr.ma ? 8 * j + g : 0) * pr.a.rs;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t m = 8 * j + 2 * t + h < pr.ma ? 8 * j + 2 * t + h : 0;
+            xs[j][h] = pr.a.scale + (m >> pr.a.shift) * pr.a.s_rs;
+        }
+    }
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    for (int64_t m0 = (int64_t)blockIdx.y * 8 * kG; m0 < pr.ma; m0 += (int64_t)gridDim.y * 8 * kG) {
-        float acc[kG][4] = {};
-#pragma unroll 2
-        for (int kb = warp; kb < blocks; kb += kWarps) {
-            const int64_t k0 = (int64_t)kb * kScaleBlock + t * 32;
-            uint32_t wq[2][8], xq[kG][8];
+    auto load = [&](Loaded<kG> &f, int kb) {
+        const int64_t k0 = (int64_t)kb * kScaleBlock + t * 32;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load32(w + 8 * h * pr.b.rs, k0, pr.k, w_in[h], wq[h]);
-            float sw[2], sx[kG][2];
+        for (int h = 0; h < 2; ++h) {
+            load32(w[h], k0, pr.k, f.w[h]);
+            f.sw[h] = ws[h][kb * pr.b.s_cs];
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) sw[h] = w_in[h] ? ws[h][kb * pr.b.s_cs] : 0.0f;
+        for (int j = 0; j < kG; ++j) {
+            load32(x[j], k0, pr.k, f.x[j]);
 #pragma unroll
-            for (int j = 0; j < kG; ++j) {
-                load32(pr.a.p + (m0 + 8 * j + g) * pr.a.rs, k0, pr.k, m0 + 8 * j + g < pr.ma, xq[j]);
+            for (int h = 0; h < 2; ++h) f.sx[j][h] = xs[j][h][kb * pr.a.s_cs];
+        }
+    };
+    float acc[kG][4] = {};
+    auto multiply = [&](const Loaded<kG> &f) {
+        float c[kG][4] = {};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t m = m0 + 8 * j + 2 * t + h;
-                    sx[j][h] = m < pr.ma ? pr.a.scale[(m >> pr.a.shift) * pr.a.s_rs + kb * pr.a.s_cs] : 0.0f;
-                }
-            }
-            float c[kG][4] = {};
+        for (int i = 0; i < 8; ++i) {
+            uint32_t a[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t a[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    a[h] = unpack_eight_bit<kWE5m2>((uint16_t)wq[h][i]);
-                    a[2 + h] = unpack_eight_bit<kWE5m2>((uint16_t)(wq[h][i] >> 16));
-                }
-#pragma unroll
-                for (int j = 0; j < kG; ++j)
-                    mma_16816(c[j], a[0], a[1], a[2], a[3], unpack_eight_bit<kXE5m2>((uint16_t)xq[j][i]),
-                              unpack_eight_bit<kXE5m2>((uint16_t)(xq[j][i] >> 16)));
+            for (int h = 0; h < 2; ++h) {
+                a[h] = unpack_eight_bit<kWE5m2>((uint16_t)f.w[h][i]);
+                a[2 + h] = unpack_eight_bit<kWE5m2>((uint16_t)(f.w[h][i] >> 16));
             }
 #pragma unroll
             for (int j = 0; j < kG; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sw[e >> 1] * sx[j][e & 1], c[j][e], acc[j][e]);
+                mma_16816(c[j], a[0], a[1], a[2], a[3], unpack_eight_bit<kXE5m2>((uint16_t)f.x[j][i]),
+                          unpack_eight_bit<kXE5m2>((uint16_t)(f.x[j][i] >> 16)));
         }
-        __syncthreads();  // (the previous rows' sums have been read)
 #pragma unroll
         for (int j = 0; j < kG; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[warp][8 * j + 2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[j][e];
-        __syncthreads();
-        for (int i = threadIdx.x; i < 8 * kG * kRowsW; i += 32 * kWarps) {
-            const int64_t m = m0 + i / kRowsW, n = n0 + i % kRowsW;
-            if (m >= pr.ma || n >= pr.nb) continue;
-            float z = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(f.sw[e >> 1] * f.sx[j][e & 1], c[j][e], acc[j][e]);
+    };
+    Loaded<kG> f0, f1;
+    int kb = warp % split;
+    if (kb < blocks) load(f0, kb);
+#pragma unroll 1
+    for (; kb < blocks; kb += 2 * split) {
+        if (kb + split < blocks) load(f1, kb + split);
+        multiply(f0);
+        if (kb + 2 * split < blocks) load(f0, kb + 2 * split);
+        if (kb + split < blocks) multiply(f1);
+    }
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) z += part[v][i / kRowsW][i % kRowsW];
-            if (pr.bias) z += load_as_float(pr.bias, n, pr.bias_dtype);
-            if (pr.pre) store_from_float(pr.pre, m * pr.pre_sa + n * pr.pre_sb, pr.pre_dtype, z);
-            z = activate_value(z, pr.act);
-            if (pr.res) z += load_as_float(pr.res, m * pr.res_sa + n * pr.res_sb, pr.d_dtype);
-            store_from_float(pr.d, m * pr.d_sa + n * pr.d_sb, pr.d_dtype, z);
-        }
+    for (int j = 0; j < kG; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[warp][8 * j + 2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < tiles * 8 * kG * kRowsW; i += 32 * kWarps) {
+        const int tile = i / (8 * kG * kRowsW), m = i / kRowsW % (8 * kG);
+        const int64_t n = ((int64_t)blockIdx.x * tiles + tile) * kRowsW + i % kRowsW;
+        if (m >= pr.ma || n >= pr.nb) continue;
+        float z = 0.0f;
+        for (int v = 0; v < split; ++v) z += part[tile * split + v][m][i % kRowsW];
+        if (pr.bias) z += load_as_float(pr.bias, n, pr.bias_dtype);
+        if (pr.pre) store_from_float(pr.pre, m * pr.pre_sa + n * pr.pre_sb, pr.pre_dtype, z);
+        z = activate_value(z, pr.act);
+        if (pr.res) z += load_as_float(pr.res, m * pr.res_sa + n * pr.res_sb, pr.d_dtype);
+        store_from_float(pr.d, m * pr.d_sa + n * pr.d_sb, pr.d_dtype, z);
     }
 }
 
 template <int kG>
-bool launch(const ScaledProduct &pr, dim3 grid, cudaStream_t s) {
+bool launch(const ScaledProduct &pr, cudaStream_t s) {
+    // warps to the same 16 rows of w: as many as 16 per SM allow
+    const int64_t rows = (pr.nb + kRowsW - 1) / kRowsW;
+    int split = kWarps;
+    while (split > 1 && rows * split > 16 * 152) split /= 2;
+    const int64_t tiles = kWarps / split;
+    const dim3 grid((unsigned)((rows + tiles - 1) / tiles));
+    const int threads = 32 * kWarps;
     if (pr.a.e5m2)
-        return pr.b.e5m2 ? launch_behind(scaled_rows_kernel<kG, true, true>, grid, 32 * kWarps, 0, s, pr)
-                         : launch_behind(scaled_rows_kernel<kG, true, false>, grid, 32 * kWarps, 0, s, pr);
-    return pr.b.e5m2 ? launch_behind(scaled_rows_kernel<kG, false, true>, grid, 32 * kWarps, 0, s, pr)
-                     : launch_behind(scaled_rows_kernel<kG, false, false>, grid, 32 * kWarps, 0, s, pr);
+        return pr.b.e5m2 ? launch_behind(scaled_rows_kernel<kG, true, true>, grid, threads, 0, s, pr, split)
+                         : launch_behind(scaled_rows_kernel<kG, true, false>, grid, threads, 0, s, pr, split);
+    return pr.b.e5m2 ? launch_behind(scaled_rows_kernel<kG, false, true>, grid, threads, 0, s, pr, split)
+                     : launch_behind(scaled_rows_kernel<kG, false, false>, grid, threads, 0, s, pr, split);
 }
 
 }  // namespace
 
-bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k) { return ma <= 32 || k == 0; }
+// (More rows than two groups of 8 do not fit the registers with a block ahead.)
+bool scaled_rows_applies(int64_t ma, int64_t nb, int64_t k) { return ma <= 16; }
 
 conv_status scaled_rows_launch(const ScaledProduct &pr, void *stream) {
-    const int64_t groups = std::min<int64_t>((pr.ma + 7) / 8, 4);
-    const int64_t tiles = (pr.ma + 8 * groups - 1) / (8 * groups);
-    const dim3 grid((unsigned)((pr.nb + kRowsW - 1) / kRowsW), (unsigned)std::min<int64_t>(tiles, 65535));
     const cudaStream_t s = (cudaStream_t)stream;
-    bool ok;
-    switch (groups) {
-        case 1: ok = launch<1>(pr, grid, s); break;
-        case 2: ok = launch<2>(pr, grid, s); break;
-        case 3: ok = launch<3>(pr, grid, s); break;
-        default: ok = launch<4>(pr, grid, s); break;
-    }
-    return ok ? CONV_OK : CONV_ERR_CUDA;
+    return (pr.ma <= 8 ? launch<1>(pr, s) : launch<2>(pr, s)) ? CONV_OK : CONV_ERR_CUDA;
 }
 
 }  // namespace i8c

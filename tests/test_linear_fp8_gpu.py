@@ -158,10 +158,11 @@ def test_empty_extents(ic):
     def make(rows, k):
         return torch.zeros(rows, k, device="cuda").to(E4), torch.ones(rows, ob.blocks(k), device="cuda")
 
-    b, r = torch.randn(24, device="cuda"), torch.randn(5, 24, device="cuda").to(BF16)
-    y = ic.conv_linear_fp8(*make(5, 0), *make(24, 0), b, activation="silu", residual=r)
-    want = ob.activate(b.double(), "silu") + r.double()
-    check(y, want.expand(5, 24), 2.0 ** -8 * want.abs() + 2.0 ** -20, "y")
+    for m in (5, 40):
+        b, r = torch.randn(24, device="cuda"), torch.randn(m, 24, device="cuda").to(BF16)
+        y = ic.conv_linear_fp8(*make(m, 0), *make(24, 0), b, activation="silu", residual=r)
+        want = ob.activate(b.double(), "silu") + r.double()
+        check(y, want, 2.0 ** -8 * want.abs() + 2.0 ** -20, "y")
     assert ic.conv_linear_fp8(*make(0, 64), *make(24, 64)).shape == (0, 24)
     assert ic.conv_linear_fp8(*make(5, 64), *make(0, 64)).shape == (5, 0)
 
