@@ -41,7 +41,7 @@ constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;  // of a block
 constexpr int kBiasBytes = kSumWarps * 128;
 constexpr int kSlots = 4;          // staging slots of a summing warp: its columns of a tile, all on their way at once
 constexpr int kRingBytes = 147456;
-// registers: 384 threads start with 168 each; the summing warps' 128 sums, 64
+// registers: 384 threads start with 168 each; the summing warps' 128 sums, 32
 // values on their way and the rest of their state take up to 224
 constexpr int kControlRegs = 48, kSumRegs = 224, kLaunchRegs = 168;
 static_assert(128 * kControlRegs + 32 * kSumWarps * kSumRegs <= kThreads * kLaunchRegs);
