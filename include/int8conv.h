@@ -655,11 +655,13 @@ conv_status conv_layer_norm_grad(const conv_matrix_desc *dy, const void *dy_dev,
  * CONV_BFLOAT16, or x's type; slopes as in conv_linear_grad),
  *   scale = max(a / L, 2^-126),  q = v / scale rounded to nearest even
  * where a is the largest magnitude of the block and L the largest value of
- * q's type.  (q is made as v * (L / a), off by 2^-23 of itself before it is
- * rounded.)  Blocks are 128 elements of a row (tile 1) or squares of 128 x
- * 128 (tile 128), counted from the first row and column; the last ones may be
- * short.  A block that holds an infinity or a NaN has it as its scale, and
- * everything made of the block is NaN.
+ * q's type.  (The quotient, by the scale before that is rounded, is exact
+ * where 32 bits hold it and within 2^-23 of itself elsewhere: a value of 16
+ * bits goes to the nearest 8-bit one, or of two equally near ones to the even.)
+ * Blocks are 128 elements of a row (tile 1) or squares of 128 x 128 (tile 128),
+ * counted from the first row and column; the last ones may be short.  A block
+ * that holds an infinity or a NaN has it as its scale, and everything made of
+ * the block is NaN.
  *   q   [M,C], scale  [ceil(M / tile), ceil(C / 128)]   (rows)
  *   qt  [C,M], scale_t [ceil(C / tile), ceil(M / 128)]  (columns: the same of
  *              x transposed, which is what a product over the rows wants)

@@ -178,9 +178,10 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
                     if (c >= a.cols) continue;
                     if (at.t % 16 == 0)
                         ((float *)const_cast<void *>(a.y_scale.p))[r * a.y_scale.rs + c / 128 * a.y_scale.cs] = b.scale;
-                    const uint2 q = make_uint2(
-                        pack_eight_bit<false>(o[0] * b.factor, o[1] * b.factor, o[2] * b.factor, o[3] * b.factor),
-                        pack_eight_bit<false>(o[4] * b.factor, o[5] * b.factor, o[6] * b.factor, o[7] * b.factor));
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        split(quotient(pair(o[j], o[j + 1]), pair(b.factor), pair(b.rest)), &o[j], &o[j + 1]);
+                    const uint2 q = make_uint2(pack_eight_bit<false>(o[0], o[1], o[2], o[3]), pack_eight_bit<false>(o[4], o[5], o[6], o[7]));
                     uint8_t *p = (uint8_t *)const_cast<void *>(a.y.p) + r * a.y.rs + c;
                     if (c + 8 <= a.cols) {
                         *reinterpret_cast<uint2 *>(p) = q;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kAnyThreads) block_norm_any_kernel(const Block
                 const int c = b * 128 + j * 32 + lane;
                 if (c < a.cols)
                     ((uint8_t *)const_cast<void *>(a.y.p))[r * a.y.rs + c * a.y.cs] =
-                        (uint8_t)pack_eight_bit<false>(o[j] * q.factor, 0.0f, 0.0f, 0.0f);
+                        (uint8_t)pack_eight_bit<false>(quotient(o[j], q), 0.0f, 0.0f, 0.0f);
             }
         }
         __syncthreads();  // (before the next row is written over this one)

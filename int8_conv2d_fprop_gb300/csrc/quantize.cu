@@ -9,8 +9,8 @@
 // row form is written from the registers, 128 bytes of a row by 16 threads;
 // the column form is turned through 16 KB of shared memory in pieces of 4
 // bytes, so that it too leaves in runs of 128.  A stream: 16384 x 4096 bf16 to
-// rows takes 35.6 us (5.7 TB/s).  With slopes and both forms the instructions
-// bound it (58 per element; 34.6 us for 2047 x 5001 f16 with odd strides).
+// rows takes 36.6 us (5.6 TB/s).  With slopes and both forms the instructions
+// bound it (35.3 us for 2047 x 5001 f16 with odd strides).
 #include <cuda_runtime.h>
 
 #include "channel.h"
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint32_t widened(uint32_t m) {
 template <typename X, bool kRaw>
 struct Values {
     Group<X> g[kRows];
-    __device__ __forceinline__ float at(int i, int j) const { return element(g[i], j); }
+    __device__ __forceinline__ Pair at(int i, int j) const { return element2(g[i], j); }  // of row i, elements 2j and 2j + 1
     __device__ __forceinline__ uint32_t row_most(int i) const {
         uint32_t m = 0;
 #pragma unroll
@@ -186,7 +186,7 @@ struct Values {
 template <typename X>
 struct Values<X, false> {
     float v[kRows][8];
-    __device__ __forceinline__ float at(int i, int j) const { return v[i][j]; }
+    __device__ __forceinline__ Pair at(int i, int j) const { return pair(v[i][2 * j], v[i][2 * j + 1]); }
     __device__ __forceinline__ uint32_t row_most(int i) const {
         uint32_t m = 0;
 #pragma unroll
@@ -292,39 +292,33 @@ __global__ void __launch_bounds__(kThreads, kIs16<X> && !kSlope ? 3 : 2) quantiz
     }
     if (!kColumns || a.q.p) {
         // (thread i of a half warp writes row i's scale: neighbouring rows' in one access)
-        uint32_t mine = 0;
-        float f[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (a.whole) {
-                f[i] = tile_scale.factor;
-                continue;
-            }
-            uint32_t m = v.row_most(i);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (cg == i) mine = m;
-        }
+        BlockScale s = tile_scale;
         if (!a.whole) {
-            const BlockScale s = block_scale<kE5m2>(mine);  // (the divisions once for a row, by its thread)
+            uint32_t mine = 0;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                uint32_t m = v.row_most(i);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (cg == i) mine = m;
+            }
+            s = block_scale<kE5m2>(mine);  // (the divisions once for a row, by its thread)
             if (cg < kRows && r0 + cg < a.rows)
                 ((float *)const_cast<void *>(a.scale.p))[(r0 + cg) * a.scale.rs + tc * a.scale.cs] = s.scale;
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) f[i] = __shfl_sync(0xffffffffu, s.factor, i, 16);
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
+        for (int i = 0; i < kRows; ++i) {
+            const Pair f = pair(__shfl_sync(0xffffffffu, s.factor, i, 16)), rest = pair(__shfl_sync(0xffffffffu, s.rest, i, 16));
+            float q[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split(quotient(v.at(i, j), f, rest), &q[2 * j], &q[2 * j + 1]);
             if (r0 + i < a.rows)
-                store8(a.q, r0 + i, c0, a.cols, a.q_vec,
-                       pack_eight_bit<kE5m2>(v.at(i, 0) * f[i], v.at(i, 1) * f[i], v.at(i, 2) * f[i], v.at(i, 3) * f[i]),
-                       pack_eight_bit<kE5m2>(v.at(i, 4) * f[i], v.at(i, 5) * f[i], v.at(i, 6) * f[i], v.at(i, 7) * f[i]));
+                store8(a.q, r0 + i, c0, a.cols, a.q_vec, pack_eight_bit<kE5m2>(q[0], q[1], q[2], q[3]),
+                       pack_eight_bit<kE5m2>(q[4], q[5], q[6], q[7]));
+        }
     }
     if constexpr (kColumns) {
-        float f[8];
-        if (a.whole) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = tile_scale.factor;
-        } else {
+        if (!a.whole) {
             uint32_t m[8];
             v.column_most(m);
             if (threadIdx.x % 32 < 16) {
@@ -332,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, kIs16<X> && !kSlope ? 3 : 2) quantiz
                 *reinterpret_cast<uint4 *>(&most[warp][cg * 8 + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
             }
             __syncthreads();
-            // a column's scale by one thread, its factor to the others
+            // a column's scale by one thread, its factors to the others
             if (threadIdx.x < kTile) {
                 uint32_t c = 0;
 #pragma unroll
@@ -341,15 +335,31 @@ __global__ void __launch_bounds__(kThreads, kIs16<X> && !kSlope ? 3 : 2) quantiz
                 const int64_t col = tc * kTile + threadIdx.x;
                 if (col < a.cols) ((float *)const_cast<void *>(a.scale_t.p))[col * a.scale_t.rs + tr * a.scale_t.cs] = s.scale;
                 most[0][threadIdx.x] = __float_as_uint(s.factor);
+                most[1][threadIdx.x] = __float_as_uint(s.rest);
             }
             __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(most[0][cg * 8 + j]);
         }
         // (pieces exchanged in pairs so that a warp's meet all banks)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            turned[cg * 8 + j][rg ^ (cg * 2)] = pack_eight_bit<kE5m2>(v.at(0, j) * f[j], v.at(1, j) * f[j], v.at(2, j) * f[j], v.at(3, j) * f[j]);
+        for (int h = 0; h < 2; ++h) {
+            float4 f = make_float4(tile_scale.factor, tile_scale.factor, tile_scale.factor, tile_scale.factor);
+            float4 rest = make_float4(tile_scale.rest, tile_scale.rest, tile_scale.rest, tile_scale.rest);
+            if (!a.whole) {
+                f = *reinterpret_cast<const float4 *>(&most[0][cg * 8 + h * 4]);
+                rest = *reinterpret_cast<const float4 *>(&most[1][cg * 8 + h * 4]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float q[2][kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    split(quotient(v.at(i, h * 2 + j), j ? pair(f.z, f.w) : pair(f.x, f.y), j ? pair(rest.z, rest.w) : pair(rest.x, rest.y)),
+                          &q[0][i], &q[1][i]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    turned[cg * 8 + h * 4 + j * 2 + k][rg ^ (cg * 2)] = pack_eight_bit<kE5m2>(q[k][0], q[k][1], q[k][2], q[k][3]);
+            }
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kTile * 16 / kThreads; ++i) {
