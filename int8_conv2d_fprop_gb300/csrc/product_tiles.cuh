@@ -401,7 +401,8 @@ __device__ __forceinline__ void free_slot(const WarpTile &t) {
     if (t.lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
 }
-// ... of the next slot in turn, which t then has.
+// ... of the next slot in turn, which t then has: every turn commits a group, so
+// that with all but the last kSlots - 1 read this slot's is.
 template <int kSlots>
 __device__ __forceinline__ void next_slot(WarpTile &t, const WarpTile &given) {
     if (t.lane == 0) ptx::bulk_wait_group_read<kSlots - 1>();
@@ -410,6 +411,13 @@ __device__ __forceinline__ void next_slot(WarpTile &t, const WarpTile &given) {
         t.slot = given.slot + given.turn * kSlotBytes;
         given.turn = given.turn + 1 == kSlots ? 0 : given.turn + 1;
     }
+}
+
+// The slot has been written out without TMA (or not at all): an empty group in
+// its place, for next_slot counts one for every turn.
+template <int kSlots>
+__device__ __forceinline__ void skip_slot(const WarpTile &t) {
+    if (kSlots > 1 && t.lane == 0) ptx::bulk_commit_group();
 }
 
 template <int kSlots = 1>
@@ -433,6 +441,7 @@ __device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *ma
                 slot_to_words((uint16_t *)s.p + (int64_t)t.row0 * s.sa + t.b0, s.sa, t.rows, t.cols, t.slot);
             else
                 slot_to_any(s, t, 0, t.cols);
+            skip_slot<kSlots>(t);
         }
         return;
     }
@@ -450,6 +459,7 @@ __device__ __forceinline__ void store_chunk(const Side &s, const CUtensorMap *ma
         }
         __syncwarp();
         if (c < t.cols) slot_to_any(s, t, c, min(16, t.cols - c));
+        skip_slot<kSlots>(t);
     }
 }
 
