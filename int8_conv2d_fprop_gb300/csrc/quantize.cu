@@ -121,13 +121,16 @@ __device__ __forceinline__ void load8(const MatRef &m, const uint16_t *end, int6
     }
 }
 
-// 8 values of preact as stored, where it is read in vectors (and has 16 bits).
+// 8 values of preact as stored, where it is read in vectors (and has 16 bits):
+// like x's, none of them from past the matrix.
 __device__ __forceinline__ uint4 load_preact(const QuantizeArgs &a, int64_t r, int64_t c) {
     const MatRef &m = a.pre;
     if (a.pre_reads == kReadShifted)
         return load16_shifted(r < a.rows && c < a.cols + 8 ? (const uint16_t *)m.p + r * m.rs : nullptr, c, a.cols,
                               (const uint16_t *)m.p, a.pre_end);
-    return r < a.rows && c < a.cols ? *reinterpret_cast<const uint4 *>((const uint16_t *)m.p + r * m.rs + c) : make_uint4(0, 0, 0, 0);
+    Group<__half> g;  // (either type, as stored)
+    load8<__half, kReadVectors>(m, nullptr, r, a.rows, c, a.cols, g);
+    return make_uint4(g.w[0], g.w[1], g.w[2], g.w[3]);
 }
 
 template <int kAct>

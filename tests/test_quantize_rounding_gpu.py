@@ -90,3 +90,20 @@ def test_every_middle(ic):
         x = torch.cat([r for d, r in rows if d is dtype])
         assert x.count_nonzero() > 8 * 20
         check(ic.conv_quantize(x, dtype=dtype), x.double(), dtype, 1)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("m,c,pad", [(1, 5, 0), (1, 131, 0), (1, 203, 0), (7, 100, 4), (130, 261, 3)])
+def test_preactivation_that_ends_with_its_buffer(ic, dt, m, c, pad):
+    """Rows from 16-byte boundaries whose last one ends inside a vector, at the end of the memory: nothing is read past it.
+    (ReLU's slopes of the wrong elements, or of NaN beside them, would show in q.)"""
+    g = torch.Generator(device="cuda").manual_seed(m + c)
+    x = torch.randn(m, c, generator=g, device="cuda").to(dt)
+    flat = torch.full(((m - 1) * (c + pad) + c,), float("nan"), device="cuda", dtype=dt)
+    z = flat.as_strided((m, c), (c + pad, 1))
+    z.copy_(torch.randn(m, c, generator=g, device="cuda"))
+    assert z.data_ptr() % 16 == 0 and (m == 1 or (c + pad) % 8 == 0)
+    got = ic.conv_quantize(x, columns=True, preact=z, activation="relu")
+    v = x.double() * (z > 0)
+    check(got[:2], v, E4, 1)
+    check(got[2:], v.t(), E4, 1)
