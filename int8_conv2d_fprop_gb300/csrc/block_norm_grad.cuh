@@ -9,7 +9,7 @@
 // stretch and gate have.  A second kernel adds the slots in order.  Where there
 // are more gates than workers, a worker takes whole gates and writes their
 // dgate itself.  50176 x 512 bf16 with 64 gates: 69 us (4.5 TB/s), near the
-// issue rate; 2047 x 5001 f16 with odd strides 81 us, a block of 320 threads per SM.
+// issue rate; 2047 x 5001 f16 with odd strides 82 us, a block of 320 threads per SM.
 #pragma once
 
 #include "block_norm.cuh"
@@ -244,14 +244,27 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 2 : 1) block_norm_g
         fill(stage);
         if (++stage == a.stages) stage = 0, phase ^= 1;
         if (a.dx.p) {
-#pragma unroll
-            for (int i = 0; i < kNv; ++i) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)  // (minus is 0 and rx 1 without a post norm)
-                    split(fma2(element2(gx[i], j), pair(second ? minus : 0.0f), mul2(dh[i][j], pair(rx))), &o[2 * j], &o[2 * j + 1]);
+            // (two loops: without a post norm dx is db whatever x is, an infinity among it too)
+            auto put = [&](int i, const float (&o)[8]) {
                 if (!kEven && a.shift_dx) store_shifted(dx, at, i, o);
                 else store_group<true, T, kEven>(dx, at, i, o);
+            };
+            float o[8];
+            if (second) {
+#pragma unroll
+                for (int i = 0; i < kNv; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        split(fma2(element2(gx[i], j), pair(minus), mul2(dh[i][j], pair(rx))), &o[2 * j], &o[2 * j + 1]);
+                    put(i, o);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kNv; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) split(dh[i][j], &o[2 * j], &o[2 * j + 1]);
+                    put(i, o);
+                }
             }
         }
         if (a.dskip.p) dskip += rows.step * a.dskip.rs;
