@@ -563,7 +563,8 @@ PyObject *block_norm(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     }
     const Call c(*x.t, arg[16]);
     at::Tensor made_sum, made, made_scale;
-    if (!sum.t && (skip.t || gate.t || p.post_norm || !norm)) {
+    // (without any of these the sum is x itself)
+    if (!sum.t && (skip.t || gate.t || p.post_norm || p.branch_scale != 1.0f || !norm)) {
         made_sum = c.empty(x.t->sizes(), skip.t ? skip.t->scalar_type() : x.t->scalar_type());
         if (!sum.read(made_sum, "sum")) return nullptr;
     }

@@ -52,3 +52,20 @@ def test_dx_does_not_depend_on_x(ic, c, groups, bad):
         hit = torch.zeros_like(clean[2], dtype=torch.bool)
         hit[7 // (m // groups), 5] = True
         assert not bool(torch.isfinite(got[2][hit]).any()) and torch.equal(got[2][~hit], clean[2][~hit])
+
+
+@pytest.mark.parametrize("c", [200, 2003])
+def test_scaled_branch_alone_has_a_sum(ic, c):
+    """The sum is left out only where it is x itself: not where the branch is scaled."""
+    x = torch.randn(9, c, device="cuda").to(BF16)
+    s, y = ic.conv_block_norm(x)
+    assert s is None
+    for scale in (0.5, -1.0, 0.0):
+        s, y = ic.conv_block_norm(x, branch_scale=scale)
+        given, out = torch.empty_like(x), torch.empty_like(x)
+        ic.conv_block_norm(x, branch_scale=scale, sum=given, out=out)
+        assert s is not None and torch.equal(s, given) and torch.equal(s, (scale * x.float()).to(BF16))
+        assert torch.equal(y, out)
+        # (the statistics belong to this sum: |y| has a mean square of 1, where the sum has one)
+        if scale:
+            assert float((y.double().square().mean(1) - 1).abs().max()) < 2.0 ** -7
