@@ -304,7 +304,8 @@ def conv_clip_grads(grads, max_norm=None, *, eps: float = 1e-6, out=None, norm=N
     """The global norm of the tensors in grads (float32, float16 or bfloat16,
     without gaps between their elements), and, with a max_norm, the tensors
     times min(1, max_norm / (norm + eps)): in place, or to the tensors in out
-    (of the same types, shapes and strides).  norm: optional float32 tensor of
+    (of the same types, shapes and strides).  An infinite max_norm is none:
+    nothing is written then, and out is refused.  norm: optional float32 tensor of
     one element that receives the norm.  Nothing waits for the GPU.  Returns
     norm."""
     r = (_binding or _load()).clip_grads(grads, float("inf") if max_norm is None else max_norm, eps, out, norm, workspace,

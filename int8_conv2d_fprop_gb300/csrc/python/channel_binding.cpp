@@ -176,10 +176,17 @@ bool scalar_type(PyObject *o, at::ScalarType *type) {
     }
 }
 
-// A Python number as a 32-bit float.
+// A Python number as a 32-bit float; one that would become an infinity there
+// would mean something else.
 bool number(PyObject *o, float *v) {
-    *v = (float)PyFloat_AsDouble(o);
-    return !PyErr_Occurred();
+    const double d = PyFloat_AsDouble(o);
+    *v = (float)d;
+    if (PyErr_Occurred()) return false;
+    if (std::isinf(*v) && !std::isinf(d)) {
+        PyErr_SetString(PyExc_ValueError, "a number is beyond the range of 32-bit floats");
+        return false;
+    }
+    return true;
 }
 
 // One type for the parameter vectors that are there (which hold floats).
@@ -682,6 +689,8 @@ PyObject *clip_grads(PyObject *, PyObject *const *arg, Py_ssize_t n) {
     }
     float max_norm, eps;
     if (!number(arg[1], &max_norm) || !number(arg[2], &eps)) return nullptr;
+    if (outs.o && std::isinf(max_norm))  // (the library would leave them as they are)
+        return fail("out", "is for clipped tensors; without a finite max_norm nothing is clipped"), nullptr;
     bool ok;
     const at::Tensor *norm = tensor(all, arg[4], "norm", &ok);
     if (!ok || !Workspace::admit(all, arg[5])) return nullptr;
