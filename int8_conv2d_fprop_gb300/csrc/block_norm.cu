@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : kNv == 1 ? 2 : 
         if (a.sum.p) sum += rows.step * a.sum.rs;
         if (a.y.p && !a.y_scale.p) y += rows.step * a.y.rs;
     }
+    wait.settle(feed.on);
 }
 
 // Any strides, types and widths: a block per row, held in shared memory.

@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 2 : 1) block_norm_g
         if (a.dskip.p) dskip += rows.step * a.dskip.rs;
         if (a.dx.p) dx += rows.step * a.dx.rs;
     }
+    wait.settle(feed.on);
     // (workers beyond the rows leave no gate, and nothing of theirs is added)
     if (rows.first < rows.end) leave_gate();
     if constexpr (!kWarp) {

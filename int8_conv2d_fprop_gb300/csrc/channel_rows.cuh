@@ -443,7 +443,7 @@ struct RowSummer {
 };
 
 // Waits for a row, not for ever: a thread that has given up once (the status
-// word then says so) does not wait again.
+// word then says so) does not wait again until the end.
 struct RowWait {
     uint64_t limit_ns;
     int *status;
@@ -457,6 +457,17 @@ struct RowWait {
                 atomicExch(status, (int)CONV_ERR_DEVICE_TIMEOUT);
                 return;
             }
+        }
+    }
+
+    // Behind the rows: after a wait that ran out copies may still be under way to
+    // the block's shared memory.  The lanes that started them stay until they
+    // have landed: 10 ms, where a copy takes microseconds (rows were fed on
+    // without waiting, so that no phase says which of them is in).
+    __device__ __forceinline__ void settle(bool feeds) const {
+        if (!gave_up || !feeds) return;
+        const uint64_t t0 = ptx::global_timer_ns();
+        while (ptx::global_timer_ns() - t0 < 10000000) {
         }
     }
 };

@@ -254,6 +254,14 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                     rg.next(a.stages);
                 }
             }
+            // After a time-out the MMAs under way have to end before their
+            // shared and tensor memory goes: the last one's commit covers all.
+            // (Else the summing warps have waited for every accumulator.)
+            if (*abort_flag && n > 0) {
+                const uint64_t t0 = ptx::global_timer_ns();
+                while (!ptx::mbar_test_wait(ptx::smem_addr(&ctl->acc_full[(n - 1) & 1]), ((n - 1) >> 1) & 1))
+                    if (ptx::global_timer_ns() - t0 > 10000000) break;
+            }
         } else if (warp == 2) {
             // ------------------------------------------------ scales: of this CTA's rows, and of the tile's columns
             Ring rg;
