@@ -703,7 +703,9 @@ conv_status conv_quantize(const conv_matrix_desc *x, const void *x_dev, const co
  * preact [M,N] CONV_FLOAT16 or CONV_BFLOAT16; the bias holds
  * p->bias_dtype, CONV_FLOAT32 or y's type.
  * Products are exact, the sums of a block and over the blocks are in 32 bits,
- * and y and preact are each rounded once.
+ * and y and preact are each rounded once.  The two scales of a block are
+ * multiplied with each other first, in 32 bits: scales whose product is beyond
+ * them are of no use.
  *
  * The gradients are products of the same kind: with w quantised in columns
  * (wt) and the loss gradient dz quantised both ways (dz, dzt),
@@ -749,7 +751,13 @@ conv_status conv_linear_fp8(const conv_matrix_desc *x, const void *x_dev, const 
  * made of the unrounded sum) is in 32 bits.  sum may be the same matrix as
  * skip, and y or sum the same as x where the types are the same.  C is 1 to
  * 49152.  M = 0 does nothing.  No workspace.  A row with an infinity or a NaN
- * gives NaN in that row alone.
+ * gives NaN in that row alone, and so does one whose sum of squares is beyond
+ * 32-bit floats (values of some 2^60 or more).
+ * Speed: rows with adjacent columns, x's and skip's starting equally far past a
+ * multiple of 8 elements (with an 8-bit y at one), are held in registers where
+ * two of each and the parameters fit shared memory: up to 8192 columns of 16
+ * bits (not those of 7674 to 8040), fewer of 32.  Others go an element at a
+ * time, several times slower.
  * Errors as for conv_layer_norm (CONV_ERR_SHAPE_MISMATCH also where G does
  * not divide M, CONV_ERR_TOO_LARGE also for C).
  */
@@ -788,10 +796,14 @@ conv_status conv_block_norm(const conv_matrix_desc *x, const void *x_dev, const 
  * dy) may be NULL: not computed; at least one is wanted.  dskip may be the
  * same matrix as dsum, and dx the same as dy.  Sums are in 32 bits, in an
  * order that does not depend on timing.  M = 0 gives zero for the sums over
- * rows.  C is 1 to 24576.
+ * rows.  C is 1 to 24576.  Speed: as for conv_block_norm, with rows of 16 bits
+ * held in registers up to 6649 columns (not those of 4593 to 4608 and 5441 to
+ * 5632; with several gates aligned ones only), fewer of 32.
  *
  * The workspace (conv_block_norm_grad_workspace_size bytes, 256-byte aligned)
- * holds partial sums; groups is G of gate and dgate (1 without them).
+ * holds partial sums (five lines of C for each of up to 608 blocks, or 2432
+ * where C is 512 at most, whatever is wanted); groups is G of gate and dgate (1
+ * without them).
  * Errors as for conv_block_norm.
  */
 conv_status conv_block_norm_grad_workspace_size(const conv_matrix_desc *x, int64_t groups, size_t *bytes);

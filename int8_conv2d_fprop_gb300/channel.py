@@ -272,7 +272,8 @@ def conv_block_norm(x, skip=None, *, post_norm: bool = False, post_gain=None, ga
     that are not given are allocated; sum may be skip or x, and out x.  With
     x and gain alone this is the root-mean-square norm.  Returns (sum, out),
     or (sum, out, out_scale) with an 8-bit out; sum is None where it is x
-    itself and not given, out without a norm."""
+    itself (no skip, gate, post norm or branch_scale) and not given, out
+    without a norm."""
     r = (_binding or _load()).block_norm(x, skip, post_norm, post_gain, gate, skip_scale, branch_scale, gain, norm, eps,
                                          sum, out, out_scale, None if dtype is None else _type_code(dtype), post_rstd,
                                          rstd, None if stream is None else stream.cuda_stream)

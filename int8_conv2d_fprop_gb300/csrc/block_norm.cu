@@ -3,10 +3,13 @@
 // rows.
 //
 // A stream.  A row is held in the registers of a worker: a warp (up to 512
-// columns) or a block.  Its matrices come in by bulk copies, one for each row
-// and matrix, two rows ahead: that takes an instruction of a lane where
-// asynchronous copies took two of every thread, and the kernel is near its
-// issue rate.  The sums of squares run over registers, and every output is
+// columns where all rows are of whole aligned groups of 8, else up to 256 of
+// aligned rows and 249 of others) or a block (up to 8192, of unaligned rows
+// 8185).  Its matrices come in by bulk copies, one for each row and matrix, one
+// to three rows ahead as shared memory allows: that takes an instruction of a
+// lane where asynchronous copies took two of every thread.  Wider rows, and some
+// widths below whose rows and parameters do not fit shared memory beside each
+// other, go an element at a time.  The sums of squares run over registers, and every output is
 // written once.  A worker takes a stretch of rows, so that it reads its gates
 // once each.  50176 x 512 bf16 with 64 gates: 40.4 us (5.1 TB/s).
 #include <cuda_runtime.h>

@@ -176,8 +176,7 @@ inline int64_t workers_at_once(const Held &h, int threads_bound, size_t smem) {
     return device_sm_count() * per_sm * (h.warp ? 8 : 1);
 }
 
-// Rows of each of `most` workers, as stretches of `unit` rows or more: all
-// workers' alike but the last one's.
+// Rows of each of `most` workers: all stretches alike but the last one.
 inline int64_t stretch_of(int64_t rows, int64_t most) { return (rows + most - 1) / most; }
 
 // Sets of kept parameters: two gains for all workers, or (rows that begin

@@ -8,8 +8,8 @@
 // whenever a gate ends; stretch w leaves gate g's in slot w + g, which no other
 // stretch and gate have.  A second kernel adds the slots in order.  Where there
 // are more gates than workers, a worker takes whole gates and writes their
-// dgate itself.  50176 x 512 bf16 with 64 gates: 69 us (4.5 TB/s), near the
-// issue rate; 2047 x 5001 f16 with odd strides 82 us, a block of 320 threads per SM.
+// dgate itself.  50176 x 512 bf16 with 64 gates: 69 us (4.5 TB/s; 39
+// instructions per element, in half of the issue slots); 2047 x 5001 f16 with odd strides 82 us, a block of 320 threads per SM.
 #pragma once
 
 #include "block_norm.cuh"
@@ -37,8 +37,8 @@ struct BlockNormGradArgs {
     int *status;
 };
 
-// Adds or stores a thread's 8 shares of group i; a worker's shares start at
-// its lead, so that whole groups are aligned.
+// Stores a thread's 8 shares of group i; a worker's shares start at its
+// lead, so that whole groups are aligned.
 __device__ __forceinline__ void store_share(float *part, const Place<true> &at, int i, const Pair (&v)[4]) {
     const int c = at.column(i, 0) + at.lead;
     if (c >= at.cols + at.lead) return;

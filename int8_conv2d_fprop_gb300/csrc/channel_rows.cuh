@@ -422,9 +422,7 @@ __host__ __device__ constexpr uint32_t row_slot_bytes(int32_t cols, uint32_t siz
     return ((uint32_t)cols + 7) / 8 * 8 * size + 8 * size;
 }
 
-// Sum of one value over the block (at most 32 warps), the same in every thread
-// and in the same order in all of them, with one barrier: consecutive sums use
-// the two buffers in turn, and no warp can be two sums ahead.
+// Summer for one value.
 struct RowSummer {
     float (*part)[32];
     int turn = 0;

@@ -39,7 +39,10 @@ constexpr int kBatch = 4;          // blocks whose scales come together
 constexpr int kScaleSlots = 2;     // batches on their way
 constexpr int kScaleBytes = (kTileA + kMaxTileB) * 4;  // of a block
 constexpr int kBiasBytes = kSumWarps * 128;
-constexpr int kSlots = 4;          // staging slots of a summing warp: its columns of a tile, all on their way at once
+// staging slots of a summing warp: four chunks of 32 columns of 16 bits, a tile's
+// all on their way at once (twice as many turns for 32 bits, and a
+// pre-activation takes its own)
+constexpr int kSlots = 4;
 constexpr int kRingBytes = 147456;
 // registers: 384 threads start with 168 each; the summing warps' 128 sums, 32
 // values on their way and the rest of their state take up to 224
