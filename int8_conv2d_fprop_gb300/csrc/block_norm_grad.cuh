@@ -8,7 +8,7 @@
 // whenever a gate ends; stretch w leaves gate g's in slot w + g, which no other
 // stretch and gate have.  A second kernel adds the slots in order.  Where there
 // are more gates than workers, a worker takes whole gates and writes their
-// dgate itself.  50176 x 512 bf16 with 64 gates: 69 us (4.5 TB/s; 39
+// dgate itself.  50176 x 512 bf16 with 64 gates: 70 us (4.4 TB/s; 39
 // instructions per element, in half of the issue slots); 2047 x 5001 f16 with odd strides 82 us, a block of 320 threads per SM.
 #pragma once
 

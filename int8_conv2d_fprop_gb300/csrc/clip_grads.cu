@@ -9,7 +9,7 @@
 // last is still in L2.  The table of tensors travels in the launch's
 // parameters, up to 64 of them in a small launch and 960 in a large one; more
 // take several launches, whose sums meet in the workspace.  A stream: 268
-// million values in 48 tensors take 266 us (read twice and written once, 6.0
+// million values in 48 tensors take 265 us (read twice and written once, 6.0
 // TB/s), six small tensors 9.3 us of launches.
 #include <cuda_runtime.h>
 
