@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
             const int rows = min(32, min(a.ma, (ia + 1) * a.rows_a) - row0);
             if (part * 32 < a.tile_b) fetch_residual(a, wt, row0, rows, ib * a.tile_b + part * 32);
-            if (!wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status, a.spin)) break;
+            // (a warp stops as a whole: its tensor-memory loads take all lanes)
+            if (!__all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status, a.spin)))
+                break;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + slot * kMaxTileB + ((uint32_t)(quad * 32) << 16);
             if (k_lo == k_hi) {  // no products: the accumulator was never written

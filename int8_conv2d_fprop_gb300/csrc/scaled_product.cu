@@ -119,6 +119,10 @@ __device__ __forceinline__ bool wait_polling(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// Whether all lanes have got what they waited for.  A warp gives up as a whole:
+// the tensor-memory loads and the barriers of a warp take all its lanes.
+__device__ __forceinline__ bool all_lanes(bool got) { return __all_sync(0xffffffffu, got); }
+
 // sum += {lo, hi} * s
 __device__ __forceinline__ void add_scaled(Pair &sum, uint32_t lo, uint32_t hi, Pair s) {
     asm("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}" : "+l"(sum.v) : "r"(lo), "r"(hi), "l"(s.v));
@@ -233,36 +237,34 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             // instead of the 513 that the tensor cores need for them.)
             const bool issues = elect_one();
             Ring rg;
-            uint32_t n = 0;
+            uint32_t n = 0, issued = 0;
             bool ok = true;
             for (int t = first; t < units && ok; t += step) {
                 run_of(t);
-                for (int kb = k_lo; kb < k_hi; ++kb, ++n) {
+                for (int kb = k_lo; kb < k_hi && ok; ++kb, ++n) {
                     const uint32_t slot = n & 1;
-                    if (!wait_polling(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status) ||
-                        !wait_polling(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait_polling(ptx::smem_addr(&ctl->acc_empty[slot]), ((n >> 1) & 1) ^ 1u, abort_flag, a.wait_limit_ns, a.status) &&
+                         wait_polling(ptx::smem_addr(&ctl->full[rg.idx]), rg.phase, abort_flag, a.wait_limit_ns, a.status);
                     ptx::tc_fence_after();
                     const uint32_t at = ring + rg.idx * a.stage_bytes, d = tmem + slot * kMaxTileB;
                     const uint64_t da = ptx::smem_desc_sw128(at), db = ptx::smem_desc_sw128(at + 16384);
-                    if (issues) {
+                    if (issues && ok) {
+                        issued = n + 1;
 #pragma unroll
                         for (int i = 0; i < kBlockK / 32; ++i) mma8(d, da + i * 2, db + i * 2, a.idesc, i > 0 ? 1u : 0u);
                         ptx::mma_commit(ptx::smem_addr(&ctl->acc_full[slot]));
                         ptx::mma_commit(ptx::smem_addr(&ctl->empty[rg.idx]));
                     }
-                    __syncwarp();
+                    ok = all_lanes(ok);  // (behind the MMAs: a vote before them took 2 % of the time)
                     rg.next(a.stages);
                 }
             }
             // After a time-out the MMAs under way have to end before their
             // shared and tensor memory goes: the last one's commit covers all.
             // (Else the summing warps have waited for every accumulator.)
-            if (*abort_flag && n > 0) {
+            if (*abort_flag && issued > 0) {
                 const uint64_t t0 = ptx::global_timer_ns();
-                while (!ptx::mbar_test_wait(ptx::smem_addr(&ctl->acc_full[(n - 1) & 1]), ((n - 1) >> 1) & 1))
+                while (!ptx::mbar_test_wait(ptx::smem_addr(&ctl->acc_full[(issued - 1) & 1]), ((issued - 1) >> 1) & 1))
                     if (ptx::global_timer_ns() - t0 > 10000000) break;
             }
         } else if (warp == 2) {
@@ -329,20 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
             for (int k0 = k_lo; k0 < k_hi && ok; k0 += kBatch) {
                 // a batch's scales: of the row, and with it the columns' where they have one
                 const uint32_t at = scales + sr.idx * kBatch * kScaleBytes;
-                if (!wait_polling(ptx::smem_addr(&ctl->scale_full[sr.idx]), sr.phase, abort_flag, a.wait_limit_ns, a.status)) {
-                    ok = false;
-                    break;
-                }
+                // (a lane that has given up goes through the batch with the others,
+                // without waiting)
+                ok = wait_polling(ptx::smem_addr(&ctl->scale_full[sr.idx]), sr.phase, abort_flag, a.wait_limit_ns, a.status);
                 const int k1 = min(k_hi, k0 + kBatch);
 #pragma unroll 1
                 for (int kb = k0; kb < k1; ++kb, ++n) {
                     const uint32_t slot = n & 1, mine = at + (kb - k0) * kScaleBytes;
                     float s = __uint_as_float(ptx::ld_shared_b32(mine + (quad * 32 + lane) * 4));
                     if constexpr (!kPerColumn) s *= __uint_as_float(ptx::ld_shared_b32(mine + (kTileA + part) * 4));
-                    if (!wait_polling(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = ok && wait_polling(ptx::smem_addr(&ctl->acc_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns, a.status);
                     ptx::tc_fence_after();
                     const uint32_t acc = tmem + slot * kMaxTileB + part * kCols + ((uint32_t)(quad * 32) << 16);
                     const Pair s2 = pair(s);
@@ -378,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) scaled_product_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive_relaxed(ptx::smem_addr(&ctl->scale_empty[sr.idx]));  // (read, and nothing written)
                 sr.next(kScaleSlots);
+                ok = all_lanes(ok);
             }
             if (!ok) break;
             wt.row0 = ia * kTileA + quad * 32;
